@@ -2,14 +2,18 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <new>
 
+#include "kv_fp8.h"
 #include "kv_internal.h"
 
 using kvint2::Pool;
 
 struct kv_pool {
   Pool p;
+  kvint2::Fp8Store fp8;
+  kvint2::RopeParams* rope = nullptr;   // host, one per layer
 };
 
 namespace {
@@ -33,11 +37,15 @@ bool dev_alloc(T** ptr, size_t bytes) {
   return true;
 }
 
-void free_pool(Pool& p) {
+void free_pool(kv_pool* pool) {
+  Pool& p = pool->p;
   void* ptrs[] = {p.hist, p.sink_k, p.sink_v, p.rec_k,   p.rec_v,        p.bk,  p.bv,  p.Rk,
-                  p.RvT,  p.clip,   p.rfrag,  p.tickets, p.step_tickets, p.arrive, p.err};
+                  p.RvT,  p.clip,   p.rfrag,  p.tickets, p.step_tickets, p.arrive, p.err,
+                  pool->fp8.codes, pool->fp8.exps};
   for (void* q : ptrs)
     if (q) cudaFree(q);
+  delete[] pool->rope;
+  delete pool;
 }
 
 __global__ void init_rotation_kernel(float* Rk, float* RvT, float* clip, size_t n_mat, size_t n_clip) {
@@ -55,6 +63,20 @@ bool valid_layer(const kv_pool_t* pool, int layer) {
   return pool && layer >= 0 && layer < pool->p.cfg.num_layers;
 }
 
+// KV_OK when the pool's device is the current one
+kv_status_t on_pool_device(const Pool& p) {
+  int cur = -1;
+  if (cudaGetDevice(&cur) != cudaSuccess) return KV_ERR_CUDA;
+  return cur == p.device ? KV_OK : KV_ERR_INVALID_ARG;
+}
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+// a [tokens][heads][128] bf16 operand: 16-byte rows, tokens `stride` elements apart
+bool valid_rows(const void* p, int64_t stride, int heads) {
+  return aligned16(p) && stride >= (int64_t)heads * 128 && (stride & 7) == 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -63,7 +85,7 @@ kv_status_t kv_pool_create(const kv_pool_config_t* cfg, void* stream, kv_pool_t*
   if (!cfg || !out) return KV_ERR_INVALID_ARG;
   *out = nullptr;
   const kv_pool_config_t c = *cfg;
-  if (c.kind != KV_POOL_INT2_3TIER && c.kind != KV_POOL_BF16) return KV_ERR_INVALID_ARG;
+  if (c.kind != KV_POOL_INT2_3TIER && c.kind != KV_POOL_BF16 && c.kind != KV_POOL_FP8) return KV_ERR_INVALID_ARG;
   if (c.num_layers <= 0 || c.num_kv_heads <= 0 || c.num_q_heads <= 0 || c.max_seqs <= 0 ||
       c.num_pages <= 0 || c.num_pages > (int64_t)INT32_MAX)
     return KV_ERR_INVALID_ARG;
@@ -89,7 +111,8 @@ kv_status_t kv_pool_create(const kv_pool_config_t* cfg, void* stream, kv_pool_t*
   if (p.sm_count <= 0) p.sm_count = 1;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const size_t L = c.num_layers, H = c.num_kv_heads;
-  bool ok = true;
+  pool->rope = new (std::nothrow) kvint2::RopeParams[L]();
+  bool ok = pool->rope != nullptr;
   if (c.kind == KV_POOL_INT2_3TIER) {
     p.tile_bytes = 1024 + kvint2::kTile * 8 * (128 / c.group_size);
     p.page_bytes = H * (c.page_size / kvint2::kTile) * p.tile_bytes;
@@ -105,6 +128,12 @@ kv_status_t kv_pool_create(const kv_pool_config_t* cfg, void* stream, kv_pool_t*
     ok = ok && dev_alloc(&p.RvT, L * H * 128 * 128 * sizeof(float));
     ok = ok && dev_alloc(&p.clip, L * 2 * H * 128 * sizeof(float));
     ok = ok && dev_alloc(&p.rfrag, L * H * kvint2::kFragBlocks * kvint2::rfrag_per_head() * sizeof(uint4));
+  } else if (c.kind == KV_POOL_FP8) {
+    const size_t tiles = (size_t)c.num_pages * H * (c.page_size / kvint2::kTile);
+    pool->fp8.layer_stride = tiles * kvint2::kFp8TileBytes;
+    pool->fp8.exp_layer_stride = tiles * 2;
+    ok = ok && dev_alloc(&pool->fp8.codes, L * pool->fp8.layer_stride);
+    ok = ok && dev_alloc(&pool->fp8.exps, L * pool->fp8.exp_layer_stride);
   } else {
     p.bf16_layer_stride = (size_t)c.num_pages * H * c.page_size * 128;
     ok = ok && dev_alloc(&p.bk, L * p.bf16_layer_stride * 2);
@@ -115,8 +144,7 @@ kv_status_t kv_pool_create(const kv_pool_config_t* cfg, void* stream, kv_pool_t*
   ok = ok && dev_alloc(&p.step_tickets, L * ((c.max_seqs + 127) / 128) * sizeof(unsigned));
   ok = ok && dev_alloc(&p.err, sizeof(int));
   if (!ok) {
-    free_pool(p);
-    delete pool;
+    free_pool(pool);
     return KV_ERR_OOM;
   }
   cudaError_t e = cudaSuccess;
@@ -130,6 +158,8 @@ kv_status_t kv_pool_create(const kv_pool_config_t* cfg, void* stream, kv_pool_t*
   zero(p.rec_v, L * p.rec_layer_stride * 2);
   zero(p.bk, L * p.bf16_layer_stride * 2);
   zero(p.bv, L * p.bf16_layer_stride * 2);
+  zero(pool->fp8.codes, L * pool->fp8.layer_stride);
+  zero(pool->fp8.exps, L * pool->fp8.exp_layer_stride);
   zero(p.tickets, L * c.max_seqs * H * sizeof(unsigned));
   zero(p.arrive, L * c.max_seqs * H * kvint2::kMaskWords * sizeof(unsigned));
   zero(p.step_tickets, L * ((c.max_seqs + 127) / 128) * sizeof(unsigned));
@@ -145,8 +175,7 @@ kv_status_t kv_pool_create(const kv_pool_config_t* cfg, void* stream, kv_pool_t*
   }
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) {
-    free_pool(p);
-    delete pool;
+    free_pool(pool);
     return KV_ERR_CUDA;
   }
   *out = pool;
@@ -156,8 +185,7 @@ kv_status_t kv_pool_create(const kv_pool_config_t* cfg, void* stream, kv_pool_t*
 kv_status_t kv_pool_destroy(kv_pool_t* pool) {
   if (!pool) return KV_ERR_INVALID_ARG;
   cudaError_t e = cudaDeviceSynchronize();
-  free_pool(pool->p);
-  delete pool;
+  free_pool(pool);
   return cuda_status(e);
 }
 
@@ -196,7 +224,7 @@ kv_status_t kv_pool_get_layout(const kv_pool_t* pool, int32_t layer, kv_pool_lay
     out->recent_v = p.rec_v + (size_t)layer * p.rec_layer_stride;
     out->tier_layer_stride = p.sink_layer_stride * 2;
     out->recent_layer_stride = p.rec_layer_stride * 2;
-  } else {
+  } else if (p.cfg.kind == KV_POOL_BF16) {
     out->bf16_k = p.bk + (size_t)layer * p.bf16_layer_stride;
     out->bf16_v = p.bv + (size_t)layer * p.bf16_layer_stride;
     out->bf16_layer_stride = p.bf16_layer_stride * 2;
@@ -270,6 +298,7 @@ kv_status_t kv_append_step(kv_pool_t* pool, int32_t layer, int32_t B, const void
 size_t kv_decode_workspace_bytes(const kv_pool_t* pool, int32_t B, int32_t max_len) {
   if (!pool || B <= 0 || max_len < 0 || max_len > kvint2::kMaxDecodeLen || B > pool->p.cfg.max_seqs) return 0;
   const Pool& p = pool->p;
+  if (p.cfg.kind == KV_POOL_FP8) return kvint2::decode_fp8_workspace(p, B, max_len);
   kvint2::DecodePlan pl = p.cfg.kind == KV_POOL_INT2_3TIER ? kvint2::plan_decode_int2(p, B, max_len)
                                                            : kvint2::plan_decode_bf16(p, B, max_len);
   return pl.bytes;
@@ -405,6 +434,121 @@ kv_status_t kv_decode_attention_bf16(kv_pool_t* pool, int32_t layer, int32_t B, 
   return cuda_status(kvint2::launch_decode_bf16(p, layer, B, q, seq_len, page_table,
                                                 max_pages_per_seq, pl, softmax_scale, out,
                                                 workspace, static_cast<cudaStream_t>(stream)));
+}
+
+kv_status_t kv_pool_get_fp8_layout(const kv_pool_t* pool, int32_t layer, kv_fp8_layout_t* out) {
+  if (!valid_layer(pool, layer) || !out || pool->p.cfg.kind != KV_POOL_FP8) return KV_ERR_INVALID_ARG;
+  const Pool& p = pool->p;
+  const size_t per_page = p.cfg.page_size / kvint2::kTile;
+  out->codes = pool->fp8.codes + (size_t)layer * pool->fp8.layer_stride;
+  out->exps = pool->fp8.exps + (size_t)layer * pool->fp8.exp_layer_stride;
+  out->tile_bytes = kvint2::kFp8TileBytes;
+  out->codes_layer_stride = pool->fp8.layer_stride;
+  out->codes_head_stride = per_page * kvint2::kFp8TileBytes;
+  out->codes_page_stride = out->codes_head_stride * p.cfg.num_kv_heads;
+  out->exps_layer_stride = pool->fp8.exp_layer_stride;
+  out->exps_head_stride = per_page * 2;
+  out->exps_page_stride = out->exps_head_stride * p.cfg.num_kv_heads;
+  return KV_OK;
+}
+
+kv_status_t kv_pool_set_rope(kv_pool_t* pool, int32_t layer, const kv_rope_config_t* cfg) {
+  if (!valid_layer(pool, layer) || !cfg) return KV_ERR_INVALID_ARG;
+  kvint2::RopeParams r;
+  const kv_status_t st = kvint2::rope_params(*cfg, &r);
+  if (st == KV_OK) pool->rope[layer] = r;
+  return st;
+}
+
+kv_status_t kv_rope_apply(const kv_pool_t* pool, int32_t layer, int32_t n_tokens, const int32_t* positions,
+                          const void* q, int64_t q_stride, const void* k, int64_t k_stride, void* q_out,
+                          int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream) {
+  if (!valid_layer(pool, layer) || n_tokens < 0) return KV_ERR_INVALID_ARG;
+  const Pool& p = pool->p;
+  if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr)) return KV_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (!positions || (!q && !k))) return KV_ERR_INVALID_ARG;
+  const int Hq = p.cfg.num_q_heads, Hkv = p.cfg.num_kv_heads;
+  if (q && (!valid_rows(q, q_stride, Hq) || !valid_rows(q_out, q_out_stride, Hq))) return KV_ERR_INVALID_ARG;
+  if (k && (!valid_rows(k, k_stride, Hkv) || !valid_rows(k_out, k_out_stride, Hkv))) return KV_ERR_INVALID_ARG;
+  if ((q && q == q_out && q_stride != q_out_stride) || (k && k == k_out && k_stride != k_out_stride))
+    return KV_ERR_INVALID_ARG;
+  if (kv_status_t st = on_pool_device(p); st != KV_OK) return st;
+  return cuda_status(kvint2::launch_rope(p, pool->rope[layer], n_tokens, positions,
+                                         {q, q_stride, q_out, q_out_stride}, {k, k_stride, k_out, k_out_stride},
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+kv_status_t kv_append_fp8(kv_pool_t* pool, int32_t layer, int32_t n_seqs, const void* q, int64_t q_stride,
+                          const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                          const int32_t* cu_tokens, const int32_t* start_pos, const int32_t* page_table,
+                          int32_t max_pages_per_seq, int32_t max_tokens_per_seq, void* q_out, void* stream) {
+  if (!valid_layer(pool, layer) || n_seqs < 0 || max_pages_per_seq <= 0 || max_tokens_per_seq < 0)
+    return KV_ERR_INVALID_ARG;
+  const Pool& p = pool->p;
+  if (p.cfg.kind != KV_POOL_FP8) return KV_ERR_INVALID_ARG;
+  if (n_seqs > 0 && (!k || !v || !cu_tokens || !start_pos || !page_table)) return KV_ERR_INVALID_ARG;
+  if ((q == nullptr) != (q_out == nullptr)) return KV_ERR_INVALID_ARG;
+  const int Hq = p.cfg.num_q_heads, Hkv = p.cfg.num_kv_heads;
+  if (n_seqs > 0 && (!valid_rows(k, k_stride, Hkv) || !valid_rows(v, v_stride, Hkv))) return KV_ERR_INVALID_ARG;
+  if (q && (!valid_rows(q, q_stride, Hq) || !aligned16(q_out))) return KV_ERR_INVALID_ARG;
+  if (q && q == q_out && q_stride != (int64_t)Hq * 128) return KV_ERR_INVALID_ARG;
+  if ((int64_t)n_seqs * (((int64_t)max_tokens_per_seq + 30) / kvint2::kTile) > INT32_MAX) return KV_ERR_INVALID_ARG;
+  if (kv_status_t st = on_pool_device(p); st != KV_OK) return st;
+  return cuda_status(kvint2::launch_append_fp8(p, pool->fp8, pool->rope[layer], layer, n_seqs,
+                                               {q, q_stride, q_out, (int64_t)Hq * 128}, k, k_stride, v, v_stride,
+                                               cu_tokens, start_pos, page_table, max_pages_per_seq,
+                                               max_tokens_per_seq, static_cast<cudaStream_t>(stream)));
+}
+
+kv_status_t kv_decode_attention_fp8(kv_pool_t* pool, int32_t layer, int32_t B, const void* q,
+                                    const int32_t* seq_len, const int32_t* page_table, int32_t max_pages_per_seq,
+                                    int32_t max_seq_len, float softmax_scale, int32_t window, int32_t n_sink,
+                                    void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!valid_layer(pool, layer) || B <= 0 || max_pages_per_seq <= 0 || max_seq_len < 0) return KV_ERR_INVALID_ARG;
+  const Pool& p = pool->p;
+  if (p.cfg.kind != KV_POOL_FP8 || B > p.cfg.max_seqs) return KV_ERR_INVALID_ARG;
+  if (!q || !seq_len || !page_table || !out || !workspace) return KV_ERR_INVALID_ARG;
+  if (window < 0 || n_sink < 0 || !std::isfinite(softmax_scale)) return KV_ERR_INVALID_ARG;
+  if ((int64_t)max_seq_len > (int64_t)max_pages_per_seq * p.cfg.page_size || max_seq_len > kvint2::kMaxDecodeLen)
+    return KV_ERR_INVALID_ARG;
+  if (!aligned16(workspace) || !aligned16(q) || !aligned16(out) || ((uintptr_t)lse & 3)) return KV_ERR_INVALID_ARG;
+  if (workspace_bytes < kvint2::decode_fp8_workspace(p, B, max_seq_len)) return KV_ERR_INVALID_ARG;
+  if (kv_status_t st = on_pool_device(p); st != KV_OK) return st;
+  return cuda_status(kvint2::launch_decode_fp8(p, pool->fp8, layer, B,
+                                               {q, seq_len, page_table, max_pages_per_seq, max_seq_len, softmax_scale,
+                                                window, n_sink, out, lse, workspace},
+                                               static_cast<cudaStream_t>(stream)));
+}
+
+size_t kv_prefill_workspace_bytes(const kv_pool_t* pool, int32_t n_seqs, int32_t max_q_per_seq,
+                                  int32_t max_seq_len) {
+  if (!pool || pool->p.cfg.kind != KV_POOL_FP8 || n_seqs <= 0 || n_seqs > pool->p.cfg.max_seqs ||
+      max_q_per_seq < 0 || max_seq_len < 0 || max_seq_len > kvint2::kMaxDecodeLen)
+    return 0;
+  return kvint2::prefill_fp8_workspace(pool->p, n_seqs, max_q_per_seq, max_seq_len);
+}
+
+kv_status_t kv_prefill_attention_fp8(kv_pool_t* pool, int32_t layer, int32_t n_seqs, const void* q,
+                                     const int32_t* cu_q, const int32_t* seq_len, const int32_t* page_table,
+                                     int32_t max_pages_per_seq, int32_t max_q_per_seq, int32_t max_seq_len,
+                                     float softmax_scale, int32_t window, int32_t n_sink, void* out, float* lse,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  if (!valid_layer(pool, layer) || n_seqs <= 0 || max_pages_per_seq <= 0 || max_q_per_seq < 0 || max_seq_len < 0)
+    return KV_ERR_INVALID_ARG;
+  const Pool& p = pool->p;
+  if (p.cfg.kind != KV_POOL_FP8 || n_seqs > p.cfg.max_seqs) return KV_ERR_INVALID_ARG;
+  if (!q || !cu_q || !seq_len || !page_table || !out || !workspace) return KV_ERR_INVALID_ARG;
+  if (window < 0 || n_sink < 0 || !std::isfinite(softmax_scale)) return KV_ERR_INVALID_ARG;
+  if ((int64_t)max_seq_len > (int64_t)max_pages_per_seq * p.cfg.page_size || max_seq_len > kvint2::kMaxDecodeLen)
+    return KV_ERR_INVALID_ARG;
+  if (!aligned16(workspace) || !aligned16(q) || !aligned16(out) || ((uintptr_t)lse & 3)) return KV_ERR_INVALID_ARG;
+  const size_t need = kvint2::prefill_fp8_workspace(p, n_seqs, max_q_per_seq, max_seq_len);
+  if (need == 0 || workspace_bytes < need) return KV_ERR_INVALID_ARG;
+  if (kv_status_t st = on_pool_device(p); st != KV_OK) return st;
+  return cuda_status(kvint2::launch_prefill_fp8(p, pool->fp8, layer, n_seqs, cu_q, max_q_per_seq,
+                                                {q, seq_len, page_table, max_pages_per_seq, max_seq_len,
+                                                 softmax_scale, window, n_sink, out, lse, workspace},
+                                                static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

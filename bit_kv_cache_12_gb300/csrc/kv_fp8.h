@@ -1,0 +1,75 @@
+// Internal declarations of the 8-bit cache: its storage beside the pool, the
+// rotary parameters of a layer, and the launchers.
+#pragma once
+
+#include "kv_internal.h"
+
+namespace kvint2 {
+
+constexpr int kFp8TileBytes = 4096;   // e4m3 codes of one 16-token tile: K 2048 B, V 2048 B
+
+// Storage of an FP8 pool: codes [layer][page][head][tile][K, V][2048], exponents
+// [layer][page][head][tile][K, V].
+struct Fp8Store {
+  uint8_t* codes = nullptr;
+  int8_t* exps = nullptr;
+  size_t layer_stride = 0, exp_layer_stride = 0;   // bytes
+};
+
+// Rotary positions of a layer as the kernels take them (a kernel parameter).
+struct RopeParams {
+  unsigned long long turn[64];   // turns per position, modulo 1, in units of 2^-64
+  float att = 1.f;               // factor on cos and sin
+  float att2 = 1.f;              // its square
+  int rd = 0;                    // rotated channels: 0, 32, 64, 96 or 128
+  int interleaved = 0;
+};
+
+// One layer of an FP8 pool, as the attention kernels take it.
+struct Fp8Layer {
+  const uint8_t* codes;
+  const int8_t* exps;
+  long long num_pages;
+  int Hkv, P;
+};
+inline Fp8Layer fp8_layer(const Pool& p, const Fp8Store& f, int layer) {
+  return {f.codes + (size_t)layer * f.layer_stride, f.exps + (size_t)layer * f.exp_layer_stride, p.cfg.num_pages,
+          p.cfg.num_kv_heads, p.cfg.page_size};
+}
+
+// The layer's parameters from a configuration, or the reason it is refused.
+kv_status_t rope_params(const kv_rope_config_t& c, RopeParams* out);
+
+struct RopeRows {            // a [tokens][heads][128] bf16 operand and where its rotated rows go
+  const void* in;
+  int64_t in_stride;
+  void* out;
+  int64_t out_stride;
+};
+cudaError_t launch_rope(const Pool& p, const RopeParams& r, int n_tokens, const int32_t* positions, const RopeRows& q,
+                        const RopeRows& k, cudaStream_t s);
+cudaError_t launch_append_fp8(const Pool& p, const Fp8Store& f, const RopeParams& r, int layer, int n_seqs,
+                              const RopeRows& q, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                              const int32_t* cu, const int32_t* start, const int32_t* pt, int max_pages,
+                              int max_tokens, cudaStream_t s);
+
+// The arguments the two attention calls share.
+struct AttnCall {
+  const void* q;             // bf16 rows [rows][Hq][128]
+  const int32_t* seq_len;
+  const int32_t* pt;
+  int max_pages, max_len;
+  float scale;
+  int window, n_sink;
+  void* out;                 // bf16 rows
+  float* lse;                // or NULL
+  void* ws;
+};
+
+size_t decode_fp8_workspace(const Pool& p, int B, int max_len);
+cudaError_t launch_decode_fp8(const Pool& p, const Fp8Store& f, int layer, int B, const AttnCall& c, cudaStream_t s);
+size_t prefill_fp8_workspace(const Pool& p, int n_seqs, int max_q, int max_len);
+cudaError_t launch_prefill_fp8(const Pool& p, const Fp8Store& f, int layer, int n_seqs, const int32_t* cu_q,
+                               int max_q, const AttnCall& c, cudaStream_t s);
+
+}  // namespace kvint2

@@ -29,6 +29,9 @@ STATUS_NAMES = {0: "KV_OK", 1: "KV_ERR_INVALID_ARG", 2: "KV_ERR_OOM", 3: "KV_ERR
 KV_NOALLOC_SCRATCH_BYTES = 16 << 20
 KV_POOL_INT2_3TIER = 0
 KV_POOL_BF16 = 1
+KV_POOL_FP8 = 2
+KV_ROPE_STYLES = {"half": 0, "interleaved": 1}
+KV_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
 class KvPoolConfig(ctypes.Structure):
@@ -48,6 +51,22 @@ class KvPoolLayout(ctypes.Structure):
                 ("recent_v", ctypes.c_void_p), ("tier_layer_stride", ctypes.c_size_t),
                 ("recent_layer_stride", ctypes.c_size_t), ("bf16_k", ctypes.c_void_p),
                 ("bf16_v", ctypes.c_void_p), ("bf16_layer_stride", ctypes.c_size_t)]
+
+
+class KvFp8Layout(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("exps", ctypes.c_void_p),
+                ("codes_layer_stride", ctypes.c_size_t), ("codes_page_stride", ctypes.c_size_t),
+                ("codes_head_stride", ctypes.c_size_t), ("tile_bytes", ctypes.c_size_t),
+                ("exps_layer_stride", ctypes.c_size_t), ("exps_page_stride", ctypes.c_size_t),
+                ("exps_head_stride", ctypes.c_size_t)]
+
+
+class KvRopeConfig(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("style", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("original_max_position", ctypes.c_int32),
+                ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("attention_factor", ctypes.c_double), ("inv_freq", ctypes.POINTER(ctypes.c_double))]
 
 
 _P = ctypes.c_void_p
@@ -75,6 +94,15 @@ _SIG = {
     "kv_append_bf16": (_I32, [_P, _I32, _I32, _P, _P, _P, _P, _P, _I32, _I32, _P]),
     "kv_decode_attention_bf16": (_I32, [_P, _I32, _I32, _P, _P, _P, _I32, _I32,
                                         ctypes.c_float, _P, _P, ctypes.c_size_t, _P]),
+    "kv_pool_get_fp8_layout": (_I32, [_P, _I32, ctypes.POINTER(KvFp8Layout)]),
+    "kv_pool_set_rope": (_I32, [_P, _I32, ctypes.POINTER(KvRopeConfig)]),
+    "kv_rope_apply": (_I32, [_P, _I32, _I32, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P]),
+    "kv_append_fp8": (_I32, [_P, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I32, _I32, _P, _P]),
+    "kv_decode_attention_fp8": (_I32, [_P, _I32, _I32, _P, _P, _P, _I32, _I32, ctypes.c_float, _I32, _I32,
+                                       _P, _P, _P, ctypes.c_size_t, _P]),
+    "kv_prefill_workspace_bytes": (ctypes.c_size_t, [_P, _I32, _I32, _I32]),
+    "kv_prefill_attention_fp8": (_I32, [_P, _I32, _I32, _P, _P, _P, _P, _I32, _I32, _I32, ctypes.c_float,
+                                        _I32, _I32, _P, _P, _P, ctypes.c_size_t, _P]),
 }
 
 _lib = None
@@ -239,22 +267,86 @@ def kv_decode_attention_bf16(pool, layer, B, q, seq_len, page_table, max_pages_p
         _stream(stream)))
 
 
+def kv_pool_get_fp8_layout(pool, layer):
+    out = KvFp8Layout()
+    _check("kv_pool_get_fp8_layout", lib().kv_pool_get_fp8_layout(pool, layer, ctypes.byref(out)))
+    return out
+
+
+def rope_config(rotary_dim=128, style="half", theta=10000.0, scaling="none", factor=1.0,
+                original_max_position=0, beta_fast=0.0, beta_slow=0.0, attention_factor=0.0,
+                inv_freq=None):
+    """A kv_rope_config_t; inv_freq: a sequence of rotary_dim / 2 speeds or None."""
+    c = KvRopeConfig(rotary_dim, KV_ROPE_STYLES[style], KV_ROPE_SCALINGS[scaling],
+                     original_max_position, theta, factor, beta_fast, beta_slow, attention_factor)
+    if inv_freq is not None:
+        if len(inv_freq) != rotary_dim // 2:
+            raise ValueError("inv_freq holds rotary_dim / 2 speeds")
+        c.inv_freq = (ctypes.c_double * len(inv_freq))(*[float(w) for w in inv_freq])
+    return c
+
+
+def kv_pool_set_rope(pool, layer, cfg):
+    _check("kv_pool_set_rope", lib().kv_pool_set_rope(pool, layer, ctypes.byref(cfg)))
+
+
+def kv_rope_apply(pool, layer, n_tokens, positions, q, q_stride, k, k_stride, q_out, q_out_stride,
+                  k_out, k_out_stride, stream=None):
+    _check("kv_rope_apply", lib().kv_rope_apply(
+        pool, layer, n_tokens, _ptr(positions), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(q_out),
+        q_out_stride, _ptr(k_out), k_out_stride, _stream(stream)))
+
+
+def kv_append_fp8(pool, layer, n_seqs, q, q_stride, k, k_stride, v, v_stride, cu_tokens, start_pos,
+                  page_table, max_pages_per_seq, max_tokens_per_seq, q_out, stream=None):
+    _check("kv_append_fp8", lib().kv_append_fp8(
+        pool, layer, n_seqs, _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride,
+        _ptr(cu_tokens), _ptr(start_pos), _ptr(page_table), max_pages_per_seq, max_tokens_per_seq,
+        _ptr(q_out), _stream(stream)))
+
+
+def kv_decode_attention_fp8(pool, layer, B, q, seq_len, page_table, max_pages_per_seq, max_seq_len,
+                            softmax_scale, window, n_sink, out, lse, workspace, workspace_bytes,
+                            stream=None):
+    _check("kv_decode_attention_fp8", lib().kv_decode_attention_fp8(
+        pool, layer, B, _ptr(q), _ptr(seq_len), _ptr(page_table), max_pages_per_seq, max_seq_len,
+        float(softmax_scale), window, n_sink, _ptr(out), _ptr(lse), _ptr(workspace),
+        workspace_bytes, _stream(stream)))
+
+
+def kv_prefill_workspace_bytes(pool, n_seqs, max_q_per_seq, max_seq_len):
+    return lib().kv_prefill_workspace_bytes(pool, n_seqs, max_q_per_seq, max_seq_len)
+
+
+def kv_prefill_attention_fp8(pool, layer, n_seqs, q, cu_q, seq_len, page_table, max_pages_per_seq,
+                             max_q_per_seq, max_seq_len, softmax_scale, window, n_sink, out, lse,
+                             workspace, workspace_bytes, stream=None):
+    _check("kv_prefill_attention_fp8", lib().kv_prefill_attention_fp8(
+        pool, layer, n_seqs, _ptr(q), _ptr(cu_q), _ptr(seq_len), _ptr(page_table),
+        max_pages_per_seq, max_q_per_seq, max_seq_len, float(softmax_scale), window, n_sink,
+        _ptr(out), _ptr(lse), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
 # ---- device-memory views (zero copy) ---------------------------------------
 
 class _CudaArray:
-    def __init__(self, ptr, shape, typestr):
+    def __init__(self, ptr, shape, typestr, owner=None):
+        self.owner = owner     # a tensor made from this keeps it, and so the memory it views
         self.__cuda_array_interface__ = {"shape": tuple(int(s) for s in shape),
                                          "typestr": typestr, "data": (int(ptr), False),
                                          "version": 3, "strides": None}
 
 
-def device_view(ptr, shape, dtype):
-    """A torch tensor aliasing pool memory (uint8 or bf16 via int16)."""
+def device_view(ptr, shape, dtype, owner=None):
+    """A torch tensor aliasing pool memory (uint8, int8 or bf16 via int16); it keeps `owner` (the
+    KVPool whose memory it is) alive."""
     import torch
+    if dtype == torch.int8:
+        return torch.as_tensor(_CudaArray(ptr, shape, "|i1", owner), device="cuda")
     if dtype == torch.uint8:
-        return torch.as_tensor(_CudaArray(ptr, shape, "|u1"), device="cuda")
+        return torch.as_tensor(_CudaArray(ptr, shape, "|u1", owner), device="cuda")
     if dtype == torch.bfloat16:
-        return torch.as_tensor(_CudaArray(ptr, shape, "<i2"), device="cuda").view(torch.bfloat16)
+        return torch.as_tensor(_CudaArray(ptr, shape, "<i2", owner), device="cuda").view(torch.bfloat16)
     raise ValueError(dtype)
 
 
@@ -286,7 +378,8 @@ class KVPool:
         import torch
         lay = self.layout(layer)
         c = self.cfg
-        return device_view(lay.hist, (c.num_pages, c.num_kv_heads, lay.hist_head_stride), torch.uint8)
+        return device_view(lay.hist, (c.num_pages, c.num_kv_heads, lay.hist_head_stride), torch.uint8,
+                           self)
 
     def tier_views(self, layer=0):
         import torch
@@ -294,15 +387,25 @@ class KVPool:
         c = self.cfg
         s = (c.max_seqs, c.num_kv_heads, c.sink_tokens, 128)
         r = (c.max_seqs, c.num_kv_heads, c.recent_tokens, 128)
-        return (device_view(lay.sink_k, s, torch.bfloat16), device_view(lay.sink_v, s, torch.bfloat16),
-                device_view(lay.recent_k, r, torch.bfloat16), device_view(lay.recent_v, r, torch.bfloat16))
+        return (device_view(lay.sink_k, s, torch.bfloat16, self), device_view(lay.sink_v, s, torch.bfloat16, self),
+                device_view(lay.recent_k, r, torch.bfloat16, self), device_view(lay.recent_v, r, torch.bfloat16, self))
 
     def bf16_views(self, layer=0):
         import torch
         lay = self.layout(layer)
         c = self.cfg
         shp = (c.num_pages, c.num_kv_heads, c.page_size, 128)
-        return (device_view(lay.bf16_k, shp, torch.bfloat16), device_view(lay.bf16_v, shp, torch.bfloat16))
+        return (device_view(lay.bf16_k, shp, torch.bfloat16, self), device_view(lay.bf16_v, shp, torch.bfloat16, self))
+
+    def fp8_views(self, layer=0):
+        """FP8 pool: codes uint8 [num_pages, Hkv, page_size/16, 2, 2048] and exponents int8
+        [num_pages, Hkv, page_size/16, 2], K then V."""
+        import torch
+        lay = kv_pool_get_fp8_layout(self.handle, layer)
+        c = self.cfg
+        shp = (c.num_pages, c.num_kv_heads, c.page_size // 16, 2)
+        return (device_view(lay.codes, (*shp, 2048), torch.uint8, self),
+                device_view(lay.exps, shp, torch.int8, self))
 
     def error(self):
         return kv_pool_get_error(self.handle)

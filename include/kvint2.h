@@ -84,7 +84,7 @@ enum {
                                  after this code except to tear it down. */
 };
 
-typedef enum { KV_POOL_INT2_3TIER = 0, KV_POOL_BF16 = 1 } kv_pool_kind_t;
+typedef enum { KV_POOL_INT2_3TIER = 0, KV_POOL_BF16 = 1, KV_POOL_FP8 = 2 } kv_pool_kind_t;
 
 typedef struct {
   int32_t kind;           /* kv_pool_kind_t                                  */
@@ -117,7 +117,8 @@ typedef struct {
  *   sink_k / sink_v:   bf16 [max_seqs][Hkv][sink_tokens][128]
  *   recent_k/recent_v: bf16 [max_seqs][Hkv][recent_tokens][128] (ring)
  *   BF16 pool: bf16_k / bf16_v bf16 [num_pages][Hkv][page_size][128]
- * Pointers that do not apply to the pool kind are NULL. */
+ * Pointers that do not apply to the pool kind are NULL (an FP8 pool: all of
+ * them; see kv_pool_get_fp8_layout). */
 typedef struct {
   void* hist;
   size_t hist_layer_stride, hist_page_stride, hist_head_stride, tile_bytes;
@@ -268,8 +269,8 @@ kv_status_t kv_append_step(kv_pool_t* pool, int32_t layer, int32_t B, const void
                            const int32_t* page_table, int32_t max_pages_per_seq, void* stream);
 
 /* Bytes of device workspace kv_decode_attention / kv_decode_attention_bf16
- * need for a batch of B sequences whose history (INT2 pool) or total length
- * (BF16 pool) is at most max_len tokens.  0 on invalid arguments.  Every
+ * / kv_decode_attention_fp8 need for a batch of B sequences whose history (INT2
+ * pool) or total length (BF16 and FP8 pools) is at most max_len tokens.  0 on invalid arguments.  Every
  * decode call takes max_hist_len / max_seq_len <= KV_MAX_DECODE_LEN
  * (else KV_ERR_INVALID_ARG). */
 #define KV_MAX_DECODE_LEN 6553600
@@ -370,6 +371,175 @@ kv_status_t kv_decode_attention_noalloc(kv_pool_t* pool, int32_t layer, int32_t 
  * append calls; 0 restores it.  enable = 0 restores normal calls.  Not for
  * production use. */
 kv_status_t kv_debug_stall_first_copy(kv_pool_t* pool, int32_t enable, int32_t max_polls);
+
+/* ---------------------------------------------------------------------------
+ * The 8-bit cache (pool kind KV_POOL_FP8) and the operators around it: rotary
+ * positions, the append that applies them, single-token and prompt attention.
+ * Every call below requires the pool's device to be the current one
+ * (KV_ERR_INVALID_ARG otherwise) and reads the caller's buffers from device
+ * memory only.
+ *
+ * Format.  16 consecutive tokens of one sequence, KV head and tensor (K or V)
+ * are one tile: 128 e4m3 codes per token and one exponent e for the tile; the
+ * stored value is code * 2^e, -64 <= e <= 7 (so that every value also fits
+ * fp16's range from above: at most 448 * 128 = 57344).  A power of two loses
+ * nothing against a free scale, because a floating-point code's relative
+ * rounding does not depend on the scale, and moving a tile to a larger
+ * exponent is exact except for codes that become subnormal.
+ *   codes  uint8 [num_layers][num_pages][Hkv][page_size/16][K, V][2048]
+ *          K byte of (token t, channel c):
+ *            (t/8)*1024 + (c/64)*512 + (t%8)*64 + c%64
+ *          V byte: (t%2 + 2*(t/8))*512 + (c/16)*64 + ((t%8)/2)*16 + c%16
+ *   exps   int8 [num_layers][num_pages][Hkv][page_size/16][K, V]
+ * ------------------------------------------------------------------------- */
+
+#define KV_FP8_EXP_MIN (-64)
+#define KV_FP8_EXP_MAX 7
+
+typedef struct {
+  void* codes;
+  int8_t* exps;
+  size_t codes_layer_stride, codes_page_stride, codes_head_stride, tile_bytes;
+  size_t exps_layer_stride, exps_page_stride, exps_head_stride;
+} kv_fp8_layout_t;
+
+/* Where an FP8 pool keeps `layer` (device pointers, strides in bytes;
+ * tile_bytes = 4096: K then V codes of one tile). */
+kv_status_t kv_pool_get_fp8_layout(const kv_pool_t* pool, int32_t layer, kv_fp8_layout_t* out);
+
+/* Which channels form the rotated pairs of a head: (i, i + rotary_dim/2), or
+ * (2i, 2i + 1).  Channels from rotary_dim on are not rotated. */
+typedef enum { KV_ROPE_HALF = 0, KV_ROPE_INTERLEAVED = 1 } kv_rope_style_t;
+
+/* How the rotation speeds w_i = theta^(-2i/rotary_dim) (radians per position)
+ * are changed for contexts longer than the trained one:
+ *   NONE    not at all
+ *   LINEAR  w_i / factor
+ *   NTK     theta * factor^(rotary_dim/(rotary_dim-2)) in place of theta
+ *   YARN    by parts: pairs that turn more than beta_fast times over
+ *           original_max_position stay, pairs that turn less than beta_slow
+ *           times are divided by factor, a linear ramp over the pair index in
+ *           between; cos and sin are multiplied by 0.1 ln(factor) + 1 */
+typedef enum {
+  KV_ROPE_SCALE_NONE = 0,
+  KV_ROPE_SCALE_LINEAR = 1,
+  KV_ROPE_SCALE_NTK = 2,
+  KV_ROPE_SCALE_YARN = 3
+} kv_rope_scaling_t;
+
+typedef struct {
+  int32_t rotary_dim;             /* 0 (no rotation), 32, 64, 96 or 128           */
+  int32_t style;                  /* kv_rope_style_t                              */
+  int32_t scaling;                /* kv_rope_scaling_t                            */
+  int32_t original_max_position;  /* YARN: the trained context, > 0               */
+  double theta;                   /* > 1                                          */
+  double factor;                  /* >= 1; ignored for NONE                       */
+  double beta_fast, beta_slow;    /* YARN: 0 means 32 and 1                       */
+  double attention_factor;        /* on cos and sin; 0 means 1 (YARN: see above)  */
+  const double* inv_freq;         /* host [rotary_dim/2] or NULL: these speeds
+                                     replace theta, scaling and factor            */
+} kv_rope_config_t;
+
+/* Set the rotary positions of one layer (any pool kind; none until set).  A
+ * host call: it holds for the calls made after it, and a captured graph keeps
+ * what was set when it was captured.  Angles are formed as 64-bit fractions of
+ * a turn (position times speed, modulo one turn), so they are exact to 2^-32 of
+ * a turn at any int32 position. */
+kv_status_t kv_pool_set_rope(kv_pool_t* pool, int32_t layer, const kv_rope_config_t* cfg);
+
+/* Rotate q and k rows by `layer`'s rotary positions, for callers that append to
+ * an INT2 or BF16 pool (kv_append_fp8 does it on the way into an FP8 pool).
+ *   positions  device int32 [n_tokens]; the rows of a negative position are
+ *              neither read nor written
+ *   q, k       device bf16, token i at q + i*q_stride, its Hq (k: Hkv) heads of
+ *              128 channels contiguous; either may be NULL (with its output)
+ *   q_out, k_out  the same with their own strides; may be the input itself
+ *              (same pointer and stride), else must not overlap it
+ * Strides in elements.  Pointers 16-byte aligned, strides multiples of 8 and at
+ * least a token's channels, else KV_ERR_INVALID_ARG. */
+kv_status_t kv_rope_apply(const kv_pool_t* pool, int32_t layer, int32_t n_tokens,
+                          const int32_t* positions, const void* q, int64_t q_stride,
+                          const void* k, int64_t k_stride, void* q_out, int64_t q_out_stride,
+                          void* k_out, int64_t k_out_stride, void* stream);
+
+/* Append tokens to an FP8 pool, rotating q and k on the way: token i of
+ * sequence s goes to cache position p = start_pos[s] + i, in page
+ * page_table[s][p / page_size]; q and k are rotated by p.
+ *   q, k, v    device bf16 [T] rows with strides as in kv_rope_apply (for
+ *              instance the three parts of one fused projection); q may be NULL
+ *   q_out      device bf16 [T][Hq][128] contiguous: the rotated q; NULL with q;
+ *              may be q itself if q_stride is Hq * 128
+ *   cu_tokens  device int32 [n_seqs+1] prefix sums; rows from
+ *              cu_tokens[n_seqs] on are neither read nor written
+ *   start_pos  device int32 [n_seqs]: tokens the sequence already caches
+ *   max_tokens_per_seq  host bound (sizes the grid; longer sequences are
+ *              flagged KV_DEVERR_SEQ_RANGE and truncated)
+ * A tile's exponent is the smallest whose range holds the tile's values: of V
+ * their magnitudes, of K each rotated pair's length (times the attention
+ * factor), which rotation does not change.  Codes are rounded once, to nearest
+ * even, from fp32.  Where tokens join a tile that holds earlier ones, its
+ * exponent never falls, and if it rises the earlier codes are rounded to it; a
+ * tile whose first token is appended starts anew.  Values beyond 57344 saturate;
+ * a token whose k (or v) row of a head has a NaN or an infinity stores NaN in
+ * all of that row.  Slots after the last appended token keep their bytes.
+ * Sequences must not share a page that is written.  A sequence that would leave
+ * the page table's span is skipped (KV_DEVERR_SEQ_RANGE), its q_out rows too; a
+ * tile with a bad page id is not stored (KV_DEVERR_PAGE_ID), its q_out rows are
+ * written. */
+kv_status_t kv_append_fp8(kv_pool_t* pool, int32_t layer, int32_t n_seqs, const void* q,
+                          int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, const int32_t* cu_tokens, const int32_t* start_pos,
+                          const int32_t* page_table, int32_t max_pages_per_seq,
+                          int32_t max_tokens_per_seq, void* q_out, void* stream);
+
+/* One decode step over an FP8 pool: the query of sequence b, at position
+ * seq_len[b] - 1 (its own token is already in the cache), attends to the cached
+ * positions j < seq_len[b] with j >= seq_len[b] - window or j < n_sink.
+ *   q        device bf16 [B][Hq][128], rotated, 16-byte aligned
+ *   seq_len  device int32 [B]; 0 gives zeros and lse = -inf.  A length above
+ *            max_seq_len (a host bound, at most the page table's span) sets
+ *            KV_DEVERR_LENGTH and is taken as max_seq_len; one below 0 sets it
+ *            and is taken as 0
+ *   window   tokens visible up to the query's own; 0 means all of them
+ *   n_sink   first tokens that stay visible under a window (ignored without)
+ *   out      device bf16 [B][Hq][128], 16-byte aligned
+ *   lse      device fp32 [B][Hq] or NULL: ln sum_j exp(softmax_scale * q.k_j)
+ *   workspace  device, 16-byte aligned, >= kv_decode_workspace_bytes(pool, B,
+ *            max_seq_len)
+ * What hidden tokens hold never reaches the output, NaN included.  The tokens
+ * of a page with a bad id are hidden (KV_DEVERR_PAGE_ID). */
+kv_status_t kv_decode_attention_fp8(kv_pool_t* pool, int32_t layer, int32_t B, const void* q,
+                                    const int32_t* seq_len, const int32_t* page_table,
+                                    int32_t max_pages_per_seq, int32_t max_seq_len,
+                                    float softmax_scale, int32_t window, int32_t n_sink, void* out,
+                                    float* lse, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/* Prompt attention over an FP8 pool: n_s = cu_q[s+1] - cu_q[s] queries of
+ * sequence s, the last n_s of its seq_len[s] cached tokens.  Query i is at
+ * position p = seq_len[s] - n_s + i and attends to the cached positions j <= p
+ * with j > p - window or j < n_sink (window 0: all j <= p); a query at a
+ * negative position sees nothing and gets zeros and lse = -inf.
+ *   q        device bf16 [T][Hq][128], rotated, 16-byte aligned
+ *   cu_q     device int32 [n_seqs+1] prefix sums; rows from cu_q[n_seqs] on are
+ *            neither read nor written
+ *   seq_len  device int32 [n_seqs], treated as in kv_decode_attention_fp8
+ *   max_q_per_seq, max_seq_len  host bounds; a sequence with more queries (or a
+ *            negative count) sets KV_DEVERR_SEQ_RANGE and gets none of its rows
+ *            written
+ *   out, lse [T][Hq][128] bf16 and [T][Hq] fp32 (or NULL)
+ *   workspace  >= kv_prefill_workspace_bytes(pool, n_seqs, max_q_per_seq,
+ *            max_seq_len)
+ * Hidden tokens and bad pages as in kv_decode_attention_fp8. */
+size_t kv_prefill_workspace_bytes(const kv_pool_t* pool, int32_t n_seqs, int32_t max_q_per_seq,
+                                  int32_t max_seq_len);
+kv_status_t kv_prefill_attention_fp8(kv_pool_t* pool, int32_t layer, int32_t n_seqs, const void* q,
+                                     const int32_t* cu_q, const int32_t* seq_len,
+                                     const int32_t* page_table, int32_t max_pages_per_seq,
+                                     int32_t max_q_per_seq, int32_t max_seq_len,
+                                     float softmax_scale, int32_t window, int32_t n_sink, void* out,
+                                     float* lse, void* workspace, size_t workspace_bytes,
+                                     void* stream);
 
 #ifdef __cplusplus
 }

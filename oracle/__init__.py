@@ -13,6 +13,8 @@ It is a plain, slow restatement of the method, step by step, in numpy:
   (BF16 sink, INT2 history, BF16 recent) and over an all-BF16 paged cache.
 * ``oracle.tiers``     where a newly generated token goes: sink, recent ring,
   or (when the ring is full) eviction of the oldest recent token into history.
+* ``oracle.fp8cache``  the 8-bit cache: e4m3 codes with a power-of-two scale per
+  tile, rotary positions, the append, attention under a window with first tokens.
 
 Sources: "OSCAR: Offline Spectral Covariance-Aware Rotation for 2-bit KV Cache
 Quantization" (gist.science explainer), section 2.2 B "Online-Betriebsphase";
@@ -24,4 +26,4 @@ come from the oracle itself (closed forms, brute force, hand-worked fixtures
 under ``tests/golden/``).
 """
 
-from . import kvquant, attention, tiers  # noqa: F401
+from . import kvquant, attention, tiers, fp8cache  # noqa: F401
