@@ -1,39 +1,478 @@
-// Single-token attention over the 8-bit cache.
-#include "kv_fp8_simple.cuh"
+// Single-token attention over the 8-bit cache, split over the cache.
+//
+// With code values k, v (e4m3) of tile exponents eK, eV and base-2 logits
+//   x_j = scale log2(e) (q . k_j) 2^eK + eV,   w_j = 2^(x_j - M),
+// a head's output is  sum_j w_j v_j / sum_j w_j 2^-eV : the V scale rides on the
+// weight, so the products use the codes as they are, and the reference M follows
+// the largest weight times V scale.  -64 <= eV <= 7 keeps every sum in fp32.
+//
+// Both products are m16n8k16 tensor-core steps with the cached tile as the A
+// operand and the (up to 8) query heads of the KV head as the 8 columns: e4m3
+// converts to fp16 exactly (one instruction for two codes).  q enters as fp16
+// scaled per head by a power of two (its largest element in [2^14, 2^15)):
+// exact for all of bf16's 8 bits down to 2^-32 of the largest, 2^-39 of it
+// beyond, below the rounding of the fp32 sum.  The weights are rounded to fp16
+// (11 bits) relative to their own size; M lags so that they stay between 2^-31
+// of the largest and 2^15.
+//
+// Bound: HBM (256 B and 2 exponent bytes per token and KV head).  Each warp
+// streams whole 4 KB tiles through a ring of its own (bulk copies, no block
+// barrier in the loop); the stored order is the operand order, so every lane
+// reads its fragments as 16-byte pieces without bank conflicts.  The work of a
+// (sequence, KV head) is split over CTAs by the sequence's own count of visible
+// tiles; the last CTA to finish joins the parts in split order.
+#include <algorithm>
+
+#include "kv_device.cuh"
+#include "kv_fp8.h"
 
 namespace kvint2 {
 
 namespace {
 
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 3;                     // 4 KB tiles in flight per warp
+constexpr int kPolls = 1 << 22;                // bound of a copy's wait (about a second)
+constexpr int kMaxSplits = 64;
+constexpr int kPart = 132;                     // floats of a partial head: M, l, 2 unused, 128 sums
+constexpr float kNoRef = -3e38f;               // below every logit
+constexpr float kRaise = 15.f, kHead = 7.f;    // M moves when x > M + 15, to the largest x - 7
+constexpr uint32_t kRing = kWarps * kStages * kFp8TileBytes;
+constexpr uint32_t kSmem = kRing + kWarps * kStages * 8;
+// results of the warps in shared memory (over the ring): channel c of a head at
+// c + 4 (c / 16), heads 161 floats apart: few bank conflicts for either side
+constexpr int kHeadStride = 161;
+__device__ __forceinline__ int chan(int c) { return c + 4 * (c >> 4); }
+
 struct DecodeFp8Args {
   Fp8Layer L;
   AttnCall c;
-  int B, Hq, G;
+  int B, Hq, n_split;
+  unsigned* tickets;
   int* err;
+  int polls;
 };
 
-__global__ void __launch_bounds__(256) decode_fp8_kernel(DecodeFp8Args a) {
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= a.B * a.Hq) return;
-  const int b = row / a.Hq, hq = row - b * a.Hq;
+// The tiles a query at position n - 1 sees: the first `ns`, then those from
+// w0 on.
+struct Span {
+  int n, low, sinks, ns, w0, total;
+  __device__ __forceinline__ Span(int len, int window, int n_sink) {
+    n = len;
+    low = window ? max(len - window, 0) : 0;
+    sinks = window ? min(n_sink, len) : 0;
+    w0 = low / kTile;
+    ns = min((sinks + kTile - 1) / kTile, w0);
+    total = ns + (len + kTile - 1) / kTile - w0;
+  }
+  __device__ __forceinline__ int tile(int i) const { return i < ns ? i : i - ns + w0; }
+  // bit t: token t of the tile is visible
+  __device__ __forceinline__ uint32_t mask(int tile) const {
+    const int t0 = tile * kTile;
+    auto below = [&](int j) { return j <= t0 ? 0u : (j - t0 >= kTile ? 0xFFFFu : (1u << (j - t0)) - 1u); };
+    return below(n) & (~below(low) | below(sinks));
+  }
+};
+
+__device__ __forceinline__ uint32_t cvt_lo(uint32_t w) {   // codes in bytes 0, 1 -> fp16x2
+  uint32_t r;
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l; }" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t cvt_hi(uint32_t w) {   // bytes 2, 3
+  uint32_t r;
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) { return h2_as_u32(__floats2half2_rn(a, b)); }
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+template <int G>
+__global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
+  uint8_t* ring = smem + warp * kStages * kFp8TileBytes;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + kRing) + warp * kStages;
+  if (lane < kStages) mbar_init(bar + lane, 1);
+  mbar_fence_init();
+  __syncwarp();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  const int split = blockIdx.x % a.n_split, pair = blockIdx.x / a.n_split;
+  const int h = pair % a.L.Hkv, b = pair / a.L.Hkv;
   int n = a.c.seq_len[b];
   if (n < 0 || n > a.c.max_len) {
-    flag_error(a.err, KV_DEVERR_LENGTH);
+    if (split == 0 && threadIdx.x == 0) flag_error(a.err, KV_DEVERR_LENGTH);
     n = min(max(n, 0), a.c.max_len);
   }
-  attend_row(a.L, a.c.pt + (size_t)b * a.c.max_pages, a.c.max_pages, hq / a.G,
-             static_cast<const uint16_t*>(a.c.q) + (size_t)row * 128, n - 1, a.c.window, a.c.n_sink, a.c.scale,
-             static_cast<uint16_t*>(a.c.out) + (size_t)row * 128, a.c.lse ? a.c.lse + row : nullptr, a.err, lane);
+  const Span sp(n, a.c.window, a.c.n_sink);
+  const int per = (sp.total + a.n_split - 1) / a.n_split;
+  const int i0 = split * per, count = max(min(per, sp.total - i0), 0);
+  const int mine = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;   // tiles i0 + warp, + kWarps, ..
+  const int tpp = a.L.P / kTile, tpp_shift = tpp >> 1;
+  const int32_t* pt = a.c.pt + (size_t)b * a.c.max_pages;
+
+  // the stored tile of this warp's k-th tile, -1 behind a bad page id
+  auto stored = [&](int k) -> long long {
+    if (k >= mine) return -1;
+    const int tile = sp.tile(i0 + warp + k * kWarps);
+    const int pid = pt[tile >> tpp_shift];
+    if (pid < 0 || pid >= a.L.num_pages) {
+      flag_error(a.err, KV_DEVERR_PAGE_ID);
+      return -1;
+    }
+    return ((long long)pid * a.L.Hkv + h) * tpp + (tile & (tpp - 1));
+  };
+  auto exps_of = [&](long long t) -> int {
+    return t < 0 ? 0 : *reinterpret_cast<const uint16_t*>(a.L.exps + t * 2);
+  };
+  const uint64_t policy = l2_evict_first_policy();
+  auto issue = [&](int stage, long long t) {     // lane 0
+    if (t < 0) {
+      mbar_expect_tx(bar + stage, 0);
+    } else {
+      mbar_expect_tx(bar + stage, kFp8TileBytes);
+      bulk_g2s_hint(ring + stage * kFp8TileBytes, a.L.codes + t * kFp8TileBytes, kFp8TileBytes, bar + stage, policy);
+    }
+  };
+  // lane l knows the l-th tile of the current and of the next 32
+  long long cur = stored(lane);
+#pragma unroll
+  for (int k = 0; k < kStages; ++k) {
+    const long long t = __shfl_sync(0xffffffffu, cur, k);
+    if (lane == 0 && k < mine) issue(k, t);
+  }
+  int exps = exps_of(cur);
+  long long next = stored(32 + lane);
+
+  // q as the B operand: lane (r, j) holds head r, channels 64 c + 16 j + 0..15
+  uint32_t qf[2][8];
+  float cs0, cs1;
+  {
+    uint32_t top = 0;
+    if (r < G) {
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.c.q) +
+                                                      ((size_t)b * a.Hq + h * G + r) * 128);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint4 x = q[8 * c + 2 * j], y = q[8 * c + 2 * j + 1];
+        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          qf[c][i] = w[i];
+          top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) qf[i >> 3][i & 7] = 0;
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int up = min(14 - ((int)(top >> 7) - 127), 127);
+    const float mul = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : pow2i(up);   // not finite: NaN
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t w = qf[i >> 3][i & 7];
+      qf[i >> 3][i & 7] = pack_f16(bf16lo(w) * mul, bf16hi(w) * mul);
+    }
+    const float cs = a.c.scale * 1.4426950408889634f * pow2i(max(-up, -126));
+    cs0 = __shfl_sync(0xffffffffu, cs, 8 * j);          // heads 2j, 2j + 1
+    cs1 = __shfl_sync(0xffffffffu, cs, 8 * j + 4);
+  }
+
+  float M0 = kNoRef, M1 = kNoRef, l0 = 0.f, l1 = 0.f;
+  float o[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+
+  bool ok = true;
+  int k = 0, stage = 0, phase = 0;
+  for (; k < mine; ++k) {
+    if (k && (k & 31) == 0) {
+      cur = next;
+      exps = exps_of(cur);
+      next = stored(k + 32 + lane);
+    }
+    if (!mbar_wait(bar + stage, phase, a.polls)) {
+      ok = false;
+      break;
+    }
+    const int e2 = __shfl_sync(0xffffffffu, exps, k & 31);
+    const bool have = __shfl_sync(0xffffffffu, (int)(cur >= 0), k & 31);
+    if (have) {
+      const int tile = sp.tile(i0 + warp + k * kWarps);
+      const uint32_t vis = sp.mask(tile);
+      const uint8_t* codes = ring + stage * kFp8TileBytes + lane * 16;
+      uint4 kw[4], vw[4];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) kw[p] = *reinterpret_cast<const uint4*>(codes + p * 512);
+#pragma unroll
+      for (int p = 0; p < 4; ++p) vw[p] = *reinterpret_cast<const uint4*>(codes + 2048 + p * 512);
+      float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t a0 = (&kw[0].x)[w], a1 = (&kw[2].x)[w], b0 = (&kw[1].x)[w], b1 = (&kw[3].x)[w];
+        mma_f16(sa, cvt_lo(a0), cvt_lo(a1), cvt_hi(a0), cvt_hi(a1), qf[0][2 * w], qf[0][2 * w + 1]);
+        mma_f16(sb, cvt_lo(b0), cvt_lo(b1), cvt_hi(b0), cvt_hi(b1), qf[1][2 * w], qf[1][2 * w + 1]);
+      }
+      const float ev = (float)(int8_t)(e2 >> 8), fk = exp2f((float)(int8_t)(e2 & 0xFF));
+      const float c0 = cs0 * fk, c1 = cs1 * fk;
+      float x0 = fmaf(sa[0] + sb[0], c0, ev), x1 = fmaf(sa[1] + sb[1], c1, ev);   // token r, heads 2j, 2j + 1
+      float x2 = fmaf(sa[2] + sb[2], c0, ev), x3 = fmaf(sa[3] + sb[3], c1, ev);   // token r + 8
+      if (vis != 0xFFFFu) {                    // hidden tokens: no weight, and codes of zero
+        if (!((vis >> r) & 1)) x0 = x1 = -INFINITY;
+        if (!((vis >> (r + 8)) & 1)) x2 = x3 = -INFINITY;
+        const uint32_t v4 = (vis >> (2 * j)) & 3u, v5 = (vis >> (2 * j + 8)) & 3u;
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        if (!(v4 & 1)) vw[0] = z;
+        if (!(v4 & 2)) vw[1] = z;
+        if (!(v5 & 1)) vw[2] = z;
+        if (!(v5 & 2)) vw[3] = z;
+      }
+      if (__any_sync(0xffffffffu, fmaxf(x0, x2) > M0 + kRaise || fmaxf(x1, x3) > M1 + kRaise)) {
+        const float t0 = warp_max_xor(fmaxf(x0, x2), 4), t1 = warp_max_xor(fmaxf(x1, x3), 4);
+        const float n0 = t0 > M0 + kRaise ? t0 - kHead : M0, n1 = t1 > M1 + kRaise ? t1 - kHead : M1;
+        const float f0 = exp2_neg(M0 - n0), f1 = exp2_neg(M1 - n1);
+        M0 = n0;
+        M1 = n1;
+        l0 *= f0;
+        l1 *= f1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          o[i][0] *= f0;
+          o[i][1] *= f1;
+          o[i][2] *= f0;
+          o[i][3] *= f1;
+        }
+      }
+      const float w0 = exp2_neg(x0 - M0), w1 = exp2_neg(x1 - M1), w2 = exp2_neg(x2 - M0), w3 = exp2_neg(x3 - M1);
+      const float fv = exp2f(-ev);
+      l0 = fmaf(w0 + w2, fv, l0);
+      l1 = fmaf(w1 + w3, fv, l1);
+      const uint32_t p0 = movmatrix_t(pack_f16(w0, w1)), p1 = movmatrix_t(pack_f16(w2, w3));
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t v0 = (&vw[0].x)[w], v1 = (&vw[1].x)[w], v2 = (&vw[2].x)[w], v3 = (&vw[3].x)[w];
+        const uint32_t a = __byte_perm(v0, v1, 0x5140), bb = __byte_perm(v2, v3, 0x5140);
+        const uint32_t c = __byte_perm(v0, v1, 0x7362), d = __byte_perm(v2, v3, 0x7362);
+        mma_f16(o[2 * w], cvt_lo(a), cvt_hi(a), cvt_lo(bb), cvt_hi(bb), p0, p1);       // channels 16 r + 4 w + 0, 1
+        mma_f16(o[2 * w + 1], cvt_lo(c), cvt_hi(c), cvt_lo(d), cvt_hi(d), p0, p1);     // + 2, 3
+      }
+    }
+    __syncwarp();
+    const int kn = k + kStages;
+    if (kn < mine) {
+      const long long t = __shfl_sync(0xffffffffu, (kn >> 5) == (k >> 5) ? cur : next, kn & 31);
+      if (lane == 0) issue(stage, t);
+    }
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+  if (!ok) {                                   // a copy did not arrive: wait (bounded) for those in flight
+    if (lane == 0) flag_error(a.err, KV_DEVERR_TIMEOUT);
+    for (int kk = k + 1; kk < min(mine, k + kStages); ++kk) {
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+      mbar_wait(bar + stage, phase, a.polls);
+    }
+    M0 = M1 = kNoRef;
+    l0 = l1 = 0.f;
+  }
+
+  // ---- the warps' results -> the CTA's ----
+  __syncthreads();                             // every warp is done with its ring
+  float* wo = reinterpret_cast<float*>(smem);
+  float* wm = wo + kWarps * G * kHeadStride;   // [warp][head] M, then l
+  float* wl = wm + kWarps * G;
+  l0 = warp_sum_xor(l0, 4);
+  l1 = warp_sum_xor(l1, 4);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int g = 2 * j + u;
+    if (g < G) {
+      float* d = wo + (warp * G + g) * kHeadStride;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        d[chan(16 * r + 2 * i)] = o[i][u];
+        d[chan(16 * r + 2 * i + 1)] = o[i][2 + u];
+      }
+      if (r == 0) {
+        wm[warp * G + g] = u ? M1 : M0;
+        wl[warp * G + g] = u ? l1 : l0;
+      }
+    }
+  }
+  __syncthreads();
+  uint16_t* out = static_cast<uint16_t*>(a.c.out) + ((size_t)b * a.Hq + h * G) * 128;
+  float* lse = a.c.lse ? a.c.lse + (size_t)b * a.Hq + h * G : nullptr;
+  float* parts = static_cast<float*>(a.c.ws) + (size_t)pair * a.n_split * G * kPart;
+  for (int idx = threadIdx.x; idx < G * 128; idx += kThreads) {
+    const int g = idx >> 7, c = idx & 127;
+    float M = kNoRef;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w * G + g]);
+    float l = 0.f, s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = wl[w * G + g] == 0.f ? 0.f : exp2_neg(wm[w * G + g] - M);
+      l = fmaf(f, wl[w * G + g], l);
+      if (f != 0.f) s = fmaf(f, wo[(w * G + g) * kHeadStride + chan(c)], s);
+    }
+    if (a.n_split == 1) {
+      const float y = l == 0.f ? 0.f : s / l;
+      out[g * 128 + c] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+      if (c == 0 && lse) lse[g] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+    } else {
+      float* p = parts + ((size_t)split * G + g) * kPart;
+      p[4 + c] = s;
+      if (c == 0) {
+        p[0] = M;
+        p[1] = l;
+      }
+    }
+  }
+  if (a.n_split == 1) return;
+
+  // ---- the last CTA of the pair joins the splits, in their order ----
+  __shared__ int last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const unsigned t = atomicAdd(a.tickets + pair, 1u);
+    last = t == (unsigned)a.n_split - 1u;
+    if (last) a.tickets[pair] = 0;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  float* sw = reinterpret_cast<float*>(smem);  // weights [split][G]
+  float* sl = sw + kMaxSplits * G;             // [G] M, l
+  if (warp < G) {
+    const int g = warp;
+    float M = kNoRef, l = 0.f;
+    float m[kMaxSplits / 32], ll[kMaxSplits / 32];
+#pragma unroll
+    for (int u = 0; u < kMaxSplits / 32; ++u) {
+      const int s = lane + 32 * u;
+      m[u] = kNoRef;
+      ll[u] = 0.f;
+      if (s < a.n_split) {
+        const float2 t = __ldcg(reinterpret_cast<const float2*>(parts + ((size_t)s * G + g) * kPart));
+        m[u] = t.x;
+        ll[u] = t.y;
+      }
+      M = fmaxf(M, m[u]);
+    }
+    M = warp_max_xor(M, 1);
+#pragma unroll
+    for (int u = 0; u < kMaxSplits / 32; ++u) {
+      const float f = ll[u] == 0.f ? 0.f : exp2_neg(m[u] - M);
+      l = fmaf(f, ll[u], l);
+      if (lane + 32 * u < kMaxSplits) sw[(lane + 32 * u) * G + g] = f;
+    }
+    l = warp_sum_xor(l, 1);
+    if (lane == 0) {
+      sl[g] = l;
+      if (lse) lse[g] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+    }
+  }
+  __syncthreads();
+  // G * 32 columns of four channels; where threads are left, several share a
+  // column, each a run of splits
+  constexpr int kCols = G * 32, kShare = kThreads / kCols;
+  const int col = threadIdx.x % kCols, sh = threadIdx.x / kCols;
+  const int g = col >> 5, c4 = col & 31;
+  const int run = (a.n_split + kShare - 1) / kShare, s0 = sh * run, s1 = min(s0 + run, a.n_split);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int s = s0; s < s1; ++s) {
+    const float4 p = __ldcg(reinterpret_cast<const float4*>(parts + ((size_t)s * G + g) * kPart + 4) + c4);
+    const float f = sw[s * G + g];
+    if (f != 0.f) {
+      acc.x = fmaf(f, p.x, acc.x);
+      acc.y = fmaf(f, p.y, acc.y);
+      acc.z = fmaf(f, p.z, acc.z);
+      acc.w = fmaf(f, p.w, acc.w);
+    }
+  }
+  float4* red = reinterpret_cast<float4*>(sl + ((G + 3) & ~3));
+  if (kShare > 1) {
+    red[threadIdx.x] = acc;
+    __syncthreads();
+  }
+  if (sh == 0) {
+#pragma unroll
+    for (int u = 1; u < kShare; ++u) {
+      const float4 t = red[u * kCols + col];
+      acc.x += t.x;
+      acc.y += t.y;
+      acc.z += t.z;
+      acc.w += t.w;
+    }
+    const float l = sl[g], f = l == 0.f ? 0.f : 1.f / l;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * f, acc.y * f), hi = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+    *reinterpret_cast<uint2*>(out + g * 128 + 4 * c4) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
+}
+
+// Splits per (sequence, KV head), from the host's bound on visible tiles.  A
+// batch that does not fill the GPU is split into one wave of CTAs; a larger one
+// into about four waves, so that sequences of different lengths even out.  A
+// split has at least a tile per warp.
+int splits(const Pool& p, int B, long long max_len, int window, int n_sink) {
+  long long tokens = max_len;
+  if (window) tokens = std::min(tokens, (long long)window + n_sink + 2 * kTile);
+  const long long tiles = (tokens + kTile - 1) / kTile, pairs = (long long)B * p.cfg.num_kv_heads;
+  const long long slots = 2ll * p.sm_count;
+  const long long want = pairs * 2 <= slots ? slots / pairs : (4 * slots + pairs - 1) / pairs;
+  const long long most = std::min<long long>((tiles + kWarps - 1) / kWarps, kMaxSplits);
+  return (int)std::max(1ll, std::min(want, most));
+}
+
+template <int G>
+cudaError_t launch_t(const DecodeFp8Args& a, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(decode_fp8_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)a.B * a.L.Hkv * a.n_split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_fp8_kernel<G>, a);
 }
 
 }  // namespace
 
-size_t decode_fp8_workspace(const Pool& p, int B, int max_len) { return 16; }
+size_t decode_fp8_workspace(const Pool& p, int B, int max_len) {
+  const int n = splits(p, B, max_len, 0, 0);
+  return n == 1 ? 16 : (size_t)B * p.cfg.num_q_heads * n * kPart * sizeof(float);
+}
 
 cudaError_t launch_decode_fp8(const Pool& p, const Fp8Store& f, int layer, int B, const AttnCall& c, cudaStream_t s) {
-  DecodeFp8Args a{fp8_layer(p, f, layer), c, B, p.cfg.num_q_heads, p.G, p.err};
-  decode_fp8_kernel<<<(unsigned)(((long long)B * a.Hq + 7) / 8), 256, 0, s>>>(a);
-  return cudaGetLastError();
+  DecodeFp8Args a{fp8_layer(p, f, layer), c, B, p.cfg.num_q_heads, splits(p, B, c.max_len, c.window, c.n_sink),
+                  p.tickets + (size_t)layer * p.cfg.max_seqs * p.cfg.num_kv_heads, p.err,
+                  p.test_wait_polls > 0 ? p.test_wait_polls : kPolls};
+  switch (p.G) {
+    case 1: return launch_t<1>(a, s);
+    case 2: return launch_t<2>(a, s);
+    case 4: return launch_t<4>(a, s);
+    default: return launch_t<8>(a, s);
+  }
 }
 
 }  // namespace kvint2
