@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
     for (int w = 0; w < kWarps; ++w) {
       const float f = wl[w * G + g] == 0.f ? 0.f : exp2_neg(wm[w * G + g] - M);
       l = fmaf(f, wl[w * G + g], l);
-      if (f != 0.f) s = fmaf(f, wo[(w * G + g) * kHeadStride + chan(c)], s);
+      if (wl[w * G + g] != 0.f) s = fmaf(f, wo[(w * G + g) * kHeadStride + chan(c)], s);
     }
     if (a.n_split == 1) {
       const float y = l == 0.f ? 0.f : s / l;
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
     for (int u = 0; u < kMaxSplits / 32; ++u) {
       const float f = ll[u] == 0.f ? 0.f : exp2_neg(m[u] - M);
       l = fmaf(f, ll[u], l);
-      if (lane + 32 * u < kMaxSplits) sw[(lane + 32 * u) * G + g] = f;
+      sw[(lane + 32 * u) * G + g] = ll[u] == 0.f ? -1.f : f;   // below 0: a split that saw no token
     }
     l = warp_sum_xor(l, 1);
     if (lane == 0) {
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
   for (int s = s0; s < s1; ++s) {
     const float4 p = __ldcg(reinterpret_cast<const float4*>(parts + ((size_t)s * G + g) * kPart + 4) + c4);
     const float f = sw[s * G + g];
-    if (f != 0.f) {
+    if (!(f < 0.f)) {
       acc.x = fmaf(f, p.x, acc.x);
       acc.y = fmaf(f, p.y, acc.y);
       acc.z = fmaf(f, p.z, acc.z);

@@ -1,48 +1,764 @@
-// Prompt attention over the 8-bit cache.
-#include "kv_fp8_simple.cuh"
+// Prompt attention over the 8-bit cache on the tcgen05 tensor cores.
+//
+// A row is a (query token, query head of the KV head) pair, so the G heads that
+// share a KV head share its tiles: a block of 256 rows holds 256 / G tokens.
+// Per row, with base-2 logits  x_j = |scale| log2(e) 2^eK (q . k_j) + eV  (codes
+// k, v of exponents eK, eV; q carries scale's sign):
+//   w_j = 2^(x_j - M),   out = sum_j w_j v_j / sum_j w_j 2^-eV.
+// Operands are fp16: e4m3 codes times a power of two convert exactly (the 16
+// token blocks of a 128-token tile are taken together while their exponents lie
+// within 14 of one another, else in several passes); q is scaled per row by a
+// power of two (largest element in [2^14, 2^15): exact for bf16's 8 bits down
+// to 2^-32 of it); the weights are rounded to fp16 relative to their own size,
+// between 2^-31 of the largest and 2^15, M lagging behind the running maximum
+// so that the accumulator is rescaled only when a weight would pass 2^15.
+//
+// Bound: the tensor cores (4 * 128 operations per row and key), with the
+// exponentials close behind.  One CTA per SM: two tiles of 128 rows take turns,
+// one in the tensor cores while the other is in the softmax.
+//   warps 0-3, 4-7   softmax of a tile: a thread owns a row; S is read from
+//                    tensor memory, the weights go back over it as fp16
+//   warps 8-11       converters: codes from global memory to registers (loads
+//                    of the next operand in flight), fp16 in the swizzled
+//                    operand layout to shared memory (two stages each of K, V)
+//   warp 12          issues the products: S = Q K^T from shared memory, O += P V
+//                    with P from tensor memory and V token-major as it is stored
+// Tensor memory: S0, S1 (P over them), O0, O1, 128 columns each.
+// Hidden keys: a tile that some row sees only in part is masked by select after
+// the product (a NaN in a hidden K row never enters), its V rows that hold NaN
+// are zeroed and listed, and a row that sees one of those becomes NaN as a whole
+// (the append stores a row with a NaN as NaN in every channel).
+// Few rows: the keys are split over several CTAs, whose normalised parts a
+// second kernel joins by their log-sum-exp.
+#include <algorithm>
+
+#include "kv_device.cuh"
+#include "kv_fp8.h"
 
 namespace kvint2 {
 
 namespace {
 
+constexpr int kRows = 128;                     // rows of a tile (M of a product)
+constexpr int kKeys = 128;                     // keys of a tile
+constexpr int kBlocks = kKeys / kTile;
+constexpr int kThreads = 13 * 32;
+constexpr int kPolls = 1 << 20;
+constexpr int kMaxSplits = 32;
+constexpr float kNoRef = -3e38f;
+constexpr float kRaise = 15.f, kHead = 7.f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+constexpr uint32_t kOperand = kKeys * 256;     // 128 x 128 fp16
+constexpr uint32_t kOffQ = 0;                  // two tiles
+constexpr uint32_t kOffK = 2 * kOperand;       // two stages
+constexpr uint32_t kOffV = 4 * kOperand;       // two stages
+constexpr uint32_t kOffInfo = 6 * kOperand;
+
+// What a key tile's converters tell the other warps; a ring of four.
+struct TileInfo {
+  int t0;                                      // first key
+  uint32_t blocks;                             // 16-token blocks present in this pass
+  float fk, ev;                                // 2^eK, eV of the operands
+  int last;                                    // no tile follows
+  int partial;                                 // V rows with NaN were zeroed and listed
+  uint32_t nan[4];                             // those rows
+  int pad[2];
+};
+
+enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kOFull = 12, kDrain = 13, kBars = 14 };
+
+struct Shared {
+  TileInfo info[4];
+  uint64_t bars[kBars];
+  uint32_t tmem;
+  int abort;
+};
+constexpr uint32_t kSmem = kOffInfo + sizeof(Shared) + 1024;
+
 struct PrefillFp8Args {
   Fp8Layer L;
   AttnCall c;
   const int32_t* cu;
-  int max_q, Hq, G;
+  int n_seqs, max_q, Hq, G, n_split, q_blocks;
   int* err;
+  int polls;
 };
 
-__global__ void __launch_bounds__(256) prefill_fp8_kernel(PrefillFp8Args a) {
-  const int s = blockIdx.y, lane = threadIdx.x & 31;
-  const int c0 = a.cu[s], m = a.cu[s + 1] - c0;
-  int n = a.c.seq_len[s];
-  if (m < 0 || m > a.max_q) {
-    flag_error(a.err, KV_DEVERR_SEQ_RANGE);
-    return;
+// ---- tcgen05 ----------------------------------------------------------------
+
+// Shared-memory operand of 128-byte rows in the 128-byte swizzle (8-row atoms of
+// 1024 bytes).  K-major (Q, K): the leading offset is unused.  MN-major (V: rows
+// are tokens, 64 channels each): leading offset = the second 64 channels,
+// stride offset = the next 8 tokens.
+__device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t lead) {
+  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(lead >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+// kind::f16, fp32 accumulator, fp16 operands, M = N = 128; bit 16: B is MN-major
+constexpr uint32_t kIdescQK = (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(kIdescQK), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+      "r"(a), "l"(b), "r"(kIdescPV), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ void ld32(uint32_t t, float (&v)[32]) {
+  uint32_t u[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(t)
+      : "memory");
+  wait_ld();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+}
+__device__ __forceinline__ void st16(uint32_t t, const uint32_t (&u)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
+      "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+      : "memory");
+}
+__device__ __forceinline__ void st32(uint32_t t, const float (&v)[32]) {
+  uint32_t a[16], b[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    a[i] = __float_as_uint(v[i]);
+    b[i] = __float_as_uint(v[16 + i]);
   }
-  if (n < 0 || n > a.c.max_len) {
-    flag_error(a.err, KV_DEVERR_LENGTH);
-    n = min(max(n, 0), a.c.max_len);
+  st16(t, a);
+  st16(t + 16, b);
+}
+
+__device__ __forceinline__ uint32_t cvt_lo(uint32_t w) {   // codes in bytes 0, 1 -> fp16x2
+  uint32_t r;
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l; }" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t cvt_hi(uint32_t w) {
+  uint32_t r;
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) { return h2_as_u32(__floats2half2_rn(a, b)); }
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// Bits [0, x) of a word that starts at bit `from`.
+__device__ __forceinline__ uint32_t below(int x, int from) {
+  const int n = x - from;
+  return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
+}
+
+// The rows of a CTA and the key tiles they see.
+struct Work {
+  int s, h, c0, m, n, row0, split;             // sequence, KV head, first q row, queries, keys, first row of the block
+  int pos0;                                    // position of the sequence's query 0
+  int low, sinks, ns, w0, i0, i1;              // tile list: the first ns tiles, then from w0; this split's part of it
+  __device__ __forceinline__ int tile(int i) const { return i < ns ? i : i - ns + w0; }
+};
+
+__device__ __forceinline__ bool find_work(const PrefillFp8Args& a, Work& w) {
+  // blocks of a sequence from its last (most keys) to its first
+  int x = blockIdx.x;
+  w.split = x % a.n_split;
+  x /= a.n_split;
+  w.h = x % a.L.Hkv;
+  x /= a.L.Hkv;
+  w.s = x % a.n_seqs;
+  const int blk = a.q_blocks - 1 - x / a.n_seqs;
+  w.c0 = a.cu[w.s];
+  w.m = a.cu[w.s + 1] - w.c0;
+  w.n = a.c.seq_len[w.s];
+  const bool first = threadIdx.x == 0 && blk == 0 && w.split == 0 && w.h == 0;
+  if (w.m < 0 || w.m > a.max_q) {
+    if (first) flag_error(a.err, KV_DEVERR_SEQ_RANGE);
+    return false;
   }
+  if (w.n < 0 || w.n > a.c.max_len) {
+    if (first) flag_error(a.err, KV_DEVERR_LENGTH);
+    w.n = min(max(w.n, 0), a.c.max_len);
+  }
+  w.row0 = blk * 2 * kRows;
+  if ((long long)w.row0 >= (long long)w.m * a.G) return false;
+  w.pos0 = w.n - w.m;
+  const int p_lo = w.pos0 + w.row0 / a.G, p_hi = w.pos0 + min((w.row0 + 2 * kRows) / a.G, w.m) - 1;
+  w.low = a.c.window ? max(p_lo - a.c.window + 1, 0) : 0;
+  const int end = max(p_hi + 1, 0);
+  w.sinks = a.c.window ? a.c.n_sink : 0;
+  w.w0 = min(w.low, end) / kKeys;
+  w.ns = min((min(w.sinks, end) + kKeys - 1) / kKeys, w.w0);
+  const int total = w.ns + (end + kKeys - 1) / kKeys - w.w0;
+  const int per = (total + a.n_split - 1) / a.n_split;
+  w.i0 = min(w.split * per, total);
+  w.i1 = min(w.i0 + per, total);
+  return true;
+}
+
+struct Waiter {
+  int* abort;
+  int polls;
+  // whether the phase with `parity` completed; a wait that runs out ends every role
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+    if (mbar_wait(bar, parity, 64)) return true;
+    for (int i = 64; i < polls; i += 64) {
+      if (*reinterpret_cast<volatile int*>(abort)) return false;
+      if (mbar_wait(bar, parity, 64)) return true;
+    }
+    *reinterpret_cast<volatile int*>(abort) = 1;
+    return false;
+  }
+};
+
+// ---- converters (128 threads) -------------------------------------------------
+
+struct Block16 {                               // eight pieces of one operand: piece `tid` of each 16-token block
+  uint4 w[kBlocks];
+};
+
+__device__ __forceinline__ void store_run(uint8_t* operand, int token, int run, const uint4& w, uint32_t mul,
+                                          bool swap) {
+  uint32_t f[8];
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  const __half2 m = u32_as_h2(mul);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = h2_as_u32(__hmul2(u32_as_h2(cvt_lo(x[i])), m));
+    f[2 * i + 1] = h2_as_u32(__hmul2(u32_as_h2(cvt_hi(x[i])), m));
+  }
+  uint8_t* row = operand + (run >> 2) * (kOperand / 2) + token * 128;
+  const int c = 2 * (run & 3), sw = token & 7;
+  uint4* p0 = reinterpret_cast<uint4*>(row + ((c ^ sw) << 4));
+  uint4* p1 = reinterpret_cast<uint4*>(row + (((c + 1) ^ sw) << 4));
+  const uint4 v0 = make_uint4(f[0], f[1], f[2], f[3]), v1 = make_uint4(f[4], f[5], f[6], f[7]);
+  if (!swap) {
+    *p0 = v0;
+    *p1 = v1;
+  } else {                                     // the other order: the lanes of a phase hit different banks
+    *p1 = v1;
+    *p0 = v0;
+  }
+}
+
+// 2^d, d <= 0 (0 below fp16's range), in both halves
+__device__ __forceinline__ uint32_t half_pow2(int d) {
+  return h2_as_u32(__float2half2_rn(pow2i(max(min(d, 0), -126))));
+}
+
+// Whether `ok` holds for all 128 converter threads (a barrier for them).
+__device__ __forceinline__ bool converters_and(bool ok) {
+  int r;
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.b32 p, %1, 0; bar.red.and.pred q, 1, 128, p; selp.b32 %0, 1, 0, q; }"
+      : "=r"(r)
+      : "r"((int)ok)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ bool has_nan(uint32_t w) { return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0; }
+
+__device__ __forceinline__ void convert_tiles(const PrefillFp8Args& a, const Work& w, uint8_t* sm, Shared* sh,
+                                              const Waiter& wait) {
+  const int tid = threadIdx.x - 256, lane = tid & 31;
+  const int tpp = a.L.P / kTile, shift = tpp >> 1;
+  const int32_t* pt = a.c.pt + (size_t)w.s * a.c.max_pages;
+  const int lastpos = w.pos0 + min((w.row0 + 2 * kRows) / a.G, w.m) - 1, firstpos = w.pos0 + w.row0 / a.G;
+  const int keys = max(lastpos + 1, 0);        // keys behind it are hidden from every row
+  // piece `tid` of a stored K and V block: its token and run of 16 channels
+  const int ktok = 8 * (tid >> 6) + ((tid >> 2) & 7), krun = 4 * ((tid >> 5) & 1) + (tid & 3);
+  const int vtok = 8 * (tid >> 6) + 2 * (tid & 3) + ((tid >> 5) & 1), vrun = (tid >> 2) & 7;
+
+  // lane u < 8: block u of tile i -> stored tile (or -1) and exponents
+  auto find = [&](int i, long long& st, int& e) {
+    st = -1;
+    e = 0;
+    if (i >= w.i1 || lane >= kBlocks) return;
+    const int t = w.tile(i) * kBlocks + lane, j0 = t * kTile;
+    // a block that no row sees is absent (its page may have been given up)
+    if (j0 >= keys || (a.c.window && j0 + kTile <= w.low && j0 >= w.sinks)) return;
+    const int pid = pt[t >> shift];
+    if (pid < 0 || pid >= a.L.num_pages) {
+      flag_error(a.err, KV_DEVERR_PAGE_ID);
+      return;
+    }
+    st = ((long long)pid * a.L.Hkv + w.h) * tpp + (t & (tpp - 1));
+    e = *reinterpret_cast<const uint16_t*>(a.L.exps + st * 2);
+  };
+  long long st;
+  int ex;
+  find(w.i0, st, ex);
+  int it = 0;
+  bool ok = true;
+  for (int i = w.i0; i < w.i1; ++i) {
+    const int t0 = w.tile(i) * kKeys;
+    uint32_t left = __ballot_sync(0xffffffffu, st >= 0);
+    const int ek = (int8_t)(ex & 0xFF), ev = (int8_t)(ex >> 8);
+    long long st_next;
+    int ex_next;
+    find(i + 1, st_next, ex_next);
+    bool first = true;
+    while (first || left) {
+      first = false;
+      // the blocks of this pass: exponents within 7 of the first one left
+      uint32_t now = 0;
+      int mk = 0, mv = 0;
+      if (left) {
+        const int u0 = __ffs(left) - 1;
+        const int k0 = __shfl_sync(0xffffffffu, ek, u0), v0 = __shfl_sync(0xffffffffu, ev, u0);
+        const bool in = ((left >> lane) & 1) && abs(ek - k0) <= 7 && abs(ev - v0) <= 7;
+        now = __ballot_sync(0xffffffffu, in);
+        mk = __reduce_max_sync(0xffffffffu, in ? ek : -1000);
+        mv = __reduce_max_sync(0xffffffffu, in ? ev : -1000);
+        left &= ~now;
+      }
+      const bool partial = now != 0xFFu || t0 + kKeys - 1 > firstpos ||
+                           (a.c.window && t0 <= lastpos - a.c.window && t0 + kKeys > w.sinks);
+      const int stage = it & 1;
+      const uint32_t ph = ((it >> 1) & 1) ^ 1;   // of the empty barriers: the use before this one
+      TileInfo& info = sh->info[it & 3];
+      Block16 k, v;
+#pragma unroll
+      for (int u = 0; u < kBlocks; ++u) {
+        const long long s = __shfl_sync(0xffffffffu, st, u);
+        k.w[u] = v.w[u] = make_uint4(0, 0, 0, 0);
+        if ((now >> u) & 1) {
+          const uint8_t* p = a.L.codes + s * kFp8TileBytes + tid * 16;
+          k.w[u] = ld_stream_v4(p);
+          v.w[u] = ld_stream_v4(p + 2048);
+        }
+      }
+      if (ok && it >= 2) ok = wait(sh->bars + kKEmpty + stage, ph);
+      if (tid == 0) {
+        info.t0 = t0;
+        info.blocks = now;
+        info.fk = pow2i(max(min(mk, 127), -126));
+        info.ev = (float)mv;
+        info.last = i + 1 == w.i1 && !left;
+        info.partial = partial;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) info.nan[q] = 0;
+      }
+      if (!converters_and(ok)) return;         // the record is in place; all four warps go on, or none
+      uint8_t* sk = sm + kOffK + stage * kOperand;
+#pragma unroll
+      for (int u = 0; u < kBlocks; ++u) {
+        const uint32_t m = __shfl_sync(0xffffffffu, half_pow2(ek - mk), u);
+        store_run(sk, kTile * u + ktok, krun, k.w[u], m, false);
+      }
+      fence_async();
+      arrive(sh->bars + kKFull + stage);
+      if (it >= 2) ok = wait(sh->bars + kVEmpty + stage, ph);
+      ok = __all_sync(0xffffffffu, ok);        // a failure ends the next pass, for all four warps
+      uint8_t* sv = sm + kOffV + stage * kOperand;
+#pragma unroll
+      for (int u = 0; u < kBlocks; ++u) {
+        if (!ok) break;                        // products may still read the stage
+        const uint32_t m = __shfl_sync(0xffffffffu, half_pow2(ev - mv), u);
+        const int tok = kTile * u + vtok;
+        if (partial) {
+          uint4& x = v.w[u];
+          if (t0 + tok >= keys) x = make_uint4(0, 0, 0, 0);
+          if (has_nan(x.x) || has_nan(x.y) || has_nan(x.z) || has_nan(x.w)) {
+            x = make_uint4(0, 0, 0, 0);
+            atomicOr(&info.nan[tok >> 5], 1u << (tok & 31));
+          }
+        }
+        store_run(sv, tok, vrun, v.w[u], m, (vrun & 1) != 0);
+      }
+      fence_async();
+      if (ok) arrive(sh->bars + kVFull + stage);
+      ++it;
+    }
+    st = st_next;
+    ex = ex_next;
+  }
+}
+
+// ---- product issuer (one thread) ----------------------------------------------
+
+__device__ __forceinline__ void issue_products(uint32_t tmem, uint8_t* sm, Shared* sh, const Waiter& wait) {
+  const uint32_t base = smem_u32(sm);
+  auto scores = [&](int tile, int stage) {
+    const uint64_t q = desc(base + kOffQ + tile * kOperand, 16), k = desc(base + kOffK + stage * kOperand, 16);
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+      const uint32_t off = ((ks >> 2) * (kOperand / 2) + (ks & 3) * 32) >> 4;
+      mma_ss(tmem + 128 * tile, q + off, k + off, ks > 0);
+    }
+    commit(sh->bars + kSFull + tile);
+    arrive(sh->bars + kSFull + tile);          // a release after this thread saw the tile's record
+  };
+  if (!wait(sh->bars + kKFull, 0)) return;
+  fence_after();
+  scores(0, 0);
+  scores(1, 0);
+  commit(sh->bars + kKEmpty);
+  for (int it = 0;; ++it) {
+    const int stage = it & 1;
+    const uint32_t ph = (it >> 1) & 1;
+    const bool last = sh->info[it & 3].last != 0;
+    if (!wait(sh->bars + kVFull + stage, ph)) return;
+    if (!last && !wait(sh->bars + kKFull + (stage ^ 1), ((it + 1) >> 1) & 1)) return;
+    const uint64_t v = desc(base + kOffV + stage * kOperand, kOperand / 2);
+#pragma unroll
+    for (int tile = 0; tile < 2; ++tile) {
+      if (!wait(sh->bars + kPFull + tile, it & 1)) return;
+      fence_after();
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks)           // 16 tokens: 8 columns of P, 16 rows of V
+        mma_ts(tmem + 256 + 128 * tile, tmem + 128 * tile + 8 * ks, v + ((ks * 2048) >> 4), it > 0 || ks > 0);
+      if (tile == 1) commit(sh->bars + kVEmpty + stage);
+      if (!last) scores(tile, stage ^ 1);
+    }
+    if (last) break;
+    commit(sh->bars + kKEmpty + (stage ^ 1));
+  }
+  commit(sh->bars + kOFull);
+  arrive(sh->bars + kOFull);
+}
+
+// ---- softmax (a thread owns a row) ---------------------------------------------
+
+struct RowOut {
+  float M = kNoRef, l = 0.f;
+  bool poison = false;
+};
+
+__device__ __forceinline__ bool softmax_rows(const PrefillFp8Args& a, const Work& w, uint32_t trow, int tile, int pos,
+                                             float cs, Shared* sh, const Waiter& wait, RowOut& ro) {
+  const uint32_t ts = trow + 128 * tile, to = trow + 256 + 128 * tile;
+  uint32_t see[4] = {0, 0, 0, 0};
+  bool check = false;                          // `see` of the previous tile is to be held against its NaN rows
+  for (int it = 0;; ++it) {
+    if (!__all_sync(0xffffffffu, wait(sh->bars + kSFull + tile, it & 1))) return false;
+    fence_after();
+    const TileInfo& info = sh->info[it & 3];
+    if (check) {
+      const TileInfo& old = sh->info[(it - 1) & 3];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) ro.poison |= (old.nan[q] & see[q]) != 0;
+    }
+    const bool partial = info.partial != 0, last = info.last != 0;
+    const float c = cs * info.fk, ev = info.ev;
+    if (partial) {
+      const int t0 = info.t0;
+      const uint32_t blocks = info.blocks;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t m = below(pos + 1 - t0, 32 * q);
+        if (a.c.window) m &= ~below(pos + 1 - a.c.window - t0, 32 * q) | below(w.sinks - t0, 32 * q);
+        m &= ((blocks >> (2 * q)) & 1 ? 0xFFFFu : 0u) | ((blocks >> (2 * q + 1)) & 1 ? 0xFFFF0000u : 0u);
+        see[q] = m;
+      }
+    }
+    check = partial;
+    float top = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float v[32];
+      ld32(ts + 32 * q, v);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if (partial && !((see[q] >> i) & 1)) v[i] = -INFINITY;
+        top = fmaxf(top, v[i]);
+      }
+    }
+    const float x = top == -INFINITY ? -INFINITY : fmaf(top, c, ev);
+    const bool raise = x > ro.M + kRaise;
+    if (__any_sync(0xffffffffu, raise)) {
+      const float n = raise ? x - kHead : ro.M;
+      const float f = exp2_neg(ro.M - n);
+      ro.M = n;
+      ro.l *= f;
+      if (it > 0) {                            // the products so far are complete: S of this tile came after them
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v[32];
+          ld32(to + 32 * q, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] *= f;
+          st32(to + 32 * q, v);
+        }
+      }
+    }
+    const float d = ev - ro.M;
+    float sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float v[32];
+      ld32(ts + 32 * q, v);
+      uint32_t p[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float y0 = exp2_neg(fmaf(v[2 * i], c, d)), y1 = exp2_neg(fmaf(v[2 * i + 1], c, d));
+        if (partial) {
+          if (!((see[q] >> (2 * i)) & 1)) y0 = 0.f;
+          if (!((see[q] >> (2 * i + 1)) & 1)) y1 = 0.f;
+        }
+        sum += y0 + y1;
+        p[i] = pack_f16(y0, y1);
+      }
+      st16(ts + 16 * q, p);
+    }
+    ro.l = fmaf(sum, exp2f(-ev), ro.l);
+    wait_st();
+    fence_before();
+    arrive(sh->bars + kPFull + tile);
+    if (last) {
+      if (!__all_sync(0xffffffffu, wait(sh->bars + kOFull, 0))) return false;
+      fence_after();
+      if (check) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) ro.poison |= (info.nan[q] & see[q]) != 0;
+      }
+      return true;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args a) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  Shared* sh = reinterpret_cast<Shared*>(sm + kOffInfo);
+  Work w;
+  if (!find_work(a, w)) return;                // the same for all threads
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sh->bars + kKFull + i, 128);
+      mbar_init(sh->bars + kVFull + i, 128);
+      mbar_init(sh->bars + kKEmpty + i, 1);
+      mbar_init(sh->bars + kVEmpty + i, 1);
+      mbar_init(sh->bars + kSFull + i, 2);
+      mbar_init(sh->bars + kPFull + i, 128);
+    }
+    mbar_init(sh->bars + kOFull, 2);
+    mbar_init(sh->bars + kDrain, 1);
+    mbar_fence_init();
+    sh->abort = 0;
+  }
+  const bool any = w.i0 < w.i1;                // this CTA has keys at all
+  if (warp == 12 && any) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh->tmem)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // q: a thread's row, scaled by a power of two, fp16, swizzled
+  const int tile = warp >> 2, m = threadIdx.x & 127;
+  const int row = w.row0 + tile * kRows + m;   // of the sequence's rows
+  const int token = row / a.G, hq = w.h * a.G + row % a.G;
+  const bool live = warp < 8 && token < w.m;
+  const size_t qrow = ((size_t)w.c0 + token) * a.Hq + hq;
+  float cs = 0.f;
+  if (warp < 8 && any) {
+    uint32_t x[64], top = 0;
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.c.q) + (live ? qrow : 0) * 128);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint4 t = live ? q[i] : make_uint4(0, 0, 0, 0);
+      x[4 * i] = t.x;
+      x[4 * i + 1] = t.y;
+      x[4 * i + 2] = t.z;
+      x[4 * i + 3] = t.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 64; ++i) top = max(top, max(x[i] & 0x7FFFu, (x[i] >> 16) & 0x7FFFu));
+    const int up = min(14 - ((int)(top >> 7) - 127), 127);
+    float mul = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : pow2i(up);
+    if (a.c.scale < 0.f) mul = -mul;
+    cs = fabsf(a.c.scale) * 1.4426950408889634f * pow2i(max(-up, -126));
+    uint8_t* dst = sm + kOffQ + tile * kOperand + m * 128;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      uint32_t f[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) f[u] = pack_f16(bf16lo(x[4 * i + u]) * mul, bf16hi(x[4 * i + u]) * mul);
+      *reinterpret_cast<uint4*>(dst + (i >> 3) * (kOperand / 2) + (((i & 7) ^ (m & 7)) << 4)) =
+          make_uint4(f[0], f[1], f[2], f[3]);
+    }
+    fence_async();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = any ? sh->tmem : 0;
+  const Waiter wait{&sh->abort, a.polls};
+  const int pos = w.pos0 + token;
+  RowOut ro;
+  bool ok = true;
+  if (any) {
+    if (warp < 8) {
+      ok = softmax_rows(a, w, tmem + ((uint32_t)(32 * (warp & 3)) << 16), tile, pos, cs, sh, wait, ro);
+    } else if (warp < 12) {
+      convert_tiles(a, w, sm, sh, wait);
+    } else if (lane == 0) {
+      issue_products(tmem, sm, sh, wait);
+    }
+    __syncwarp();
+  }
+  // ---- results: a row per thread ----
+  if (warp < 8) {
+    const bool empty = ro.l == 0.f;
+    const float f = !ok || ro.poison ? __uint_as_float(0x7FC00000u) : (empty ? 0.f : 1.f / ro.l);
+    const float lse = empty ? -INFINITY : (ro.M + log2f(ro.l)) * kLn2;
+    const uint32_t to = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 256 + 128 * tile;
+    float* part = static_cast<float*>(a.c.ws) +
+                  (((size_t)w.s * a.max_q + token) * a.Hq + hq) * a.n_split * 132 + (size_t)w.split * 132;
+    uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.c.out) + qrow * 128);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float v[32];
+      __syncwarp();
+      if (any && ok) {                         // the same for the whole warp
+        ld32(to + 32 * q, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = empty ? 0.f : v[i] * f;
+      if (live && a.n_split > 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<float4*>(part + 4 + 32 * q + 4 * i) =
+              make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      } else if (live) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t u[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 y = __floats2bfloat162_rn(v[8 * i + 2 * e], v[8 * i + 2 * e + 1]);
+            u[e] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+          out[4 * q + i] = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+      }
+    }
+    if (live) {
+      if (a.n_split > 1)
+        part[0] = lse;
+      else if (a.c.lse)
+        a.c.lse[qrow] = lse;
+    }
+  }
+  if (!any) return;
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 12) {
+    if (sh->abort) {                           // products may be in flight: wait (bounded) before giving back the memory
+      if (lane == 0) {
+        flag_error(a.err, KV_DEVERR_TIMEOUT);
+        commit(sh->bars + kDrain);
+        mbar_wait(sh->bars + kDrain, 0, kPolls);
+      }
+      __syncwarp();
+    }
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// Joins the splits of a row: a warp per row, four channels per lane.
+__global__ void __launch_bounds__(256) prefill_join_kernel(PrefillFp8Args a) {
   const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int i = (int)(item / a.Hq), hq = (int)(item - (long long)i * a.Hq);
-  if (i >= m) return;
+  const int lane = threadIdx.x & 31;
+  const int hq = (int)(item % a.Hq);
+  const long long t = item / a.Hq;
+  const int s = (int)(t / a.max_q), i = (int)(t % a.max_q);
+  if (s >= a.n_seqs) return;
+  const int c0 = a.cu[s], m = a.cu[s + 1] - c0;
+  if (m > a.max_q || i >= m) return;
+  const float* part = static_cast<const float*>(a.c.ws) + (size_t)item * a.n_split * 132;
+  const float mine = lane < a.n_split ? part[(size_t)lane * 132] : -INFINITY;
+  const bool nan = __any_sync(0xffffffffu, isnan(mine));
+  const float top = warp_max_xor(mine, 1);
+  const float wt = mine == -INFINITY ? 0.f : expf(mine - top);
+  const float sum = warp_sum_xor(wt, 1);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < a.n_split; ++k) {
+    const float f = __shfl_sync(0xffffffffu, wt, k);
+    if (__shfl_sync(0xffffffffu, mine, k) == -INFINITY) continue;   // saw no key
+    const float4 p = *reinterpret_cast<const float4*>(part + (size_t)k * 132 + 4 + 4 * lane);
+    acc.x = fmaf(f, p.x, acc.x);
+    acc.y = fmaf(f, p.y, acc.y);
+    acc.z = fmaf(f, p.z, acc.z);
+    acc.w = fmaf(f, p.w, acc.w);
+  }
+  const float r = sum == 0.f ? 0.f : 1.f / sum;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * r, acc.y * r), hi = __floats2bfloat162_rn(acc.z * r, acc.w * r);
   const size_t row = ((size_t)c0 + i) * a.Hq + hq;
-  attend_row(a.L, a.c.pt + (size_t)s * a.c.max_pages, a.c.max_pages, hq / a.G,
-             static_cast<const uint16_t*>(a.c.q) + row * 128, n - m + i, a.c.window, a.c.n_sink, a.c.scale,
-             static_cast<uint16_t*>(a.c.out) + row * 128, a.c.lse ? a.c.lse + row : nullptr, a.err, lane);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.c.out) + row * 128 + 4 * lane) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  if (a.c.lse && lane == 0)
+    a.c.lse[row] = nan ? __uint_as_float(0x7FC00000u) : (sum == 0.f ? -INFINITY : top + logf(sum));
+}
+
+long long q_blocks(const Pool& p, int max_q) { return ((long long)max_q * p.G + 2 * kRows - 1) / (2 * kRows); }
+
+// Splits of the keys: where the blocks of rows fill less than half of the SMs,
+// as many as fit in one wave, of at least four tiles each.
+int splits(const Pool& p, int n_seqs, int max_q, long long max_len, int window, int n_sink) {
+  long long keys = max_len;
+  if (window) keys = std::min(keys, (long long)window + n_sink + std::min<long long>(max_q, 2 * kRows / p.G) + 2 * kKeys);
+  const long long tiles = (keys + kKeys - 1) / kKeys, blocks = q_blocks(p, max_q) * n_seqs * p.cfg.num_kv_heads;
+  if (blocks == 0) return 1;
+  return (int)std::max(1ll, std::min<long long>({p.sm_count / blocks, tiles / 4, kMaxSplits}));
 }
 
 }  // namespace
 
-size_t prefill_fp8_workspace(const Pool& p, int n_seqs, int max_q, int max_len) { return 16; }
+size_t prefill_fp8_workspace(const Pool& p, int n_seqs, int max_q, int max_len) {
+  const int n = splits(p, n_seqs, max_q, max_len, 0, 0);
+  return n == 1 ? 16 : (size_t)n_seqs * max_q * p.cfg.num_q_heads * n * 132 * sizeof(float);
+}
 
 cudaError_t launch_prefill_fp8(const Pool& p, const Fp8Store& f, int layer, int n_seqs, const int32_t* cu_q,
                                int max_q, const AttnCall& c, cudaStream_t s) {
   if (max_q == 0) return cudaSuccess;
-  PrefillFp8Args a{fp8_layer(p, f, layer), c, cu_q, max_q, p.cfg.num_q_heads, p.G, p.err};
-  prefill_fp8_kernel<<<dim3((unsigned)(((long long)max_q * a.Hq + 7) / 8), n_seqs), 256, 0, s>>>(a);
+  PrefillFp8Args a{fp8_layer(p, f, layer), c, cu_q, n_seqs, max_q, p.cfg.num_q_heads, p.G,
+                   splits(p, n_seqs, max_q, c.max_len, c.window, c.n_sink), (int)q_blocks(p, max_q), p.err,
+                   p.test_wait_polls > 0 ? p.test_wait_polls : kPolls};
+  const long long ctas = (long long)a.q_blocks * n_seqs * a.L.Hkv * a.n_split;
+  if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(prefill_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return e;
+  prefill_fp8_kernel<<<(unsigned)ctas, kThreads, kSmem, s>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.n_split == 1) return e;
+  prefill_join_kernel<<<(unsigned)(((long long)n_seqs * max_q * a.Hq + 7) / 8), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 
