@@ -21,7 +21,7 @@
 //   warps 8-11       converters: codes from global memory to registers (loads
 //                    of the next operand in flight), fp16 in the swizzled
 //                    operand layout to shared memory (two stages each of K, V)
-//   warp 12          issues the products: S = Q K^T from shared memory, O += P V
+//   warp 12          (13-15 idle) issues the products: S = Q K^T from shared memory, O += P V
 //                    with P from tensor memory and V token-major as it is stored
 // Tensor memory: S0, S1 (P over them), O0, O1, 128 columns each.
 // Hidden keys: a tile that some row sees only in part is masked by select after
@@ -42,7 +42,10 @@ namespace {
 constexpr int kRows = 128;                     // rows of a tile (M of a product)
 constexpr int kKeys = 128;                     // keys of a tile
 constexpr int kBlocks = kKeys / kTile;
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 16 * 32;              // four warpgroups
+// registers per thread of the softmax, converter and issuer warpgroups: they
+// share the launch's 128 each (2 * 184 + 104 + 40 = 4 * 128)
+constexpr int kSoftRegs = 184, kConvRegs = 104, kIssueRegs = 40;
 constexpr int kPolls = 1 << 20;
 constexpr int kMaxSplits = 32;
 constexpr float kNoRef = -3e38f;
@@ -121,27 +124,33 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-__device__ __forceinline__ void ld32(uint32_t t, float (&v)[32]) {
-  uint32_t u[32];
+#define KV_TIE8(v, i) \
+  "+f"((v)[i]), "+f"((v)[i + 1]), "+f"((v)[i + 2]), "+f"((v)[i + 3]), "+f"((v)[i + 4]), "+f"((v)[i + 5]), \
+      "+f"((v)[i + 6]), "+f"((v)[i + 7])
+// 32 columns of this thread's row; the values are there after settle()
+__device__ __forceinline__ void ld32(uint32_t t, float* v) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
       "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
-        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
-        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
-        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(t)
       : "memory");
-  wait_ld();
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+}
+// no use of the values moves above the wait
+__device__ __forceinline__ void settle(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : KV_TIE8(v, 0), KV_TIE8(v, 8), KV_TIE8(v, 16), KV_TIE8(v, 24)
+               :
+               : "memory");
 }
 __device__ __forceinline__ void st16(uint32_t t, const uint32_t (&u)[16]) {
   asm volatile(
@@ -150,15 +159,30 @@ __device__ __forceinline__ void st16(uint32_t t, const uint32_t (&u)[16]) {
       "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
       : "memory");
 }
-__device__ __forceinline__ void st32(uint32_t t, const float (&v)[32]) {
-  uint32_t a[16], b[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    a[i] = __float_as_uint(v[i]);
-    b[i] = __float_as_uint(v[16 + i]);
-  }
-  st16(t, a);
-  st16(t + 16, b);
+// Pairs of fp32 values in one register pair: one instruction for both, each
+// rounded as the scalar one.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_split(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t cvt_lo(uint32_t w) {   // codes in bytes 0, 1 -> fp16x2
@@ -242,10 +266,6 @@ struct Waiter {
 
 // ---- converters (128 threads) -------------------------------------------------
 
-struct Block16 {                               // eight pieces of one operand: piece `tid` of each 16-token block
-  uint4 w[kBlocks];
-};
-
 __device__ __forceinline__ void store_run(uint8_t* operand, int token, int run, const uint4& w, uint32_t mul,
                                           bool swap) {
   uint32_t f[8];
@@ -315,93 +335,103 @@ __device__ __forceinline__ void convert_tiles(const PrefillFp8Args& a, const Wor
     st = ((long long)pid * a.L.Hkv + w.h) * tpp + (t & (tpp - 1));
     e = *reinterpret_cast<const uint16_t*>(a.L.exps + st * 2);
   };
-  long long st;
-  int ex;
-  find(w.i0, st, ex);
-  int it = 0;
-  bool ok = true;
-  for (int i = w.i0; i < w.i1; ++i) {
-    const int t0 = w.tile(i) * kKeys;
-    uint32_t left = __ballot_sync(0xffffffffu, st >= 0);
+  // The walk over the passes: a tile's blocks whose exponents lie within 7 of
+  // the first one left make a pass.  Lanes hold the blocks of tile i and, read
+  // ahead, of tile i + 1.
+  int i = w.i0 - 1, ex = 0, ex_next;
+  long long st = -1, st_next;
+  uint32_t left = 0;
+  find(w.i0, st_next, ex_next);
+  // the pass in hand: first key, blocks, operand exponents, per-lane exponents below them
+  int t0 = 0, mk = 0, mv = 0, dk = 0, dv = 0;
+  uint32_t now = 0;
+  auto advance = [&]() -> bool {
+    if (!left) {
+      if (++i >= w.i1) return false;
+      st = st_next;
+      ex = ex_next;
+      find(i + 1, st_next, ex_next);
+      left = __ballot_sync(0xffffffffu, st >= 0);
+      t0 = w.tile(i) * kKeys;
+    }
     const int ek = (int8_t)(ex & 0xFF), ev = (int8_t)(ex >> 8);
-    long long st_next;
-    int ex_next;
-    find(i + 1, st_next, ex_next);
-    bool first = true;
-    while (first || left) {
-      first = false;
-      // the blocks of this pass: exponents within 7 of the first one left
-      uint32_t now = 0;
-      int mk = 0, mv = 0;
-      if (left) {
-        const int u0 = __ffs(left) - 1;
-        const int k0 = __shfl_sync(0xffffffffu, ek, u0), v0 = __shfl_sync(0xffffffffu, ev, u0);
-        const bool in = ((left >> lane) & 1) && abs(ek - k0) <= 7 && abs(ev - v0) <= 7;
-        now = __ballot_sync(0xffffffffu, in);
-        mk = __reduce_max_sync(0xffffffffu, in ? ek : -1000);
-        mv = __reduce_max_sync(0xffffffffu, in ? ev : -1000);
-        left &= ~now;
-      }
-      const bool partial = now != 0xFFu || t0 + kKeys - 1 > firstpos ||
-                           (a.c.window && t0 <= lastpos - a.c.window && t0 + kKeys > w.sinks);
-      const int stage = it & 1;
-      const uint32_t ph = ((it >> 1) & 1) ^ 1;   // of the empty barriers: the use before this one
-      TileInfo& info = sh->info[it & 3];
-      Block16 k, v;
+    now = 0;
+    mk = mv = 0;
+    if (left) {
+      const int u0 = __ffs(left) - 1;
+      const int k0 = __shfl_sync(0xffffffffu, ek, u0), v0 = __shfl_sync(0xffffffffu, ev, u0);
+      const bool in = ((left >> lane) & 1) && abs(ek - k0) <= 7 && abs(ev - v0) <= 7;
+      now = __ballot_sync(0xffffffffu, in);
+      mk = __reduce_max_sync(0xffffffffu, in ? ek : -1000);
+      mv = __reduce_max_sync(0xffffffffu, in ? ev : -1000);
+      left &= ~now;
+    }
+    dk = ek - mk;
+    dv = ev - mv;
+    return true;
+  };
+  uint4 k[kBlocks], v[kBlocks];                // piece `tid` of each block
+  auto load = [&](uint4 (&x)[kBlocks], int operand) {
 #pragma unroll
-      for (int u = 0; u < kBlocks; ++u) {
-        const long long s = __shfl_sync(0xffffffffu, st, u);
-        k.w[u] = v.w[u] = make_uint4(0, 0, 0, 0);
-        if ((now >> u) & 1) {
-          const uint8_t* p = a.L.codes + s * kFp8TileBytes + tid * 16;
-          k.w[u] = ld_stream_v4(p);
-          v.w[u] = ld_stream_v4(p + 2048);
-        }
-      }
-      if (ok && it >= 2) ok = wait(sh->bars + kKEmpty + stage, ph);
-      if (tid == 0) {
-        info.t0 = t0;
-        info.blocks = now;
-        info.fk = pow2i(max(min(mk, 127), -126));
-        info.ev = (float)mv;
-        info.last = i + 1 == w.i1 && !left;
-        info.partial = partial;
+    for (int u = 0; u < kBlocks; ++u) {
+      const long long s = __shfl_sync(0xffffffffu, st, u);
+      x[u] = make_uint4(0, 0, 0, 0);
+      if ((now >> u) & 1) x[u] = ld_stream_v4(a.L.codes + s * kFp8TileBytes + operand * 2048 + tid * 16);
+    }
+  };
+  bool more = advance(), ok = true;
+  load(k, 0);
+  load(v, 1);
+  for (int it = 0; more; ++it) {
+    const int stage = it & 1;
+    const uint32_t ph = ((it >> 1) & 1) ^ 1;   // of the empty barriers: the use before this one
+    TileInfo& info = sh->info[it & 3];
+    const int t0c = t0;
+    const bool partial = now != 0xFFu || t0 + kKeys - 1 > firstpos ||
+                         (a.c.window && t0 <= lastpos - a.c.window && t0 + kKeys > w.sinks);
+    const uint32_t nowc = now, mulk = half_pow2(dk), mulv = half_pow2(dv);
+    const int mkc = mk, mvc = mv;
+    more = advance();                          // the next pass's blocks are known from here
+    if (ok && it >= 2) ok = wait(sh->bars + kKEmpty + stage, ph);
+    if (tid == 0) {
+      info.t0 = t0c;
+      info.blocks = nowc;
+      info.fk = pow2i(max(min(mkc, 127), -126));
+      info.ev = (float)mvc;
+      info.last = !more;
+      info.partial = partial;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) info.nan[q] = 0;
-      }
-      if (!converters_and(ok)) return;         // the record is in place; all four warps go on, or none
-      uint8_t* sk = sm + kOffK + stage * kOperand;
+      for (int q = 0; q < 4; ++q) info.nan[q] = 0;
+    }
+    if (!converters_and(ok)) return;           // the record is in place; all four warps go on, or none
+    uint8_t* sk = sm + kOffK + stage * kOperand;
 #pragma unroll
-      for (int u = 0; u < kBlocks; ++u) {
-        const uint32_t m = __shfl_sync(0xffffffffu, half_pow2(ek - mk), u);
-        store_run(sk, kTile * u + ktok, krun, k.w[u], m, false);
-      }
-      fence_async();
-      arrive(sh->bars + kKFull + stage);
-      if (it >= 2) ok = wait(sh->bars + kVEmpty + stage, ph);
-      ok = __all_sync(0xffffffffu, ok);        // a failure ends the next pass, for all four warps
+    for (int u = 0; u < kBlocks; ++u)
+      store_run(sk, kTile * u + ktok, krun, k[u], __shfl_sync(0xffffffffu, mulk, u), false);
+    fence_async();
+    arrive(sh->bars + kKFull + stage);
+    if (more) load(k, 0);
+    if (it >= 2) ok = wait(sh->bars + kVEmpty + stage, ph);
+    ok = __all_sync(0xffffffffu, ok);          // a failure ends the next pass, for all four warps
+    if (ok) {                                  // else products may still read the stage
       uint8_t* sv = sm + kOffV + stage * kOperand;
 #pragma unroll
       for (int u = 0; u < kBlocks; ++u) {
-        if (!ok) break;                        // products may still read the stage
-        const uint32_t m = __shfl_sync(0xffffffffu, half_pow2(ev - mv), u);
         const int tok = kTile * u + vtok;
         if (partial) {
-          uint4& x = v.w[u];
-          if (t0 + tok >= keys) x = make_uint4(0, 0, 0, 0);
+          uint4& x = v[u];
+          if (t0c + tok >= keys) x = make_uint4(0, 0, 0, 0);
           if (has_nan(x.x) || has_nan(x.y) || has_nan(x.z) || has_nan(x.w)) {
             x = make_uint4(0, 0, 0, 0);
             atomicOr(&info.nan[tok >> 5], 1u << (tok & 31));
           }
         }
-        store_run(sv, tok, vrun, v.w[u], m, (vrun & 1) != 0);
+        store_run(sv, tok, vrun, v[u], __shfl_sync(0xffffffffu, mulv, u), (vrun & 1) != 0);
       }
       fence_async();
-      if (ok) arrive(sh->bars + kVFull + stage);
-      ++it;
+      arrive(sh->bars + kVFull + stage);
     }
-    st = st_next;
-    ex = ex_next;
+    if (more) load(v, 1);
   }
 }
 
@@ -429,7 +459,6 @@ __device__ __forceinline__ void issue_products(uint32_t tmem, uint8_t* sm, Share
     const uint32_t ph = (it >> 1) & 1;
     const bool last = sh->info[it & 3].last != 0;
     if (!wait(sh->bars + kVFull + stage, ph)) return;
-    if (!last && !wait(sh->bars + kKFull + (stage ^ 1), ((it + 1) >> 1) & 1)) return;
     const uint64_t v = desc(base + kOffV + stage * kOperand, kOperand / 2);
 #pragma unroll
     for (int tile = 0; tile < 2; ++tile) {
@@ -439,7 +468,9 @@ __device__ __forceinline__ void issue_products(uint32_t tmem, uint8_t* sm, Share
       for (int ks = 0; ks < 8; ++ks)           // 16 tokens: 8 columns of P, 16 rows of V
         mma_ts(tmem + 256 + 128 * tile, tmem + 128 * tile + 8 * ks, v + ((ks * 2048) >> 4), it > 0 || ks > 0);
       if (tile == 1) commit(sh->bars + kVEmpty + stage);
-      if (!last) scores(tile, stage ^ 1);
+      if (last) continue;
+      if (tile == 0 && !wait(sh->bars + kKFull + (stage ^ 1), ((it + 1) >> 1) & 1)) return;
+      scores(tile, stage ^ 1);
     }
     if (last) break;
     commit(sh->bars + kKEmpty + (stage ^ 1));
@@ -470,7 +501,11 @@ __device__ __forceinline__ bool softmax_rows(const PrefillFp8Args& a, const Work
       for (int q = 0; q < 4; ++q) ro.poison |= (old.nan[q] & see[q]) != 0;
     }
     const bool partial = info.partial != 0, last = info.last != 0;
-    const float c = cs * info.fk, ev = info.ev;
+    // above 0, so that a hidden key's -inf stays one
+    const float c = fmaxf(cs * info.fk, 1.17549435e-38f), ev = info.ev;
+    float v[kKeys];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) ld32(ts + 32 * q, v + 32 * q);
     if (partial) {
       const int t0 = info.t0;
       const uint32_t blocks = info.blocks;
@@ -483,18 +518,21 @@ __device__ __forceinline__ bool softmax_rows(const PrefillFp8Args& a, const Work
       }
     }
     check = partial;
-    float top = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) settle(v + 32 * q);
+    if (partial) {
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i)
+        if (!((see[i >> 5] >> (i & 31)) & 1)) v[i] = -INFINITY;
+    }
+    float top[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      float v[32];
-      ld32(ts + 32 * q, v);
+      top[q] = fmaxf(v[32 * q], v[32 * q + 1]);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        if (partial && !((see[q] >> i) & 1)) v[i] = -INFINITY;
-        top = fmaxf(top, v[i]);
-      }
+      for (int i = 2; i < 32; i += 2) top[q] = max3(top[q], v[32 * q + i], v[32 * q + i + 1]);
     }
-    const float x = top == -INFINITY ? -INFINITY : fmaf(top, c, ev);
+    const float x = fmaf(max3(fmaxf(top[0], top[1]), top[2], top[3]), c, ev);
     const bool raise = x > ro.M + kRaise;
     if (__any_sync(0xffffffffu, raise)) {
       const float n = raise ? x - kHead : ro.M;
@@ -502,36 +540,44 @@ __device__ __forceinline__ bool softmax_rows(const PrefillFp8Args& a, const Work
       ro.M = n;
       ro.l *= f;
       if (it > 0) {                            // the products so far are complete: S of this tile came after them
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < 4; ++q) {
-          float v[32];
-          ld32(to + 32 * q, v);
+          float o[32];
+          ld32(to + 32 * q, o);
+          settle(o);
+          uint32_t u[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] *= f;
-          st32(to + 32 * q, v);
+          for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i] * f);
+          st16(to + 32 * q, u);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[16 + i] * f);
+          st16(to + 32 * q + 16, u);
         }
       }
     }
     const float d = ev - ro.M;
-    float sum = 0.f;
+    const uint64_t c2 = f2(c, c), d2 = f2(d, d);
+    uint64_t s0 = f2(0.f, 0.f), s1 = s0;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      float v[32];
-      ld32(ts + 32 * q, v);
       uint32_t p[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        float y0 = exp2_neg(fmaf(v[2 * i], c, d)), y1 = exp2_neg(fmaf(v[2 * i + 1], c, d));
-        if (partial) {
-          if (!((see[q] >> (2 * i)) & 1)) y0 = 0.f;
-          if (!((see[q] >> (2 * i + 1)) & 1)) y1 = 0.f;
-        }
-        sum += y0 + y1;
+        float y0, y1;
+        f2_split(f2_fma(f2(v[32 * q + 2 * i], v[32 * q + 2 * i + 1]), c2, d2), y0, y1);
+        y0 = exp2_neg(y0);
+        y1 = exp2_neg(y1);
+        if (i & 1)
+          s1 = f2_add(s1, f2(y0, y1));
+        else
+          s0 = f2_add(s0, f2(y0, y1));
         p[i] = pack_f16(y0, y1);
       }
       st16(ts + 16 * q, p);
     }
-    ro.l = fmaf(sum, exp2f(-ev), ro.l);
+    float sa, sb;
+    f2_split(f2_add(s0, s1), sa, sb);
+    ro.l = fmaf(sa + sb, exp2f(-ev), ro.l);
     wait_st();
     fence_before();
     arrive(sh->bars + kPFull + tile);
@@ -620,11 +666,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
   bool ok = true;
   if (any) {
     if (warp < 8) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
       ok = softmax_rows(a, w, tmem + ((uint32_t)(32 * (warp & 3)) << 16), tile, pos, cs, sh, wait, ro);
     } else if (warp < 12) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
       convert_tiles(a, w, sm, sh, wait);
-    } else if (lane == 0) {
-      issue_products(tmem, sm, sh, wait);
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+      if (warp == 12 && lane == 0) issue_products(tmem, sm, sh, wait);
     }
     __syncwarp();
   }
@@ -643,6 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
       __syncwarp();
       if (any && ok) {                         // the same for the whole warp
         ld32(to + 32 * q, v);
+        settle(v);
       } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = 0.f;
