@@ -18,11 +18,13 @@
 // one in the tensor cores while the other is in the softmax.
 //   warps 0-3, 4-7   softmax of a tile: a thread owns a row; S is read from
 //                    tensor memory, the weights go back over it as fp16
-//   warps 8-11       converters: codes from global memory to registers (loads
-//                    of the next operand in flight), fp16 in the swizzled
-//                    operand layout to shared memory (two stages each of K, V)
-//   warp 12          (13-15 idle) issues the products: S = Q K^T from shared memory, O += P V
+//   warps 8-11       converters: codes from global memory to registers a tile
+//                    ahead, fp16 in the swizzled operand layout to shared memory
+//                    (two stages each of K and V)
+//   warp 12          issues the products: S = Q K^T from shared memory, O += P V
 //                    with P from tensor memory and V token-major as it is stored
+//   warp 13          (14, 15 idle) walks the key tiles ahead of the converters:
+//                    page ids, exponents, block addresses into a ring of records
 // Tensor memory: S0, S1 (P over them), O0, O1, 128 columns each.
 // Hidden keys: a tile that some row sees only in part is masked by select after
 // the product (a NaN in a hidden K row never enters), its V rows that hold NaN
@@ -44,8 +46,9 @@ constexpr int kKeys = 128;                     // keys of a tile
 constexpr int kBlocks = kKeys / kTile;
 constexpr int kThreads = 16 * 32;              // four warpgroups
 // registers per thread of the softmax, converter and issuer warpgroups: they
-// share the launch's 128 each (2 * 184 + 104 + 40 = 4 * 128)
-constexpr int kSoftRegs = 184, kConvRegs = 104, kIssueRegs = 40;
+// share the launch's 128 each
+constexpr int kSoftRegs = 176, kConvRegs = 120, kIssueRegs = 40;
+static_assert(2 * kSoftRegs + kConvRegs + kIssueRegs <= 4 * 128, "setmaxnreg.inc draws on the launch's registers");
 constexpr int kPolls = 1 << 20;
 constexpr int kMaxSplits = 32;
 constexpr float kNoRef = -3e38f;
@@ -58,24 +61,38 @@ constexpr uint32_t kOffK = 2 * kOperand;       // two stages
 constexpr uint32_t kOffV = 4 * kOperand;       // two stages
 constexpr uint32_t kOffInfo = 6 * kOperand;
 
-// What a key tile's converters tell the other warps; a ring of four.
-struct TileInfo {
+// A pass over a key tile: what the walker tells the other warps; a ring of eight.
+struct Pass {
   int t0;                                      // first key
   uint32_t blocks;                             // 16-token blocks present in this pass
   float fk, ev;                                // 2^eK, eV of the operands
-  int last;                                    // no tile follows
-  int partial;                                 // V rows with NaN were zeroed and listed
-  uint32_t nan[4];                             // those rows
+  int last;                                    // no pass follows
+  int partial;                                 // some row sees the tile only in part
   int pad[2];
+  uint32_t nan[4];                             // its V rows that hold NaN, zeroed (by the converters)
+  int tile[kBlocks];                           // stored tile of each block (0 for an absent one)
+  uint32_t mulk[kBlocks], mulv[kBlocks];       // fp16x2 2^(e - eK), 2^(e - eV)
+};
+constexpr int kRing = 8;
+
+enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kOFull = 12, kDrain = 13, kPass = 14, kBars = 14 + kRing };
+
+// The rows of a CTA and the key tiles they see.
+struct Work {
+  int s, h, c0, m, n, row0, split;             // sequence, KV head, first q row, queries, keys, first row of the block
+  int pos0;                                    // position of the sequence's query 0
+  int first, keys;                             // position of the first row; keys from here on are hidden from every row
+  int low, sinks, ns, w0, i0, i1;              // tile list: the first ns tiles, then from w0; this split's part of it
+  __device__ __forceinline__ int tile(int i) const { return i < ns ? i : i - ns + w0; }
 };
 
-enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kOFull = 12, kDrain = 13, kBars = 14 };
-
 struct Shared {
-  TileInfo info[4];
+  Pass pass[kRing];
+  Work work;                                   // for the warps with few registers
   uint64_t bars[kBars];
   uint32_t tmem;
   int abort;
+  int converted;                               // passes whose K is in shared memory
 };
 constexpr uint32_t kSmem = kOffInfo + sizeof(Shared) + 1024;
 
@@ -204,14 +221,6 @@ __device__ __forceinline__ uint32_t below(int x, int from) {
   return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
 }
 
-// The rows of a CTA and the key tiles they see.
-struct Work {
-  int s, h, c0, m, n, row0, split;             // sequence, KV head, first q row, queries, keys, first row of the block
-  int pos0;                                    // position of the sequence's query 0
-  int low, sinks, ns, w0, i0, i1;              // tile list: the first ns tiles, then from w0; this split's part of it
-  __device__ __forceinline__ int tile(int i) const { return i < ns ? i : i - ns + w0; }
-};
-
 __device__ __forceinline__ bool find_work(const PrefillFp8Args& a, Work& w) {
   // blocks of a sequence from its last (most keys) to its first
   int x = blockIdx.x;
@@ -239,6 +248,8 @@ __device__ __forceinline__ bool find_work(const PrefillFp8Args& a, Work& w) {
   const int p_lo = w.pos0 + w.row0 / a.G, p_hi = w.pos0 + min((w.row0 + 2 * kRows) / a.G, w.m) - 1;
   w.low = a.c.window ? max(p_lo - a.c.window + 1, 0) : 0;
   const int end = max(p_hi + 1, 0);
+  w.first = p_lo;
+  w.keys = end;
   w.sinks = a.c.window ? a.c.n_sink : 0;
   w.w0 = min(w.low, end) / kKeys;
   w.ns = min((min(w.sinks, end) + kKeys - 1) / kKeys, w.w0);
@@ -266,8 +277,7 @@ struct Waiter {
 
 // ---- converters (128 threads) -------------------------------------------------
 
-__device__ __forceinline__ void store_run(uint8_t* operand, int token, int run, const uint4& w, uint32_t mul,
-                                          bool swap) {
+__device__ __forceinline__ void store_run(uint8_t* operand, int token, int run, const uint4& w, uint32_t mul) {
   uint32_t f[8];
   const uint32_t x[4] = {w.x, w.y, w.z, w.w};
   const __half2 m = u32_as_h2(mul);
@@ -278,16 +288,8 @@ __device__ __forceinline__ void store_run(uint8_t* operand, int token, int run, 
   }
   uint8_t* row = operand + (run >> 2) * (kOperand / 2) + token * 128;
   const int c = 2 * (run & 3), sw = token & 7;
-  uint4* p0 = reinterpret_cast<uint4*>(row + ((c ^ sw) << 4));
-  uint4* p1 = reinterpret_cast<uint4*>(row + (((c + 1) ^ sw) << 4));
-  const uint4 v0 = make_uint4(f[0], f[1], f[2], f[3]), v1 = make_uint4(f[4], f[5], f[6], f[7]);
-  if (!swap) {
-    *p0 = v0;
-    *p1 = v1;
-  } else {                                     // the other order: the lanes of a phase hit different banks
-    *p1 = v1;
-    *p0 = v0;
-  }
+  *reinterpret_cast<uint4*>(row + ((c ^ sw) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
+  *reinterpret_cast<uint4*>(row + (((c + 1) ^ sw) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
 }
 
 // 2^d, d <= 0 (0 below fp16's range), in both halves
@@ -295,143 +297,161 @@ __device__ __forceinline__ uint32_t half_pow2(int d) {
   return h2_as_u32(__float2half2_rn(pow2i(max(min(d, 0), -126))));
 }
 
-// Whether `ok` holds for all 128 converter threads (a barrier for them).
-__device__ __forceinline__ bool converters_and(bool ok) {
-  int r;
-  asm volatile(
-      "{ .reg .pred p, q; setp.ne.b32 p, %1, 0; bar.red.and.pred q, 1, 128, p; selp.b32 %0, 1, 0, q; }"
-      : "=r"(r)
-      : "r"((int)ok)
-      : "memory");
-  return r != 0;
-}
-
 __device__ __forceinline__ bool has_nan(uint32_t w) { return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0; }
 
-__device__ __forceinline__ void convert_tiles(const PrefillFp8Args& a, const Work& w, uint8_t* sm, Shared* sh,
+// K and V of every pass.
+__device__ __forceinline__ void convert_tiles(const PrefillFp8Args& a, int keys, uint8_t* sm, Shared* sh,
                                               const Waiter& wait) {
-  const int tid = threadIdx.x - 256, lane = tid & 31;
-  const int tpp = a.L.P / kTile, shift = tpp >> 1;
-  const int32_t* pt = a.c.pt + (size_t)w.s * a.c.max_pages;
-  const int lastpos = w.pos0 + min((w.row0 + 2 * kRows) / a.G, w.m) - 1, firstpos = w.pos0 + w.row0 / a.G;
-  const int keys = max(lastpos + 1, 0);        // keys behind it are hidden from every row
-  // piece `tid` of a stored K and V block: its token and run of 16 channels
+  const int tid = threadIdx.x & 127;
+  // this thread's piece of a stored block of K and of V: token and run of 16
+  // channels, chosen so that eight lanes store to eight different banks
   const int ktok = 8 * (tid >> 6) + ((tid >> 2) & 7), krun = 4 * ((tid >> 5) & 1) + (tid & 3);
-  const int vtok = 8 * (tid >> 6) + 2 * (tid & 3) + ((tid >> 5) & 1), vrun = (tid >> 2) & 7;
-
-  // lane u < 8: block u of tile i -> stored tile (or -1) and exponents
-  auto find = [&](int i, long long& st, int& e) {
-    st = -1;
-    e = 0;
-    if (i >= w.i1 || lane >= kBlocks) return;
-    const int t = w.tile(i) * kBlocks + lane, j0 = t * kTile;
-    // a block that no row sees is absent (its page may have been given up)
-    if (j0 >= keys || (a.c.window && j0 + kTile <= w.low && j0 >= w.sinks)) return;
-    const int pid = pt[t >> shift];
-    if (pid < 0 || pid >= a.L.num_pages) {
-      flag_error(a.err, KV_DEVERR_PAGE_ID);
-      return;
-    }
-    st = ((long long)pid * a.L.Hkv + w.h) * tpp + (t & (tpp - 1));
-    e = *reinterpret_cast<const uint16_t*>(a.L.exps + st * 2);
-  };
-  // The walk over the passes: a tile's blocks whose exponents lie within 7 of
-  // the first one left make a pass.  Lanes hold the blocks of tile i and, read
-  // ahead, of tile i + 1.
-  int i = w.i0 - 1, ex = 0, ex_next;
-  long long st = -1, st_next;
-  uint32_t left = 0;
-  find(w.i0, st_next, ex_next);
-  // the pass in hand: first key, blocks, operand exponents, per-lane exponents below them
-  int t0 = 0, mk = 0, mv = 0, dk = 0, dv = 0;
-  uint32_t now = 0;
-  auto advance = [&]() -> bool {
-    if (!left) {
-      if (++i >= w.i1) return false;
-      st = st_next;
-      ex = ex_next;
-      find(i + 1, st_next, ex_next);
-      left = __ballot_sync(0xffffffffu, st >= 0);
-      t0 = w.tile(i) * kKeys;
-    }
-    const int ek = (int8_t)(ex & 0xFF), ev = (int8_t)(ex >> 8);
-    now = 0;
-    mk = mv = 0;
-    if (left) {
-      const int u0 = __ffs(left) - 1;
-      const int k0 = __shfl_sync(0xffffffffu, ek, u0), v0 = __shfl_sync(0xffffffffu, ev, u0);
-      const bool in = ((left >> lane) & 1) && abs(ek - k0) <= 7 && abs(ev - v0) <= 7;
-      now = __ballot_sync(0xffffffffu, in);
-      mk = __reduce_max_sync(0xffffffffu, in ? ek : -1000);
-      mv = __reduce_max_sync(0xffffffffu, in ? ev : -1000);
-      left &= ~now;
-    }
-    dk = ek - mk;
-    dv = ev - mv;
-    return true;
-  };
-  uint4 k[kBlocks], v[kBlocks];                // piece `tid` of each block
-  auto load = [&](uint4 (&x)[kBlocks], int operand) {
+  const int vtok = 8 * (tid >> 6) + (tid & 7), vrun = (tid >> 3) & 7;
+  const uint8_t* ksrc = a.L.codes + tid * 16;
+  const uint8_t* vsrc = a.L.codes + 2048 + ((tid & 1) + 2 * (tid >> 6)) * 512 + vrun * 64 + ((tid & 7) >> 1) * 16;
+  uint4 k[kBlocks], v[kBlocks];                // a pass ahead
+  auto load = [&](uint4 (&x)[kBlocks], const uint8_t* src, const Pass& p) {
+    int t[kBlocks];
 #pragma unroll
-    for (int u = 0; u < kBlocks; ++u) {
-      const long long s = __shfl_sync(0xffffffffu, st, u);
-      x[u] = make_uint4(0, 0, 0, 0);
-      if ((now >> u) & 1) x[u] = ld_stream_v4(a.L.codes + s * kFp8TileBytes + operand * 2048 + tid * 16);
-    }
+    for (int u = 0; u < kBlocks; u += 4) *reinterpret_cast<int4*>(t + u) = *reinterpret_cast<const int4*>(p.tile + u);
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) x[u] = ld_stream_v4(src + (size_t)t[u] * kFp8TileBytes);
   };
-  bool more = advance(), ok = true;
-  load(k, 0);
-  load(v, 1);
-  for (int it = 0; more; ++it) {
+  auto ready = [&](int it) { return __all_sync(0xffffffffu, wait(sh->bars + kPass + (it & (kRing - 1)), (it / kRing) & 1)); };
+  if (!ready(0)) return;
+  load(k, ksrc, sh->pass[0]);
+  load(v, vsrc, sh->pass[0]);
+  for (int it = 0;; ++it) {
     const int stage = it & 1;
     const uint32_t ph = ((it >> 1) & 1) ^ 1;   // of the empty barriers: the use before this one
-    TileInfo& info = sh->info[it & 3];
-    const int t0c = t0;
-    const bool partial = now != 0xFFu || t0 + kKeys - 1 > firstpos ||
-                         (a.c.window && t0 <= lastpos - a.c.window && t0 + kKeys > w.sinks);
-    const uint32_t nowc = now, mulk = half_pow2(dk), mulv = half_pow2(dv);
-    const int mkc = mk, mvc = mv;
-    more = advance();                          // the next pass's blocks are known from here
-    if (ok && it >= 2) ok = wait(sh->bars + kKEmpty + stage, ph);
-    if (tid == 0) {
-      info.t0 = t0c;
-      info.blocks = nowc;
-      info.fk = pow2i(max(min(mkc, 127), -126));
-      info.ev = (float)mvc;
-      info.last = !more;
-      info.partial = partial;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) info.nan[q] = 0;
-    }
-    if (!converters_and(ok)) return;           // the record is in place; all four warps go on, or none
+    Pass& p = sh->pass[it & (kRing - 1)];
+    const Pass& next = sh->pass[(it + 1) & (kRing - 1)];
+    const bool partial = p.partial != 0, last = p.last != 0;
+    const uint32_t present = p.blocks;
+    const int t0 = p.t0;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint32_t mul[kBlocks];
+    if (it >= 2 && !__all_sync(0xffffffffu, wait(sh->bars + kKEmpty + stage, ph))) return;
     uint8_t* sk = sm + kOffK + stage * kOperand;
 #pragma unroll
-    for (int u = 0; u < kBlocks; ++u)
-      store_run(sk, kTile * u + ktok, krun, k[u], __shfl_sync(0xffffffffu, mulk, u), false);
+    for (int u = 0; u < kBlocks; u += 4) *reinterpret_cast<uint4*>(mul + u) = *reinterpret_cast<const uint4*>(p.mulk + u);
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+      if (partial && !((present >> u) & 1)) k[u] = zero;
+      store_run(sk, kTile * u + ktok, krun, k[u], mul[u]);
+    }
     fence_async();
     arrive(sh->bars + kKFull + stage);
-    if (more) load(k, 0);
-    if (it >= 2) ok = wait(sh->bars + kVEmpty + stage, ph);
-    ok = __all_sync(0xffffffffu, ok);          // a failure ends the next pass, for all four warps
-    if (ok) {                                  // else products may still read the stage
-      uint8_t* sv = sm + kOffV + stage * kOperand;
+    if (tid == 0) *reinterpret_cast<volatile int*>(&sh->converted) = it + 1;
+    if (!last) {
+      if (!ready(it + 1)) return;
+      load(k, ksrc, next);
+    }
+    if (it >= 2 && !__all_sync(0xffffffffu, wait(sh->bars + kVEmpty + stage, ph))) return;
+    uint8_t* sv = sm + kOffV + stage * kOperand;
+#pragma unroll
+    for (int u = 0; u < kBlocks; u += 4) *reinterpret_cast<uint4*>(mul + u) = *reinterpret_cast<const uint4*>(p.mulv + u);
+    if (partial) {
 #pragma unroll
       for (int u = 0; u < kBlocks; ++u) {
         const int tok = kTile * u + vtok;
-        if (partial) {
-          uint4& x = v[u];
-          if (t0c + tok >= keys) x = make_uint4(0, 0, 0, 0);
-          if (has_nan(x.x) || has_nan(x.y) || has_nan(x.z) || has_nan(x.w)) {
-            x = make_uint4(0, 0, 0, 0);
-            atomicOr(&info.nan[tok >> 5], 1u << (tok & 31));
-          }
+        if (!((present >> u) & 1) || t0 + tok >= keys) v[u] = zero;
+        if (has_nan(v[u].x) || has_nan(v[u].y) || has_nan(v[u].z) || has_nan(v[u].w)) {
+          v[u] = zero;
+          atomicOr(&p.nan[tok >> 5], 1u << (tok & 31));
         }
-        store_run(sv, tok, vrun, v[u], __shfl_sync(0xffffffffu, mulv, u), (vrun & 1) != 0);
       }
-      fence_async();
-      arrive(sh->bars + kVFull + stage);
     }
-    if (more) load(v, 1);
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) store_run(sv, kTile * u + vtok, vrun, v[u], mul[u]);
+    fence_async();
+    arrive(sh->bars + kVFull + stage);
+    if (last) return;
+    load(v, vsrc, next);
+  }
+}
+
+// ---- walker (one warp) ----------------------------------------------------------
+
+// The passes: a tile's blocks whose exponents lie within 7 of the first one left
+// make a pass.  Lane u < 8 holds block u: its stored tile (-1: absent) and
+// exponents for tile i, its exponents in flight for tile i + 1, its page id in
+// flight for tile i + 2; no load waits where it is issued.
+__device__ __forceinline__ void walk_tiles(const PrefillFp8Args& a, const Work& w, Shared* sh, const Waiter& wait) {
+  const int lane = threadIdx.x & 31;
+  const int tpp = a.L.P / kTile, shift = tpp >> 1;
+  const int32_t* pt = a.c.pt + (size_t)w.s * a.c.max_pages;
+  auto seen = [&](int i) -> bool {             // by some row; a page that none sees may have been given up
+    const int j0 = (w.tile(i) * kBlocks + lane) * kTile;
+    return i < w.i1 && lane < kBlocks && j0 < w.keys && !(a.c.window && j0 + kTile <= w.low && j0 >= w.sinks);
+  };
+  auto page_of = [&](int i) -> int { return pt[seen(i) ? (w.tile(i) * kBlocks + lane) >> shift : 0]; };
+  auto stored = [&](int i, int pid) -> int {   // below 2^31: 4 KB each
+    if (!seen(i)) return -1;
+    if (pid < 0 || pid >= a.L.num_pages) {
+      flag_error(a.err, KV_DEVERR_PAGE_ID);
+      return -1;
+    }
+    return (pid * a.L.Hkv + w.h) * tpp + ((w.tile(i) * kBlocks + lane) & (tpp - 1));
+  };
+  auto exps_of = [&](int st) -> int { return *reinterpret_cast<const uint16_t*>(a.L.exps + (size_t)max(st, 0) * 2); };
+  int st1 = stored(w.i0, page_of(w.i0));
+  int ex1 = exps_of(st1), pid2 = page_of(w.i0 + 1);
+  int n = 0;                                   // passes written
+  for (int i = w.i0; i < w.i1; ++i) {
+    const int st = st1, ex = ex1, t0 = w.tile(i) * kKeys;
+    st1 = stored(i + 1, pid2);
+    ex1 = exps_of(st1);
+    pid2 = page_of(i + 2);
+    uint32_t left = __ballot_sync(0xffffffffu, st >= 0);
+    const int ek = (int8_t)(ex & 0xFF), ev = (int8_t)(ex >> 8);
+    do {
+      uint32_t now = 0;
+      int mk = 0, mv = 0;
+      if (left) {
+        const int first = __shfl_sync(0xffffffffu, ex, __ffs(left) - 1);
+        const bool in =
+            ((left >> lane) & 1) && abs(ek - (int8_t)(first & 0xFF)) <= 7 && abs(ev - (int8_t)(first >> 8)) <= 7;
+        now = __ballot_sync(0xffffffffu, in);
+        mk = __reduce_max_sync(0xffffffffu, in ? ek : -1000);
+        mv = __reduce_max_sync(0xffffffffu, in ? ev : -1000);
+        left &= ~now;
+      }
+      // the record of pass n - 8 was last read by the softmax of pass n - 7,
+      // over when K of pass n - 4 has its stage
+      bool ok = true;
+      for (int spin = 0; n >= kRing && *reinterpret_cast<volatile int*>(&sh->converted) < n - 3; ++spin) {
+        if (spin >= wait.polls || *reinterpret_cast<volatile int*>(wait.abort)) {
+          ok = false;
+          break;
+        }
+        __nanosleep(100);
+      }
+      if (!__all_sync(0xffffffffu, ok)) {
+        *reinterpret_cast<volatile int*>(wait.abort) = 1;
+        return;
+      }
+      Pass& p = sh->pass[n & (kRing - 1)];
+      if (lane < kBlocks) {
+        const bool in = (now >> lane) & 1;
+        p.tile[lane] = in ? st : 0;
+        p.mulk[lane] = half_pow2(ek - mk);
+        p.mulv[lane] = half_pow2(ev - mv);
+        if (lane < 4) p.nan[lane] = 0;
+      }
+      if (lane == 0) {
+        p.t0 = t0;
+        p.blocks = now;
+        p.fk = pow2i(max(min(mk, 127), -126));
+        p.ev = (float)mv;
+        p.last = i + 1 == w.i1 && !left;
+        p.partial = now != 0xFFu || t0 + kKeys - 1 > w.first ||
+                    (a.c.window && t0 < w.keys - a.c.window && t0 + kKeys > w.sinks);
+      }
+      __syncwarp();
+      if (lane == 0) arrive(sh->bars + kPass + (n & (kRing - 1)));
+      ++n;
+    } while (left);
   }
 }
 
@@ -457,10 +477,10 @@ __device__ __forceinline__ void issue_products(uint32_t tmem, uint8_t* sm, Share
   for (int it = 0;; ++it) {
     const int stage = it & 1;
     const uint32_t ph = (it >> 1) & 1;
-    const bool last = sh->info[it & 3].last != 0;
+    const bool last = sh->pass[it & (kRing - 1)].last != 0;
     if (!wait(sh->bars + kVFull + stage, ph)) return;
     const uint64_t v = desc(base + kOffV + stage * kOperand, kOperand / 2);
-#pragma unroll
+#pragma unroll 1
     for (int tile = 0; tile < 2; ++tile) {
       if (!wait(sh->bars + kPFull + tile, it & 1)) return;
       fence_after();
@@ -494,9 +514,9 @@ __device__ __forceinline__ bool softmax_rows(const PrefillFp8Args& a, const Work
   for (int it = 0;; ++it) {
     if (!__all_sync(0xffffffffu, wait(sh->bars + kSFull + tile, it & 1))) return false;
     fence_after();
-    const TileInfo& info = sh->info[it & 3];
+    const Pass& info = sh->pass[it & (kRing - 1)];
     if (check) {
-      const TileInfo& old = sh->info[(it - 1) & 3];
+      const Pass& old = sh->pass[(it - 1) & (kRing - 1)];
 #pragma unroll
       for (int q = 0; q < 4; ++q) ro.poison |= (old.nan[q] & see[q]) != 0;
     }
@@ -593,6 +613,55 @@ __device__ __forceinline__ bool softmax_rows(const PrefillFp8Args& a, const Work
   }
 }
 
+// A row's result: normalised to the output, or as a part of a split.
+__device__ __forceinline__ void write_row(const PrefillFp8Args& a, const Work& w, uint32_t to, bool any, bool ok, bool live,
+                                          int token, int hq, const RowOut& ro) {
+  const size_t qrow = ((size_t)w.c0 + token) * a.Hq + hq;
+  const bool empty = ro.l == 0.f;
+  const float f = !ok || ro.poison ? __uint_as_float(0x7FC00000u) : (empty ? 0.f : 1.f / ro.l);
+  const float lse = empty ? -INFINITY : (ro.M + log2f(ro.l)) * kLn2;
+  float* part = static_cast<float*>(a.c.ws) +
+                (((size_t)w.s * a.max_q + token) * a.Hq + hq) * a.n_split * 132 + (size_t)w.split * 132;
+  uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.c.out) + qrow * 128);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float v[32];
+    __syncwarp();
+    if (any && ok) {                         // the same for the whole warp
+      ld32(to + 32 * q, v);
+      settle(v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = empty ? 0.f : v[i] * f;
+    if (live && a.n_split > 1) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<float4*>(part + 4 + 32 * q + 4 * i) =
+            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else if (live) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 y = __floats2bfloat162_rn(v[8 * i + 2 * e], v[8 * i + 2 * e + 1]);
+          u[e] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+        out[4 * q + i] = make_uint4(u[0], u[1], u[2], u[3]);
+      }
+    }
+  }
+  if (live) {
+    if (a.n_split > 1)
+      part[0] = lse;
+    else if (a.c.lse)
+      a.c.lse[qrow] = lse;
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args a) {
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -611,8 +680,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
     }
     mbar_init(sh->bars + kOFull, 2);
     mbar_init(sh->bars + kDrain, 1);
+    for (int i = 0; i < kRing; ++i) mbar_init(sh->bars + kPass + i, 1);
     mbar_fence_init();
     sh->abort = 0;
+    sh->converted = 0;
+    sh->work = w;
   }
   const bool any = w.i0 < w.i1;                // this CTA has keys at all
   if (warp == 12 && any) {
@@ -662,69 +734,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
   const uint32_t tmem = any ? sh->tmem : 0;
   const Waiter wait{&sh->abort, a.polls};
   const int pos = w.pos0 + token;
-  RowOut ro;
-  bool ok = true;
-  if (any) {
+  if (!any) {
+    if (warp < 8) write_row(a, w, 0, false, true, live, token, hq, RowOut());
+    return;
+  }
+  {
     if (warp < 8) {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-      ok = softmax_rows(a, w, tmem + ((uint32_t)(32 * (warp & 3)) << 16), tile, pos, cs, sh, wait, ro);
+      const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+      RowOut ro;
+      const bool ok = softmax_rows(a, w, trow, tile, pos, cs, sh, wait, ro);
+      write_row(a, w, trow + 256 + 128 * tile, true, ok, live, token, hq, ro);
     } else if (warp < 12) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
-      convert_tiles(a, w, sm, sh, wait);
+      convert_tiles(a, sh->work.keys, sm, sh, wait);
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+      if (warp == 13) walk_tiles(a, sh->work, sh, wait);
       if (warp == 12 && lane == 0) issue_products(tmem, sm, sh, wait);
     }
     __syncwarp();
   }
-  // ---- results: a row per thread ----
-  if (warp < 8) {
-    const bool empty = ro.l == 0.f;
-    const float f = !ok || ro.poison ? __uint_as_float(0x7FC00000u) : (empty ? 0.f : 1.f / ro.l);
-    const float lse = empty ? -INFINITY : (ro.M + log2f(ro.l)) * kLn2;
-    const uint32_t to = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 256 + 128 * tile;
-    float* part = static_cast<float*>(a.c.ws) +
-                  (((size_t)w.s * a.max_q + token) * a.Hq + hq) * a.n_split * 132 + (size_t)w.split * 132;
-    uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.c.out) + qrow * 128);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float v[32];
-      __syncwarp();
-      if (any && ok) {                         // the same for the whole warp
-        ld32(to + 32 * q, v);
-        settle(v);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = empty ? 0.f : v[i] * f;
-      if (live && a.n_split > 1) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<float4*>(part + 4 + 32 * q + 4 * i) =
-              make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-      } else if (live) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t u[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 y = __floats2bfloat162_rn(v[8 * i + 2 * e], v[8 * i + 2 * e + 1]);
-            u[e] = *reinterpret_cast<const uint32_t*>(&y);
-          }
-          out[4 * q + i] = make_uint4(u[0], u[1], u[2], u[3]);
-        }
-      }
-    }
-    if (live) {
-      if (a.n_split > 1)
-        part[0] = lse;
-      else if (a.c.lse)
-        a.c.lse[qrow] = lse;
-    }
-  }
-  if (!any) return;
   fence_before();
   __syncthreads();
   fence_after();
