@@ -455,48 +455,76 @@ __device__ __forceinline__ void walk_tiles(const PrefillFp8Args& a, const Work& 
   }
 }
 
-// ---- product issuer (one thread) ----------------------------------------------
+// ---- product issuer (one warp) ----------------------------------------------------
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.b32 %0, 1, 0, p; }" : "=r"(r));
+  return r != 0;
+}
+
+// The whole warp runs this, in step, and one lane of it issues: addresses stay in
+// uniform registers.  The loops are not unrolled: the code of the other warps
+// passes through the same instruction cache, and a short loop stays in it.
 __device__ __forceinline__ void issue_products(uint32_t tmem, uint8_t* sm, Shared* sh, const Waiter& wait) {
   const uint32_t base = smem_u32(sm);
+  const uint64_t q0 = desc(base + kOffQ, 16), k0 = desc(base + kOffK, 16), v0 = desc(base + kOffV, kOperand / 2);
+  auto ready = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(sh->bars + bar, parity)) != 0; };
   auto scores = [&](int tile, int stage) {
-    const uint64_t q = desc(base + kOffQ + tile * kOperand, 16), k = desc(base + kOffK + stage * kOperand, 16);
+    if (elect_one()) {
+      uint64_t q = q0 + ((tile * kOperand) >> 4), k = k0 + ((stage * kOperand) >> 4);
+      const uint32_t d = tmem + 128 * tile;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
 #pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
-      const uint32_t off = ((ks >> 2) * (kOperand / 2) + (ks & 3) * 32) >> 4;
-      mma_ss(tmem + 128 * tile, q + off, k + off, ks > 0);
+        for (int ks = 0; ks < 4; ++ks) mma_ss(d, q + 2 * ks, k + 2 * ks, half | ks);
+        q += (kOperand / 2) >> 4;
+        k += (kOperand / 2) >> 4;
+      }
+      commit(sh->bars + kSFull + tile);
+      arrive(sh->bars + kSFull + tile);        // a release after this warp saw the tile's record
+      if (tile == 1) commit(sh->bars + kKEmpty + stage);
     }
-    commit(sh->bars + kSFull + tile);
-    arrive(sh->bars + kSFull + tile);          // a release after this thread saw the tile's record
+    __syncwarp();
   };
-  if (!wait(sh->bars + kKFull, 0)) return;
+  if (!ready(kKFull, 0)) return;
   fence_after();
   scores(0, 0);
   scores(1, 0);
-  commit(sh->bars + kKEmpty);
   for (int it = 0;; ++it) {
     const int stage = it & 1;
-    const uint32_t ph = (it >> 1) & 1;
     const bool last = sh->pass[it & (kRing - 1)].last != 0;
-    if (!wait(sh->bars + kVFull + stage, ph)) return;
-    const uint64_t v = desc(base + kOffV + stage * kOperand, kOperand / 2);
+    if (!ready(kVFull + stage, (it >> 1) & 1)) return;
 #pragma unroll 1
     for (int tile = 0; tile < 2; ++tile) {
-      if (!wait(sh->bars + kPFull + tile, it & 1)) return;
+      if (!ready(kPFull + tile, it & 1)) return;
       fence_after();
+      if (elect_one()) {
+        uint64_t v = v0 + ((stage * kOperand) >> 4);
+        uint32_t p = tmem + 128 * tile;
+        const uint32_t d = tmem + 256 + 128 * tile;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks)           // 16 tokens: 8 columns of P, 16 rows of V
-        mma_ts(tmem + 256 + 128 * tile, tmem + 128 * tile + 8 * ks, v + ((ks * 2048) >> 4), it > 0 || ks > 0);
-      if (tile == 1) commit(sh->bars + kVEmpty + stage);
+          for (int ks = 0; ks < 4; ++ks)       // 16 tokens: 8 columns of P, 16 rows of V
+            mma_ts(d, p + 8 * ks, v + ((ks * 2048) >> 4), it | half | ks);
+          p += 32;
+          v += (4 * 2048) >> 4;
+        }
+        if (tile == 1) commit(sh->bars + kVEmpty + stage);
+      }
+      __syncwarp();
       if (last) continue;
-      if (tile == 0 && !wait(sh->bars + kKFull + (stage ^ 1), ((it + 1) >> 1) & 1)) return;
+      if (tile == 0 && !ready(kKFull + (stage ^ 1), ((it + 1) >> 1) & 1)) return;
       scores(tile, stage ^ 1);
     }
     if (last) break;
-    commit(sh->bars + kKEmpty + (stage ^ 1));
   }
-  commit(sh->bars + kOFull);
-  arrive(sh->bars + kOFull);
+  if (elect_one()) {
+    commit(sh->bars + kOFull);
+    arrive(sh->bars + kOFull);
+  }
+  __syncwarp();
 }
 
 // ---- softmax (a thread owns a row) ---------------------------------------------
@@ -751,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
       if (warp == 13) walk_tiles(a, sh->work, sh, wait);
-      if (warp == 12 && lane == 0) issue_products(tmem, sm, sh, wait);
+      if (warp == 12) issue_products(__shfl_sync(0xffffffffu, tmem, 0), sm, sh, wait);
     }
     __syncwarp();
   }
@@ -760,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
   fence_after();
   if (warp == 12) {
     if (sh->abort) {                           // products may be in flight: wait (bounded) before giving back the memory
-      if (lane == 0) {
+      if (elect_one()) {                       // the lane that issued them
         flag_error(a.err, KV_DEVERR_TIMEOUT);
         commit(sh->bars + kDrain);
         mbar_wait(sh->bars + kDrain, 0, kPolls);
