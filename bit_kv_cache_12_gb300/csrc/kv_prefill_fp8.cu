@@ -265,13 +265,13 @@ struct Waiter {
   int polls;
   // whether the phase with `parity` completed; a wait that runs out ends every role
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-    if (mbar_wait(bar, parity, 64)) return true;
-    for (int i = 64; i < polls; i += 64) {
-      if (*reinterpret_cast<volatile int*>(abort)) return false;
-      if (mbar_wait(bar, parity, 64)) return true;
+    for (int i = 0; !mbar_wait(bar, parity, 1); ++i) {
+      if ((i & 63) == 63 && (i >= polls || *reinterpret_cast<volatile int*>(abort))) {
+        *reinterpret_cast<volatile int*>(abort) = 1;
+        return false;
+      }
     }
-    *reinterpret_cast<volatile int*>(abort) = 1;
-    return false;
+    return true;
   }
 };
 
