@@ -70,42 +70,54 @@ __device__ __forceinline__ void fill_table(float2* tab, const RopeParams& rp, co
   }
 }
 
-// 16 channels of a row (run c of 8) and, for the half style, the 16 channels
-// they are paired with.
+// 16 channels of a row (run c of 8).
 struct Run {
   uint32_t own[8];
-  uint32_t mate[8];
 };
+
+// read once by this kernel (and perhaps written by it: not the read-only path)
+__device__ __forceinline__ uint4 ld_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
 
 __device__ __forceinline__ void load_run(Run& r, const uint16_t* row, int c, bool live) {
   uint4 a = make_uint4(0, 0, 0, 0), b = a;
   if (live) {
-    const uint4* p = reinterpret_cast<const uint4*>(row + 16 * c);
-    a = p[0];
-    b = p[1];
+    a = ld_once(row + 16 * c);
+    b = ld_once(row + 16 * c + 8);
   }
   r.own[0] = a.x; r.own[1] = a.y; r.own[2] = a.z; r.own[3] = a.w;
   r.own[4] = b.x; r.own[5] = b.y; r.own[6] = b.z; r.own[7] = b.w;
 }
 
-// The paired run sits in another lane of the same row (lanes 8k .. 8k + 7).
-__device__ __forceinline__ void fetch_mate(Run& r, const RopeParams& rp, int lane) {
-  if (rp.interleaved || rp.rd == 0) return;
-  const int c = lane & 7, n = rp.rd >> 4, h = n >> 1;
-  const int m = c < h ? c + h : (c < n ? c - h : c);
-  const int src = (lane & 24) | m;
+// The run that channel run c is paired with (half style) sits in another lane of
+// the same row (lanes 8k .. 8k + 7).  It is fetched where it is used, twice for a
+// quantized tile: kept, it would cost 32 registers and a third of the warps.
+__device__ __forceinline__ int mate_lane(const RopeParams& rp, int lane) {
+  const int c = lane & 7, n = rp.rd >> 4, h = n >> 1;   // rotated runs, half of them
+  return (lane & 24) | (c < h ? c + h : (c < n ? c - h : c));
+}
+template <bool kPairs>
+__device__ __forceinline__ void fetch_mate(const Run& r, uint32_t (&mate)[8], int src) {
+  if (!kPairs) {                               // else the pair is in the run itself
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r.mate[i] = __shfl_sync(0xffffffffu, r.own[i], src);
+    for (int i = 0; i < 8; ++i) mate[i] = __shfl_sync(0xffffffffu, r.own[i], src);
+  }
 }
 
 // The rotated values of the run.
-__device__ __forceinline__ void rotate_run(const Run& r, const RopeParams& rp, const float2* tok, int c,
-                                           float (&y)[16]) {
+template <bool kPairs>
+__device__ __forceinline__ void rotate_run(const Run& r, const uint32_t (&mate)[8], const RopeParams& rp,
+                                           const float2* tok, int c, float (&y)[16]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) bf16x2_unpack(r.own[i], y[2 * i], y[2 * i + 1]);
   const int n = rp.rd >> 4;
   if (c >= n) return;
-  if (rp.interleaved) {
+  if (kPairs) {
     const float2* cs = tok + (c >> 1) * kRunStride + (c & 1) * 8;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -121,7 +133,7 @@ __device__ __forceinline__ void rotate_run(const Run& r, const RopeParams& rp, c
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float m0, m1;
-      bf16x2_unpack(r.mate[i], m0, m1);
+      bf16x2_unpack(mate[i], m0, m1);
       const float2 t0 = cs[2 * i], t1 = cs[2 * i + 1];
       y[2 * i] = y[2 * i] * t0.x + sg * m0 * t0.y;
       y[2 * i + 1] = y[2 * i + 1] * t1.x + sg * m1 * t1.y;
@@ -132,7 +144,9 @@ __device__ __forceinline__ void rotate_run(const Run& r, const RopeParams& rp, c
 // The largest square the run contributes to the K exponent: pair lengths where
 // rotated, magnitudes elsewhere.  Squares of bf16 values are exact in fp32 and
 // their sum is rounded once, so every lane and order gives the same value.
-__device__ __forceinline__ float run_square(const Run& r, const RopeParams& rp, int c, bool rotate) {
+template <bool kPairs>
+__device__ __forceinline__ float run_square(const Run& r, const uint32_t (&mate)[8], const RopeParams& rp, int c,
+                                            bool rotate) {
   const int n = rotate ? rp.rd >> 4 : 0;
   float m = 0.f;
 #pragma unroll
@@ -141,11 +155,11 @@ __device__ __forceinline__ float run_square(const Run& r, const RopeParams& rp, 
     bf16x2_unpack(r.own[i], a, b);
     if (c >= n) {
       m = fmaxf(m, fmaxf(a * a, b * b));
-    } else if (rp.interleaved) {
+    } else if (kPairs) {
       m = fmaxf(m, fmaf(a, a, b * b));
     } else {
       float ma, mb;
-      bf16x2_unpack(r.mate[i], ma, mb);
+      bf16x2_unpack(mate[i], ma, mb);
       m = fmaxf(m, fmaxf(fmaf(a, a, ma * ma), fmaf(b, b, mb * mb)));
     }
   }
@@ -193,9 +207,10 @@ __device__ __forceinline__ int code_offset(int tensor, int t, int c) {
 
 // One head of 16 tokens, rotated (or not) and stored as bf16: lanes 8k .. 8k+7
 // hold one row, four rows per pass.  pos[t] < 0: the row is not touched.
+template <bool kPairs>
 __device__ __forceinline__ void rows_unit(const RopeParams& rp, const float2* tab, const int* pos, const uint16_t* in,
                                           int64_t in_stride, uint16_t* out, int64_t out_stride, int lane) {
-  const int c = lane & 7;
+  const int c = lane & 7, src = mate_lane(rp, lane);
   Run r[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
@@ -205,10 +220,11 @@ __device__ __forceinline__ void rows_unit(const RopeParams& rp, const float2* ta
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int t = 4 * u + (lane >> 3);
-    fetch_mate(r[u], rp, lane);
+    uint32_t mate[8];
+    fetch_mate<kPairs>(r[u], mate, src);
     if (pos[t] < 0) continue;
     float y[16];
-    rotate_run(r[u], rp, tab + t * kTokStride, c, y);
+    rotate_run<kPairs>(r[u], mate, rp, tab + t * kTokStride, c, y);
     uint4* o = reinterpret_cast<uint4*>(out + t * out_stride + 16 * c);
     o[0] = make_uint4(bf16x2_pack(y[0], y[1]), bf16x2_pack(y[2], y[3]), bf16x2_pack(y[4], y[5]),
                       bf16x2_pack(y[6], y[7]));
@@ -226,7 +242,9 @@ struct RopeArgs {
   int n_tokens;
 };
 
-__global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, const __grid_constant__ RopeParams rp) {
+// kPairs: rotated pairs are neighbouring channels (interleaved style)
+template <bool kPairs>
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(RopeArgs a, const __grid_constant__ RopeParams rp) {
   __shared__ float2 tab[kTile * kTokStride];
   __shared__ int pos[kTile];
   const int t0 = blockIdx.x * kTile;
@@ -236,9 +254,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, const __grid
   __syncthreads();
   const int lane = threadIdx.x & 31, units = a.heads[0] + a.heads[1];
   for (int u = blockIdx.y * kWarps + (threadIdx.x >> 5); u < units; u += gridDim.y * kWarps) {
-    const int w = u < a.heads[0] ? 0 : 1, h = u - (w ? a.heads[0] : 0);
-    rows_unit(rp, tab, pos, a.in[w] + t0 * a.in_stride[w] + h * 128, a.in_stride[w],
-              a.out[w] + t0 * a.out_stride[w] + h * 128, a.out_stride[w], lane);
+    const bool k = u >= a.heads[0];
+    const int h = u - (k ? a.heads[0] : 0);
+    const int64_t is = k ? a.in_stride[1] : a.in_stride[0], os = k ? a.out_stride[1] : a.out_stride[0];
+    rows_unit<kPairs>(rp, tab, pos, (k ? a.in[1] : a.in[0]) + t0 * is + h * 128, is,
+                      (k ? a.out[1] : a.out[0]) + t0 * os + h * 128, os, lane);
   }
 }
 
@@ -256,9 +276,10 @@ struct AppendFp8Args {
 
 // One (tile, head) of K (tensor 0) or V (tensor 1): tokens [t0, t1) of the tile
 // are new, in + t * stride is the row of tile slot t.
+template <bool kPairs>
 __device__ __forceinline__ void quant_unit(const RopeParams& rp, const float2* tab, const uint16_t* in, int64_t stride,
                                            int t0, int t1, int tensor, uint8_t* codes, int8_t* exp, int lane) {
-  const int c = lane & 7;
+  const int c = lane & 7, src = mate_lane(rp, lane);
   const bool rot = tensor == 0;
   const int e_old = t0 > 0 ? *exp : KV_FP8_EXP_MIN;
   Run r[4];
@@ -271,12 +292,13 @@ __device__ __forceinline__ void quant_unit(const RopeParams& rp, const float2* t
   }
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    if (rot) fetch_mate(r[u], rp, lane);
+    uint32_t mate[8];
+    if (rot) fetch_mate<kPairs>(r[u], mate, src);
     const uint32_t b = __ballot_sync(0xffffffffu, run_nonfinite(r[u]));
     if ((b >> (lane & 24)) & 0xFFu)
       bad |= 1u << u;
     else
-      sq = fmaxf(sq, run_square(r[u], rp, c, rot));
+      sq = fmaxf(sq, run_square<kPairs>(r[u], mate, rp, c, rot));
   }
   const int e = max(tile_exponent(warp_max_xor(sq, 1)), e_old);
   if (t0 > 0 && e > e_old) {                     // earlier tokens move to the larger exponent
@@ -295,12 +317,14 @@ __device__ __forceinline__ void quant_unit(const RopeParams& rp, const float2* t
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int t = 4 * u + (lane >> 3);
+    uint32_t mate[8];
+    if (rot) fetch_mate<kPairs>(r[u], mate, src);
     if (t < t0 || t >= t1) continue;
     uint4 w = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
     if (!((bad >> u) & 1)) {
       float y[16];
       if (rot) {
-        rotate_run(r[u], rp, tab + t * kTokStride, c, y);
+        rotate_run<kPairs>(r[u], mate, rp, tab + t * kTokStride, c, y);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) bf16x2_unpack(r[u].own[i], y[2 * i], y[2 * i + 1]);
@@ -315,7 +339,8 @@ __device__ __forceinline__ void quant_unit(const RopeParams& rp, const float2* t
   if (lane == 0 && (t0 == 0 || e > e_old)) *exp = (int8_t)e;
 }
 
-__global__ void __launch_bounds__(kThreads) append_fp8_kernel(AppendFp8Args a, const __grid_constant__ RopeParams rp) {
+template <bool kPairs>
+__global__ void __launch_bounds__(kThreads, 3) append_fp8_kernel(AppendFp8Args a, const __grid_constant__ RopeParams rp) {
   __shared__ float2 tab[kTile * kTokStride];
   __shared__ int pos[kTile];
   const int s = blockIdx.x / a.tiles, i = blockIdx.x - s * a.tiles;
@@ -355,11 +380,11 @@ __global__ void __launch_bounds__(kThreads) append_fp8_kernel(AppendFp8Args a, c
       const int tensor = u >= a.Hkv, h = u - (tensor ? a.Hkv : 0);
       const size_t tile = ((size_t)pid * a.Hkv + h) * per + sub;
       const int64_t stride = tensor ? a.v_stride : a.k_stride;
-      quant_unit(rp, tab, (tensor ? a.v : a.k) + row0 * stride + h * 128, stride, t0, t1, tensor,
+      quant_unit<kPairs>(rp, tab, (tensor ? a.v : a.k) + row0 * stride + h * 128, stride, t0, t1, tensor,
                  a.codes + tile * kFp8TileBytes + tensor * 2048, a.exps + tile * 2 + tensor, lane);
     } else {
       const int h = u - nkv;
-      rows_unit(rp, tab, pos, a.q + row0 * a.q_stride + h * 128, a.q_stride, a.q_out + row0 * a.qo_stride + h * 128,
+      rows_unit<kPairs>(rp, tab, pos, a.q + row0 * a.q_stride + h * 128, a.q_stride, a.q_out + row0 * a.qo_stride + h * 128,
                 a.qo_stride, lane);
     }
   }
@@ -443,7 +468,11 @@ cudaError_t launch_rope(const Pool& p, const RopeParams& r, int n_tokens, const 
   a.positions = positions;
   a.n_tokens = n_tokens;
   const long long tiles = ((long long)n_tokens + kTile - 1) / kTile;
-  rope_kernel<<<dim3((unsigned)tiles, slices(p, tiles, a.heads[0] + a.heads[1])), kThreads, 0, s>>>(a, r);
+  const dim3 grid((unsigned)tiles, slices(p, tiles, a.heads[0] + a.heads[1]));
+  if (r.interleaved)
+    rope_kernel<true><<<grid, kThreads, 0, s>>>(a, r);
+  else
+    rope_kernel<false><<<grid, kThreads, 0, s>>>(a, r);
   return cudaGetLastError();
 }
 
@@ -475,7 +504,11 @@ cudaError_t launch_append_fp8(const Pool& p, const Fp8Store& f, const RopeParams
   a.P = p.cfg.page_size;
   a.err = p.err;
   const long long tiles = (long long)n_seqs * a.tiles;
-  append_fp8_kernel<<<dim3((unsigned)tiles, slices(p, tiles, 2 * a.Hkv + (a.q ? a.Hq : 0))), kThreads, 0, s>>>(a, r);
+  const dim3 grid((unsigned)tiles, slices(p, tiles, 2 * a.Hkv + (a.q ? a.Hq : 0)));
+  if (r.interleaved)
+    append_fp8_kernel<true><<<grid, kThreads, 0, s>>>(a, r);
+  else
+    append_fp8_kernel<false><<<grid, kThreads, 0, s>>>(a, r);
   return cudaGetLastError();
 }
 
