@@ -103,6 +103,19 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
   const int split = blockIdx.x % a.n_split, pair = blockIdx.x / a.n_split;
   const int h = pair % a.L.Hkv, b = pair / a.L.Hkv;
   int n = a.c.seq_len[b];
+  // lane (r, j) holds head r, channels 64 c + 16 j + 0..15; on its way with the length
+  uint32_t qf[2][8];
+  {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.c.q) +
+                                                    ((size_t)b * a.Hq + h * G + (r < G ? r : 0)) * 128);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint4 x = q[8 * c + 2 * j], y = q[8 * c + 2 * j + 1];
+      const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) qf[c][i] = w[i];
+    }
+  }
   if (n < 0 || n > a.c.max_len) {
     if (split == 0 && threadIdx.x == 0) flag_error(a.err, KV_DEVERR_LENGTH);
     n = min(max(n, 0), a.c.max_len);
@@ -114,19 +127,21 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
   const int tpp = a.L.P / kTile, tpp_shift = tpp >> 1;
   const int32_t* pt = a.c.pt + (size_t)b * a.c.max_pages;
 
-  // the stored tile of this warp's k-th tile, -1 behind a bad page id
-  auto stored = [&](int k) -> long long {
+  // The warp's k-th tile: its page id is read a batch of 32 tiles ahead and not
+  // looked at before its turn (no load below waits for another where it is issued).
+  auto page_of = [&](int k) -> int {
+    return pt[k < mine ? sp.tile(i0 + warp + k * kWarps) >> tpp_shift : 0];
+  };
+  auto stored = [&](int k, int pid) -> long long {   // -1: no such tile, or behind a bad page id
     if (k >= mine) return -1;
-    const int tile = sp.tile(i0 + warp + k * kWarps);
-    const int pid = pt[tile >> tpp_shift];
     if (pid < 0 || pid >= a.L.num_pages) {
       flag_error(a.err, KV_DEVERR_PAGE_ID);
       return -1;
     }
-    return ((long long)pid * a.L.Hkv + h) * tpp + (tile & (tpp - 1));
+    return ((long long)pid * a.L.Hkv + h) * tpp + (sp.tile(i0 + warp + k * kWarps) & (tpp - 1));
   };
   auto exps_of = [&](long long t) -> int {
-    return t < 0 ? 0 : *reinterpret_cast<const uint16_t*>(a.L.exps + t * 2);
+    return *reinterpret_cast<const uint16_t*>(a.L.exps + max(t, 0ll) * 2);
   };
   const uint64_t policy = l2_evict_first_policy();
   auto issue = [&](int stage, long long t) {     // lane 0
@@ -137,37 +152,26 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
       bulk_g2s_hint(ring + stage * kFp8TileBytes, a.L.codes + t * kFp8TileBytes, kFp8TileBytes, bar + stage, policy);
     }
   };
-  // lane l knows the l-th tile of the current and of the next 32
-  long long cur = stored(lane);
+  // lane l knows the l-th tile of the current 32 and the page id of the next
+  const int pid0 = page_of(lane);
+  int next_pid = page_of(32 + lane);
+  long long cur = stored(lane, pid0), next = -1;
 #pragma unroll
   for (int k = 0; k < kStages; ++k) {
     const long long t = __shfl_sync(0xffffffffu, cur, k);
     if (lane == 0 && k < mine) issue(k, t);
   }
   int exps = exps_of(cur);
-  long long next = stored(32 + lane);
 
-  // q as the B operand: lane (r, j) holds head r, channels 64 c + 16 j + 0..15
-  uint32_t qf[2][8];
+  // q as the B operand: scaled per head by a power of two, fp16
   float cs0, cs1;
   {
     uint32_t top = 0;
-    if (r < G) {
-      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.c.q) +
-                                                      ((size_t)b * a.Hq + h * G + r) * 128);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const uint4 x = q[8 * c + 2 * j], y = q[8 * c + 2 * j + 1];
-        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          qf[c][i] = w[i];
-          top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) qf[i >> 3][i & 7] = 0;
+    for (int i = 0; i < 16; ++i) {
+      if (r >= G) qf[i >> 3][i & 7] = 0;       // columns without a head
+      const uint32_t w = qf[i >> 3][i & 7];
+      top = max(top, max(w & 0x7FFFu, (w >> 16) & 0x7FFFu));
     }
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -193,10 +197,13 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
   bool ok = true;
   int k = 0, stage = 0, phase = 0;
   for (; k < mine; ++k) {
-    if (k && (k & 31) == 0) {
-      cur = next;
-      exps = exps_of(cur);
-      next = stored(k + 32 + lane);
+    if ((k & 31) == 0) {                       // the next 32: their page ids have been on the way since the last batch
+      if (k) {
+        cur = next;
+        exps = exps_of(cur);
+      }
+      next = stored(k + 32 + lane, next_pid);
+      next_pid = page_of(k + 64 + lane);
     }
     if (!mbar_wait(bar + stage, phase, a.polls)) {
       ok = false;
@@ -356,6 +363,19 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
   __threadfence();
   float* sw = reinterpret_cast<float*>(smem);  // weights [split][G]
   float* sl = sw + kMaxSplits * G;             // [G] M, l
+  // G * 32 columns of four channels; where threads are left, several share a
+  // column, each a run of splits.  The first kFly parts of a run are on their way
+  // before the weights are formed.
+  constexpr int kCols = G * 32, kShare = kThreads / kCols, kFly = 16;
+  const int col = threadIdx.x % kCols, sh = threadIdx.x / kCols;
+  const int g = col >> 5, c4 = col & 31;
+  const int run = (a.n_split + kShare - 1) / kShare, s0 = sh * run, s1 = min(s0 + run, a.n_split);
+  auto part_of = [&](int s) {
+    return __ldcg(reinterpret_cast<const float4*>(parts + ((size_t)s * G + g) * kPart + 4) + c4);
+  };
+  float4 fly[kFly];
+#pragma unroll
+  for (int u = 0; u < kFly; ++u) fly[u] = part_of(min(s0 + u, a.n_split - 1));
   if (warp < G) {
     const int g = warp;
     float M = kNoRef, l = 0.f;
@@ -386,16 +406,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
     }
   }
   __syncthreads();
-  // G * 32 columns of four channels; where threads are left, several share a
-  // column, each a run of splits
-  constexpr int kCols = G * 32, kShare = kThreads / kCols;
-  const int col = threadIdx.x % kCols, sh = threadIdx.x / kCols;
-  const int g = col >> 5, c4 = col & 31;
-  const int run = (a.n_split + kShare - 1) / kShare, s0 = sh * run, s1 = min(s0 + run, a.n_split);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int s = s0; s < s1; ++s) {
-    const float4 p = __ldcg(reinterpret_cast<const float4*>(parts + ((size_t)s * G + g) * kPart + 4) + c4);
+  auto add = [&](int s, const float4& p) {
     const float f = sw[s * G + g];
     if (!(f < 0.f)) {
       acc.x = fmaf(f, p.x, acc.x);
@@ -403,7 +415,12 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
       acc.z = fmaf(f, p.z, acc.z);
       acc.w = fmaf(f, p.w, acc.w);
     }
-  }
+  };
+#pragma unroll
+  for (int u = 0; u < kFly; ++u)
+    if (s0 + u < s1) add(s0 + u, fly[u]);
+#pragma unroll 8
+  for (int s = s0 + kFly; s < s1; ++s) add(s, part_of(s));
   float4* red = reinterpret_cast<float4*>(sl + ((G + 3) & ~3));
   if (kShare > 1) {
     red[threadIdx.x] = acc;
@@ -425,16 +442,18 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
   }
 }
 
-// Splits per (sequence, KV head), from the host's bound on visible tiles.  A
-// batch that does not fill the GPU is split into one wave of CTAs; a larger one
-// into about four waves, so that sequences of different lengths even out.  A
-// split has at least a tile per warp.
+// Splits per (sequence, KV head), from the host's bound on visible tiles; a split
+// has at least a tile per warp.  Few pairs: one wave with one CTA per SM (8 pairs
+// of 100,000 tokens: 37.7 us against 39.9 with two per SM, whose join reads twice
+// the parts).  Enough pairs that this would leave SMs idle: two per SM (128 pairs
+// of 4,160 tokens: 29.3 us against 35.9).  More pairs than that: about six waves,
+// so that sequences of different lengths even out (512 pairs of 8k to 32k tokens:
+// 398 us, with four waves 408).
 int splits(const Pool& p, int B, long long max_len, int window, int n_sink) {
   long long tokens = max_len;
   if (window) tokens = std::min(tokens, (long long)window + n_sink + 2 * kTile);
-  const long long tiles = (tokens + kTile - 1) / kTile, pairs = (long long)B * p.cfg.num_kv_heads;
-  const long long slots = 2ll * p.sm_count;
-  const long long want = pairs * 2 <= slots ? slots / pairs : (4 * slots + pairs - 1) / pairs;
+  const long long tiles = (tokens + kTile - 1) / kTile, pairs = (long long)B * p.cfg.num_kv_heads, sms = p.sm_count;
+  const long long want = sms >= 4 * pairs ? sms / pairs : (pairs <= sms ? 2 * sms / pairs : (12 * sms + pairs - 1) / pairs);
   const long long most = std::min<long long>((tiles + kWarps - 1) / kWarps, kMaxSplits);
   return (int)std::max(1ll, std::min(want, most));
 }
