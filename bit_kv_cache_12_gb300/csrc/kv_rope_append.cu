@@ -18,7 +18,11 @@
 // for a slice of the heads: the 16 x 64 cosines and sines are formed once per
 // CTA in shared memory and used by every head, and a warp owns the whole
 // (tile, head) it quantizes, so the tile's maximum is one warp reduction, no
-// atomics, and a tile that already holds tokens has one writer.
+// atomics, and a tile that already holds tokens has one writer.  A lane holds
+// both members of its pairs (two chunks of eight channels), so nothing crosses
+// lanes but the maximum; what counted was the number of instructions (269 per 16
+// channels with pairs fetched from other lanes: 47 us for a prompt of 8192
+// tokens, 39 us now, 4.7 TB/s) and of registers (64: four CTAs per SM).
 #include <cuda_fp8.h>
 
 #include <cmath>
@@ -32,19 +36,35 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-// cos / sin rows: 16 pairs (128 B) and 16 B of padding, so that the four runs
-// of a token a quarter warp reads fall in different banks
-constexpr int kRunStride = 18;                 // float2
-constexpr int kTokStride = 4 * kRunStride;     // float2
-
-__device__ __forceinline__ void bf16x2_unpack(uint32_t w, float& a, float& b) {
-  a = bf16lo(w);
-  b = bf16hi(w);
-}
+// Cosines and sines of a token: pair i = 8 l + e (lane l of the token's eight)
+// at 4 l + e % 4 + 32 (e / 4), the sines 64 behind; 4 floats of padding.  The
+// eight lanes of a token read 16 bytes each, all banks once.
+constexpr int kTokStride = 132;
 
 __device__ __forceinline__ uint32_t bf16x2_pack(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Pairs of fp32 values in one register pair: one instruction for both, each
+// rounded as the scalar one.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_split(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
 // cos and sin of `turns` (units of 2^-64 of a turn), times att.  The nearest
@@ -60,20 +80,34 @@ __device__ __forceinline__ float2 turn_cos_sin(unsigned long long turns, float a
 }
 
 // Table of the CTA's 16 tokens: pos < 0 marks a token without work.
-__device__ __forceinline__ void fill_table(float2* tab, const RopeParams& rp, const int* pos) {
+__device__ __forceinline__ void fill_table(float* tab, const RopeParams& rp, const int* pos) {
   const int n = rp.rd >> 1;
   for (int i = threadIdx.x; i < kTile * 64; i += kThreads) {
     const int t = i >> 6, f = i & 63;
-    if (f < n && pos[t] >= 0)
-      tab[t * kTokStride + (f >> 4) * kRunStride + (f & 15)] =
-          turn_cos_sin((unsigned long long)pos[t] * rp.turn[f], rp.att);
+    if (f < n && pos[t] >= 0) {
+      const float2 cs = turn_cos_sin((unsigned long long)pos[t] * rp.turn[f], rp.att);
+      float* d = tab + t * kTokStride + 4 * (f >> 3) + (f & 3) + 32 * ((f >> 2) & 1);
+      d[0] = cs.x;
+      d[64] = cs.y;
+    }
   }
 }
 
-// 16 channels of a row (run c of 8).
-struct Run {
-  uint32_t own[8];
+// The 16 channels of a row that a lane holds: two chunks of eight.  Half style:
+// the first and the second members of eight pairs where rotated, else two
+// neighbouring chunks.  Interleaved (kPairs): neighbouring chunks, the pairs in
+// their words.  No value crosses lanes.
+struct Chunks {
+  int a, b;                                    // first channels
+  bool rotated;
 };
+template <bool kPairs>
+__device__ __forceinline__ Chunks chunks_of(const RopeParams& rp, int lane) {
+  const int l = lane & 7;
+  if (kPairs) return {16 * l, 16 * l + 8, 16 * l < rp.rd};
+  const int np = rp.rd >> 4;                   // lanes that hold pairs
+  return l < np ? Chunks{8 * l, 8 * l + (rp.rd >> 1), true} : Chunks{16 * l, 16 * l + 8, false};
+}
 
 // read once by this kernel (and perhaps written by it: not the read-only path)
 __device__ __forceinline__ uint4 ld_once(const void* p) {
@@ -84,94 +118,82 @@ __device__ __forceinline__ uint4 ld_once(const void* p) {
   return v;
 }
 
-__device__ __forceinline__ void load_run(Run& r, const uint16_t* row, int c, bool live) {
-  uint4 a = make_uint4(0, 0, 0, 0), b = a;
+struct Run {
+  uint32_t w[8];                               // chunk a, chunk b
+};
+
+__device__ __forceinline__ void load_run(Run& r, const uint16_t* row, int a, int b, bool live) {
+  uint4 x = make_uint4(0, 0, 0, 0), y = x;
   if (live) {
-    a = ld_once(row + 16 * c);
-    b = ld_once(row + 16 * c + 8);
+    x = ld_once(row + a);
+    y = ld_once(row + b);
   }
-  r.own[0] = a.x; r.own[1] = a.y; r.own[2] = a.z; r.own[3] = a.w;
-  r.own[4] = b.x; r.own[5] = b.y; r.own[6] = b.z; r.own[7] = b.w;
+  r.w[0] = x.x; r.w[1] = x.y; r.w[2] = x.z; r.w[3] = x.w;
+  r.w[4] = y.x; r.w[5] = y.y; r.w[6] = y.z; r.w[7] = y.w;
 }
 
-// The run that channel run c is paired with (half style) sits in another lane of
-// the same row (lanes 8k .. 8k + 7).  It is fetched where it is used, twice for a
-// quantized tile: kept, it would cost 32 registers and a third of the warps.
-__device__ __forceinline__ int mate_lane(const RopeParams& rp, int lane) {
-  const int c = lane & 7, n = rp.rd >> 4, h = n >> 1;   // rotated runs, half of them
-  return (lane & 24) | (c < h ? c + h : (c < n ? c - h : c));
-}
-template <bool kPairs>
-__device__ __forceinline__ void fetch_mate(const Run& r, uint32_t (&mate)[8], int src) {
-  if (!kPairs) {                               // else the pair is in the run itself
-#pragma unroll
-    for (int i = 0; i < 8; ++i) mate[i] = __shfl_sync(0xffffffffu, r.own[i], src);
-  }
-}
+__device__ __forceinline__ uint64_t f2_of(uint32_t w) { return f2(bf16lo(w), bf16hi(w)); }
 
-// The rotated values of the run.
+// The rotated values, chunk a then chunk b, as fp32 pairs.
 template <bool kPairs>
-__device__ __forceinline__ void rotate_run(const Run& r, const uint32_t (&mate)[8], const RopeParams& rp,
-                                           const float2* tok, int c, float (&y)[16]) {
+__device__ __forceinline__ void rotate_run(const Run& r, const float* tok, int lane, bool rotated, uint64_t (&y)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) bf16x2_unpack(r.own[i], y[2 * i], y[2 * i + 1]);
-  const int n = rp.rd >> 4;
-  if (c >= n) return;
+  for (int i = 0; i < 8; ++i) y[i] = f2_of(r.w[i]);
+  if (!rotated) return;
+  const float4* t = reinterpret_cast<const float4*>(tok) + (lane & 7);
+  const float4 c0 = t[0], c1 = t[8], s0 = t[16], s1 = t[24];
   if (kPairs) {
-    const float2* cs = tok + (c >> 1) * kRunStride + (c & 1) * 8;
+    const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+    const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float2 t = cs[i];
-      const float a = y[2 * i], b = y[2 * i + 1];
-      y[2 * i] = a * t.x - b * t.y;
-      y[2 * i + 1] = b * t.x + a * t.y;
+      float a, b;
+      f2_split(y[i], a, b);
+      y[i] = f2(a * c[i] - b * s[i], b * c[i] + a * s[i]);
     }
   } else {
-    const int h = n >> 1;
-    const float2* cs = tok + (c < h ? c : c - h) * kRunStride;
-    const float sg = c < h ? -1.f : 1.f;       // first of the pair: a cos - b sin
+    const uint64_t c[4] = {f2(c0.x, c0.y), f2(c0.z, c0.w), f2(c1.x, c1.y), f2(c1.z, c1.w)};
+    const uint64_t s[4] = {f2(s0.x, s0.y), f2(s0.z, s0.w), f2(s1.x, s1.y), f2(s1.z, s1.w)};
+    const uint64_t minus = f2(-1.f, -1.f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float m0, m1;
-      bf16x2_unpack(mate[i], m0, m1);
-      const float2 t0 = cs[2 * i], t1 = cs[2 * i + 1];
-      y[2 * i] = y[2 * i] * t0.x + sg * m0 * t0.y;
-      y[2 * i + 1] = y[2 * i + 1] * t1.x + sg * m1 * t1.y;
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t a = y[i], b = y[4 + i];
+      y[i] = f2_fma(f2_mul(b, minus), s[i], f2_mul(a, c[i]));
+      y[4 + i] = f2_fma(a, s[i], f2_mul(b, c[i]));
     }
   }
 }
 
 // The largest square the run contributes to the K exponent: pair lengths where
 // rotated, magnitudes elsewhere.  Squares of bf16 values are exact in fp32 and
-// their sum is rounded once, so every lane and order gives the same value.
+// their sum is rounded once, so every order gives the same value.
 template <bool kPairs>
-__device__ __forceinline__ float run_square(const Run& r, const uint32_t (&mate)[8], const RopeParams& rp, int c,
-                                            bool rotate) {
-  const int n = rotate ? rp.rd >> 4 : 0;
+__device__ __forceinline__ float run_square(const Run& r, const RopeParams& rp, bool rotated) {
   float m = 0.f;
+  if (kPairs || !rotated) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float a, b;
-    bf16x2_unpack(r.own[i], a, b);
-    if (c >= n) {
-      m = fmaxf(m, fmaxf(a * a, b * b));
-    } else if (kPairs) {
-      m = fmaxf(m, fmaf(a, a, b * b));
-    } else {
-      float ma, mb;
-      bf16x2_unpack(mate[i], ma, mb);
-      m = fmaxf(m, fmaxf(fmaf(a, a, ma * ma), fmaf(b, b, mb * mb)));
+    for (int i = 0; i < 8; ++i) {
+      const float a = bf16lo(r.w[i]), b = bf16hi(r.w[i]);
+      m = rotated ? fmaxf(m, fmaf(a, a, b * b)) : fmaxf(m, fmaxf(a * a, b * b));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t a = f2_of(r.w[i]), b = f2_of(r.w[4 + i]);
+      float x, y;
+      f2_split(f2_fma(a, a, f2_mul(b, b)), x, y);
+      m = fmaxf(m, fmaxf(x, y));
     }
   }
-  return (c < n && rp.att2 != 1.f) ? m * rp.att2 : m;
+  return rotated && rp.att2 != 1.f ? m * rp.att2 : m;
 }
 
-__device__ __forceinline__ bool run_nonfinite(const Run& r) {
-  bool bad = false;
+// The largest magnitude of the run, as bf16 bits (above 0x7F7F: not finite).
+__device__ __forceinline__ uint32_t run_magnitude(const Run& r) {
+  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    bad = bad || (r.own[i] & 0x7F80u) == 0x7F80u || (r.own[i] & 0x7F800000u) == 0x7F800000u;
-  return bad;
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, r.w[i] & 0x7FFF7FFFu);
+  return max(m & 0xFFFFu, m >> 16);
 }
 
 // The smallest e with square <= (448 * 2^e)^2 = 1.53125 * 2^(17 + 2e), clamped.
@@ -180,6 +202,12 @@ __device__ __forceinline__ int tile_exponent(float square) {
   const int k = (int)(u >> 23) - 127;
   if (k == 128) return KV_FP8_EXP_MAX;
   const int e = (k - 16 + ((u & 0x7FFFFFu) > 0x440000u ? 1 : 0)) >> 1;
+  return min(max(e, KV_FP8_EXP_MIN), KV_FP8_EXP_MAX);
+}
+
+// The same from the largest magnitude, as finite bf16 bits: 448 = 1.75 * 2^8.
+__device__ __forceinline__ int magnitude_exponent(uint32_t bits) {
+  const int e = (int)(bits >> 7) - 127 - 8 + ((bits & 0x7Fu) > 0x60u ? 1 : 0);
   return min(max(e, KV_FP8_EXP_MIN), KV_FP8_EXP_MAX);
 }
 
@@ -199,37 +227,40 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
   return e4m3x4(x.x * f, x.y * f, y.x * f, y.y * f);
 }
 
-// Byte offset of run c (16 channels) of token t in the stored K or V codes.
-__device__ __forceinline__ int code_offset(int tensor, int t, int c) {
-  return tensor == 0 ? (t >> 3) * 1024 + (c >> 2) * 512 + (t & 7) * 64 + (c & 3) * 16
-                     : ((t & 1) + 2 * (t >> 3)) * 512 + c * 64 + ((t & 7) >> 1) * 16;
+// Byte offset of channel c (a multiple of 8) of token t in the stored K or V codes.
+__device__ __forceinline__ int code_offset(bool v, int t, int c) {
+  return v ? ((t & 1) + 2 * (t >> 3)) * 512 + (c >> 4) * 64 + ((t & 7) >> 1) * 16 + (c & 15)
+           : (t >> 3) * 1024 + (c >> 6) * 512 + (t & 7) * 64 + (c & 63);
 }
 
-// One head of 16 tokens, rotated (or not) and stored as bf16: lanes 8k .. 8k+7
-// hold one row, four rows per pass.  pos[t] < 0: the row is not touched.
+// One head of 16 tokens, rotated and stored as bf16: lanes 8k .. 8k + 7 hold one
+// row, four rows per pass.  pos[t] < 0: the row is not touched.
 template <bool kPairs>
-__device__ __forceinline__ void rows_unit(const RopeParams& rp, const float2* tab, const int* pos, const uint16_t* in,
+__device__ __forceinline__ void rows_unit(const RopeParams& rp, const float* tab, const int* pos, const uint16_t* in,
                                           int64_t in_stride, uint16_t* out, int64_t out_stride, int lane) {
-  const int c = lane & 7, src = mate_lane(rp, lane);
+  const Chunks ch = chunks_of<kPairs>(rp, lane);
   Run r[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int t = 4 * u + (lane >> 3);
-    load_run(r[u], in + t * in_stride, c, pos[t] >= 0);
+    load_run(r[u], in + t * in_stride, ch.a, ch.b, pos[t] >= 0);
   }
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int t = 4 * u + (lane >> 3);
-    uint32_t mate[8];
-    fetch_mate<kPairs>(r[u], mate, src);
     if (pos[t] < 0) continue;
-    float y[16];
-    rotate_run<kPairs>(r[u], mate, rp, tab + t * kTokStride, c, y);
-    uint4* o = reinterpret_cast<uint4*>(out + t * out_stride + 16 * c);
-    o[0] = make_uint4(bf16x2_pack(y[0], y[1]), bf16x2_pack(y[2], y[3]), bf16x2_pack(y[4], y[5]),
-                      bf16x2_pack(y[6], y[7]));
-    o[1] = make_uint4(bf16x2_pack(y[8], y[9]), bf16x2_pack(y[10], y[11]), bf16x2_pack(y[12], y[13]),
-                      bf16x2_pack(y[14], y[15]));
+    uint64_t y[8];
+    rotate_run<kPairs>(r[u], tab + t * kTokStride, lane, ch.rotated, y);
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float a, b;
+      f2_split(y[i], a, b);
+      o[i] = bf16x2_pack(a, b);
+    }
+    uint16_t* row = out + t * out_stride;
+    *reinterpret_cast<uint4*>(row + ch.a) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(row + ch.b) = make_uint4(o[4], o[5], o[6], o[7]);
   }
 }
 
@@ -245,7 +276,7 @@ struct RopeArgs {
 // kPairs: rotated pairs are neighbouring channels (interleaved style)
 template <bool kPairs>
 __global__ void __launch_bounds__(kThreads, 4) rope_kernel(RopeArgs a, const __grid_constant__ RopeParams rp) {
-  __shared__ float2 tab[kTile * kTokStride];
+  __shared__ __align__(16) float tab[kTile * kTokStride];
   __shared__ int pos[kTile];
   const int t0 = blockIdx.x * kTile;
   if (threadIdx.x < kTile) pos[threadIdx.x] = t0 + (int)threadIdx.x < a.n_tokens ? a.positions[t0 + threadIdx.x] : -1;
@@ -274,37 +305,38 @@ struct AppendFp8Args {
   int* err;
 };
 
-// One (tile, head) of K (tensor 0) or V (tensor 1): tokens [t0, t1) of the tile
-// are new, in + t * stride is the row of tile slot t.
-template <bool kPairs>
-__device__ __forceinline__ void quant_unit(const RopeParams& rp, const float2* tab, const uint16_t* in, int64_t stride,
-                                           int t0, int t1, int tensor, uint8_t* codes, int8_t* exp, int lane) {
-  const int c = lane & 7, src = mate_lane(rp, lane);
-  const bool rot = tensor == 0;
+// One (tile, head) of K (kV false) or V: tokens [t0, t1) of the tile are new,
+// in + t * stride is the row of tile slot t.
+template <bool kPairs, bool kV>
+__device__ __forceinline__ void quant_unit(const RopeParams& rp, const float* tab, const uint16_t* in, int64_t stride,
+                                           int t0, int t1, uint8_t* codes, int8_t* exp, int lane) {
+  const Chunks ch = kV ? Chunks{16 * (lane & 7), 16 * (lane & 7) + 8, false} : chunks_of<kPairs>(rp, lane);
   const int e_old = t0 > 0 ? *exp : KV_FP8_EXP_MIN;
   Run r[4];
-  uint32_t bad = 0;
-  float sq = 0.f;
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int t = 4 * u + (lane >> 3);
-    load_run(r[u], in + t * stride, c, t >= t0 && t < t1);
+    load_run(r[u], in + t * stride, ch.a, ch.b, t >= t0 && t < t1);
   }
+  uint32_t bad = 0, mag = 0;                   // passes whose row is not finite; V: the largest magnitude
+  float sq = 0.f;
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    uint32_t mate[8];
-    if (rot) fetch_mate<kPairs>(r[u], mate, src);
-    const uint32_t b = __ballot_sync(0xffffffffu, run_nonfinite(r[u]));
+    const uint32_t m = run_magnitude(r[u]);
+    const uint32_t b = __ballot_sync(0xffffffffu, m >= 0x7F80u);
     if ((b >> (lane & 24)) & 0xFFu)
       bad |= 1u << u;
+    else if (kV)
+      mag = max(mag, m);
     else
-      sq = fmaxf(sq, run_square<kPairs>(r[u], mate, rp, c, rot));
+      sq = fmaxf(sq, run_square<kPairs>(r[u], rp, ch.rotated));
   }
-  const int e = max(tile_exponent(warp_max_xor(sq, 1)), e_old);
-  if (t0 > 0 && e > e_old) {                     // earlier tokens move to the larger exponent
+  // V: a magnitude's exponent by itself (its square would give the same)
+  const int e = max(kV ? magnitude_exponent(__reduce_max_sync(0xffffffffu, mag)) : tile_exponent(warp_max_xor(sq, 1)), e_old);
+  if (t0 > 0 && e > e_old) {                   // earlier tokens move to the larger exponent
     const float f = pow2i(max(e_old - e, -126));
     for (int t = lane >> 3; t < t0; t += 4) {
-      uint4* p = reinterpret_cast<uint4*>(codes + code_offset(tensor, t, c));
+      uint4* p = reinterpret_cast<uint4*>(codes + code_offset(kV, t, 16 * (lane & 7)));
       uint4 w = *p;
       w.x = rescale4(w.x, f);
       w.y = rescale4(w.y, f);
@@ -314,34 +346,36 @@ __device__ __forceinline__ void quant_unit(const RopeParams& rp, const float2* t
     }
   }
   const float inv = pow2i(-e);
+  const uint64_t inv2 = f2(inv, inv);
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int t = 4 * u + (lane >> 3);
-    uint32_t mate[8];
-    if (rot) fetch_mate<kPairs>(r[u], mate, src);
     if (t < t0 || t >= t1) continue;
-    uint4 w = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    uint32_t c[4] = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
     if (!((bad >> u) & 1)) {
-      float y[16];
-      if (rot) {
-        rotate_run<kPairs>(r[u], mate, rp, tab + t * kTokStride, c, y);
-      } else {
+      uint64_t y[8];
+      rotate_run<kPairs>(r[u], tab + t * kTokStride, lane, !kV && ch.rotated, y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) bf16x2_unpack(r[u].own[i], y[2 * i], y[2 * i + 1]);
+      for (int i = 0; i < 4; ++i) {
+        float x0, x1, x2, x3;
+        f2_split(f2_mul(y[2 * i], inv2), x0, x1);
+        f2_split(f2_mul(y[2 * i + 1], inv2), x2, x3);
+        c[i] = e4m3x4(x0, x1, x2, x3);
       }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) y[i] *= inv;
-      w = make_uint4(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]),
-                     e4m3x4(y[8], y[9], y[10], y[11]), e4m3x4(y[12], y[13], y[14], y[15]));
     }
-    *reinterpret_cast<uint4*>(codes + code_offset(tensor, t, c)) = w;
+    if (kV) {
+      *reinterpret_cast<uint4*>(codes + code_offset(true, t, ch.a)) = make_uint4(c[0], c[1], c[2], c[3]);
+    } else {
+      *reinterpret_cast<uint2*>(codes + code_offset(false, t, ch.a)) = make_uint2(c[0], c[1]);
+      *reinterpret_cast<uint2*>(codes + code_offset(false, t, ch.b)) = make_uint2(c[2], c[3]);
+    }
   }
   if (lane == 0 && (t0 == 0 || e > e_old)) *exp = (int8_t)e;
 }
 
 template <bool kPairs>
-__global__ void __launch_bounds__(kThreads, 3) append_fp8_kernel(AppendFp8Args a, const __grid_constant__ RopeParams rp) {
-  __shared__ float2 tab[kTile * kTokStride];
+__global__ void __launch_bounds__(kThreads, 4) append_fp8_kernel(AppendFp8Args a, const __grid_constant__ RopeParams rp) {
+  __shared__ __align__(16) float tab[kTile * kTokStride];
   __shared__ int pos[kTile];
   const int s = blockIdx.x / a.tiles, i = blockIdx.x - s * a.tiles;
   const int c0 = a.cu[s];
@@ -380,8 +414,12 @@ __global__ void __launch_bounds__(kThreads, 3) append_fp8_kernel(AppendFp8Args a
       const int tensor = u >= a.Hkv, h = u - (tensor ? a.Hkv : 0);
       const size_t tile = ((size_t)pid * a.Hkv + h) * per + sub;
       const int64_t stride = tensor ? a.v_stride : a.k_stride;
-      quant_unit<kPairs>(rp, tab, (tensor ? a.v : a.k) + row0 * stride + h * 128, stride, t0, t1, tensor,
-                 a.codes + tile * kFp8TileBytes + tensor * 2048, a.exps + tile * 2 + tensor, lane);
+      uint8_t* codes = a.codes + tile * kFp8TileBytes;
+      if (tensor == 0)
+        quant_unit<kPairs, false>(rp, tab, a.k + row0 * stride + h * 128, stride, t0, t1, codes, a.exps + tile * 2, lane);
+      else
+        quant_unit<kPairs, true>(rp, tab, a.v + row0 * stride + h * 128, stride, t0, t1, codes + 2048,
+                                 a.exps + tile * 2 + 1, lane);
     } else {
       const int h = u - nkv;
       rows_unit<kPairs>(rp, tab, pos, a.q + row0 * a.q_stride + h * 128, a.q_stride, a.q_out + row0 * a.qo_stride + h * 128,
@@ -390,10 +428,13 @@ __global__ void __launch_bounds__(kThreads, 3) append_fp8_kernel(AppendFp8Args a
   }
 }
 
-// Slices of the heads per tile: enough CTAs for four per SM, at most one unit
-// per warp.
-unsigned slices(const Pool& p, long long tiles, int units) {
-  const long long want = (4ll * p.sm_count + tiles - 1) / tiles;
+// Slices of the heads per tile: about `per_sm` CTAs per SM, at most one unit per
+// warp.  A slice forms the tile's table again, so the append, whose units are
+// longer, takes fewer (8: ragged chunks 59 us, with 4: 63; a prompt of 8192: 39,
+// with 16: 43) than the rotary rows (16: 54 us, with 4: 57).
+constexpr int kRopePerSm = 16, kAppendPerSm = 8;
+unsigned slices(const Pool& p, long long tiles, int units, int per_sm) {
+  const long long want = ((long long)per_sm * p.sm_count + tiles - 1) / tiles;
   return (unsigned)std::max(1ll, std::min<long long>((units + kWarps - 1) / kWarps, want));
 }
 
@@ -468,7 +509,7 @@ cudaError_t launch_rope(const Pool& p, const RopeParams& r, int n_tokens, const 
   a.positions = positions;
   a.n_tokens = n_tokens;
   const long long tiles = ((long long)n_tokens + kTile - 1) / kTile;
-  const dim3 grid((unsigned)tiles, slices(p, tiles, a.heads[0] + a.heads[1]));
+  const dim3 grid((unsigned)tiles, slices(p, tiles, a.heads[0] + a.heads[1], kRopePerSm));
   if (r.interleaved)
     rope_kernel<true><<<grid, kThreads, 0, s>>>(a, r);
   else
@@ -504,7 +545,7 @@ cudaError_t launch_append_fp8(const Pool& p, const Fp8Store& f, const RopeParams
   a.P = p.cfg.page_size;
   a.err = p.err;
   const long long tiles = (long long)n_seqs * a.tiles;
-  const dim3 grid((unsigned)tiles, slices(p, tiles, 2 * a.Hkv + (a.q ? a.Hq : 0)));
+  const dim3 grid((unsigned)tiles, slices(p, tiles, 2 * a.Hkv + (a.q ? a.Hq : 0), kAppendPerSm));
   if (r.interleaved)
     append_fp8_kernel<true><<<grid, kThreads, 0, s>>>(a, r);
   else

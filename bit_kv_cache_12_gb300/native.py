@@ -132,17 +132,32 @@ class KVError(RuntimeError):
 def _ptr(x):
     if x is None:
         return None
-    if isinstance(x, int):
-        return x
-    if hasattr(x, "data_ptr"):
+    try:
         return x.data_ptr()
-    return int(x)
+    except AttributeError:
+        return int(x)
+
+
+_current_stream = None
+
+
+def _find_current_stream():
+    """The raw handle of torch's current stream: torch's own short way where it has one (a
+    Stream object for every call costs more than the launch)."""
+    global _current_stream
+    import torch
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    torch.cuda.init()
+    if raw and device:
+        _current_stream = lambda: raw(device())  # noqa: E731
+    else:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _current_stream()
 
 
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream() if _current_stream else _find_current_stream()
     if hasattr(s, "cuda_stream"):
         return s.cuda_stream
     return int(s)
