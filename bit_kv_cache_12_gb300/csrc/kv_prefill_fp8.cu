@@ -75,7 +75,7 @@ struct Pass {
 };
 constexpr int kRing = 8;
 
-enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kOFull = 12, kDrain = 13, kPass = 14, kBars = 14 + kRing };
+enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kOFull = 12, kDrain = 13, kQFull = 14, kPass = 16, kBars = 16 + kRing };
 
 // The rows of a CTA and the key tiles they see.
 struct Work {
@@ -488,13 +488,17 @@ __device__ __forceinline__ void issue_products(uint32_t tmem, uint8_t* sm, Share
     __syncwarp();
   };
   if (!ready(kKFull, 0)) return;
-  fence_after();
-  scores(0, 0);
-  scores(1, 0);
+  for (int tile = 0; tile < 2; ++tile) {
+    if (!ready(kQFull + tile, 0)) return;
+    fence_after();
+    scores(tile, 0);
+  }
   for (int it = 0;; ++it) {
     const int stage = it & 1;
     const bool last = sh->pass[it & (kRing - 1)].last != 0;
+    // V, and the K of the next scores, long since there: looked at before P is due
     if (!ready(kVFull + stage, (it >> 1) & 1)) return;
+    if (!last && !ready(kKFull + (stage ^ 1), ((it + 1) >> 1) & 1)) return;
 #pragma unroll 1
     for (int tile = 0; tile < 2; ++tile) {
       if (!ready(kPFull + tile, it & 1)) return;
@@ -515,7 +519,6 @@ __device__ __forceinline__ void issue_products(uint32_t tmem, uint8_t* sm, Share
       }
       __syncwarp();
       if (last) continue;
-      if (tile == 0 && !ready(kKFull + (stage ^ 1), ((it + 1) >> 1) & 1)) return;
       scores(tile, stage ^ 1);
     }
     if (last) break;
@@ -641,21 +644,56 @@ __device__ __forceinline__ bool softmax_rows(const PrefillFp8Args& a, const Work
   }
 }
 
-// A row's result: normalised to the output, or as a part of a split.
-__device__ __forceinline__ void write_row(const PrefillFp8Args& a, const Work& w, uint32_t to, bool any, bool ok, bool live,
-                                          int token, int hq, const RowOut& ro) {
+// q: this thread's row, scaled by a power of two, as fp16 into the swizzled operand;
+// returns the factor that brings a score back to base-2 logits (without 2^eK).
+__device__ __forceinline__ float load_q(const PrefillFp8Args& a, uint8_t* operand, int m, size_t qrow, bool live) {
+  uint32_t x[64], top = 0;
+  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.c.q) + (live ? qrow : 0) * 128);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint4 t = live ? q[i] : make_uint4(0, 0, 0, 0);
+    x[4 * i] = t.x;
+    x[4 * i + 1] = t.y;
+    x[4 * i + 2] = t.z;
+    x[4 * i + 3] = t.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 64; ++i) top = max(top, max(x[i] & 0x7FFFu, (x[i] >> 16) & 0x7FFFu));
+  const int up = min(14 - ((int)(top >> 7) - 127), 127);
+  float mul = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : pow2i(up);
+  if (a.c.scale < 0.f) mul = -mul;
+  uint8_t* dst = operand + m * 128;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    uint32_t f[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) f[u] = pack_f16(bf16lo(x[4 * i + u]) * mul, bf16hi(x[4 * i + u]) * mul);
+    *reinterpret_cast<uint4*>(dst + (i >> 3) * (kOperand / 2) + (((i & 7) ^ (m & 7)) << 4)) =
+        make_uint4(f[0], f[1], f[2], f[3]);
+  }
+  fence_async();
+  return fabsf(a.c.scale) * 1.4426950408889634f * pow2i(max(-up, -126));
+}
+
+// A row's result: normalised to the output, or as a part of a split.  `stage`:
+// 8 KB of shared memory for the warp's 32 rows, from which they are written
+// 256 bytes at a time (a row per thread straight from registers took 2.6 us).
+__device__ __forceinline__ void write_row(const PrefillFp8Args& a, const Work& w, uint32_t to, uint8_t* stage, bool any,
+                                          bool ok, bool live, int token, int hq, const RowOut& ro) {
+  const int lane = threadIdx.x & 31;
   const size_t qrow = ((size_t)w.c0 + token) * a.Hq + hq;
   const bool empty = ro.l == 0.f;
   const float f = !ok || ro.poison ? __uint_as_float(0x7FC00000u) : (empty ? 0.f : 1.f / ro.l);
   const float lse = empty ? -INFINITY : (ro.M + log2f(ro.l)) * kLn2;
   float* part = static_cast<float*>(a.c.ws) +
                 (((size_t)w.s * a.max_q + token) * a.Hq + hq) * a.n_split * 132 + (size_t)w.split * 132;
-  uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.c.out) + qrow * 128);
+  uint4* out = static_cast<uint4*>(a.c.out);
+  const bool staged = any && a.n_split == 1;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     float v[32];
     __syncwarp();
-    if (any && ok) {                         // the same for the whole warp
+    if (any && ok) {                           // the same for the whole warp
       ld32(to + 32 * q, v);
       settle(v);
     } else {
@@ -664,12 +702,14 @@ __device__ __forceinline__ void write_row(const PrefillFp8Args& a, const Work& w
     }
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = empty ? 0.f : v[i] * f;
-    if (live && a.n_split > 1) {
+    if (a.n_split > 1) {
+      if (live) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        *reinterpret_cast<float4*>(part + 4 + 32 * q + 4 * i) =
-            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else if (live) {
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<float4*>(part + 4 + 32 * q + 4 * i) =
+              make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      }
+    } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t u[4];
@@ -678,8 +718,23 @@ __device__ __forceinline__ void write_row(const PrefillFp8Args& a, const Work& w
           const __nv_bfloat162 y = __floats2bfloat162_rn(v[8 * i + 2 * e], v[8 * i + 2 * e + 1]);
           u[e] = *reinterpret_cast<const uint32_t*>(&y);
         }
-        out[4 * q + i] = make_uint4(u[0], u[1], u[2], u[3]);
+        const uint4 y = make_uint4(u[0], u[1], u[2], u[3]);
+        if (staged)                            // 16-byte chunk c of row r at c ^ (r % 16): no bank conflicts either way
+          *reinterpret_cast<uint4*>(stage + lane * 256 + (((4 * q + i) ^ (lane & 15)) << 4)) = y;
+        else if (live)
+          out[qrow * 16 + 4 * q + i] = y;
       }
+    }
+  }
+  if (staged) {
+    __syncwarp();
+    // two rows per step, 16 lanes each
+    const int half = lane >> 4, c = lane & 15;
+#pragma unroll 4
+    for (int r = half; r < 32; r += 2) {
+      const bool to_write = __shfl_sync(0xffffffffu, (int)live, r);
+      const size_t dst = __shfl_sync(0xffffffffu, (unsigned long long)qrow, r);
+      if (to_write) out[dst * 16 + c] = *reinterpret_cast<const uint4*>(stage + r * 256 + ((c ^ (r & 15)) << 4));
     }
   }
   if (live) {
@@ -696,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
   Shared* sh = reinterpret_cast<Shared*>(sm + kOffInfo);
   Work w;
   if (!find_work(a, w)) return;                // the same for all threads
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(sh->bars + kKFull + i, 128);
@@ -705,6 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
       mbar_init(sh->bars + kVEmpty + i, 1);
       mbar_init(sh->bars + kSFull + i, 2);
       mbar_init(sh->bars + kPFull + i, 128);
+      mbar_init(sh->bars + kQFull + i, 128);
     }
     mbar_init(sh->bars + kOFull, 2);
     mbar_init(sh->bars + kDrain, 1);
@@ -721,58 +777,32 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  // q: a thread's row, scaled by a power of two, fp16, swizzled
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = any ? sh->tmem : 0;
   const int tile = warp >> 2, m = threadIdx.x & 127;
   const int row = w.row0 + tile * kRows + m;   // of the sequence's rows
   const int token = row / a.G, hq = w.h * a.G + row % a.G;
   const bool live = warp < 8 && token < w.m;
   const size_t qrow = ((size_t)w.c0 + token) * a.Hq + hq;
-  float cs = 0.f;
-  if (warp < 8 && any) {
-    uint32_t x[64], top = 0;
-    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.c.q) + (live ? qrow : 0) * 128);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint4 t = live ? q[i] : make_uint4(0, 0, 0, 0);
-      x[4 * i] = t.x;
-      x[4 * i + 1] = t.y;
-      x[4 * i + 2] = t.z;
-      x[4 * i + 3] = t.w;
-    }
-#pragma unroll
-    for (int i = 0; i < 64; ++i) top = max(top, max(x[i] & 0x7FFFu, (x[i] >> 16) & 0x7FFFu));
-    const int up = min(14 - ((int)(top >> 7) - 127), 127);
-    float mul = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : pow2i(up);
-    if (a.c.scale < 0.f) mul = -mul;
-    cs = fabsf(a.c.scale) * 1.4426950408889634f * pow2i(max(-up, -126));
-    uint8_t* dst = sm + kOffQ + tile * kOperand + m * 128;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      uint32_t f[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) f[u] = pack_f16(bf16lo(x[4 * i + u]) * mul, bf16hi(x[4 * i + u]) * mul);
-      *reinterpret_cast<uint4*>(dst + (i >> 3) * (kOperand / 2) + (((i & 7) ^ (m & 7)) << 4)) =
-          make_uint4(f[0], f[1], f[2], f[3]);
-    }
-    fence_async();
-  }
-  fence_before();
-  __syncthreads();
-  fence_after();
-  const uint32_t tmem = any ? sh->tmem : 0;
   const Waiter wait{&sh->abort, a.polls};
   const int pos = w.pos0 + token;
   if (!any) {
-    if (warp < 8) write_row(a, w, 0, false, true, live, token, hq, RowOut());
+    if (warp < 8) write_row(a, w, 0, nullptr, false, true, live, token, hq, RowOut());
     return;
   }
   {
     if (warp < 8) {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
       const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+      uint8_t* operand = sm + kOffQ + tile * kOperand;
+      const float cs = load_q(a, operand, m, qrow, live);
+      arrive(sh->bars + kQFull + tile);
       RowOut ro;
       const bool ok = softmax_rows(a, w, trow, tile, pos, cs, sh, wait, ro);
-      write_row(a, w, trow + 256 + 128 * tile, true, ok, live, token, hq, ro);
+      // Q has been read: its place holds this warp's 32 rows of output
+      write_row(a, w, trow + 256 + 128 * tile, operand + (warp & 3) * 32 * 256, true, ok, live, token, hq, ro);
     } else if (warp < 12) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
       convert_tiles(a, sh->work.keys, sm, sh, wait);
