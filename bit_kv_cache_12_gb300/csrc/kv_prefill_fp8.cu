@@ -644,35 +644,46 @@ __device__ __forceinline__ bool softmax_rows(const PrefillFp8Args& a, const Work
   }
 }
 
-// q: this thread's row, scaled by a power of two, as fp16 into the swizzled operand;
-// returns the factor that brings a score back to base-2 logits (without 2^eK).
-__device__ __forceinline__ float load_q(const PrefillFp8Args& a, uint8_t* operand, int m, size_t qrow, bool live) {
-  uint32_t x[64], top = 0;
-  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.c.q) + (live ? qrow : 0) * 128);
+// q: the warp's 32 rows, each scaled by a power of two, as fp16 into the swizzled
+// operand (`operand` + 128 bytes per row of the tile, first row m0); returns the
+// factor that brings a score of this thread's row back to base-2 logits (without
+// 2^eK).  Sixteen lanes read a row together (a row per thread cost eight times the
+// wavefronts).
+__device__ __forceinline__ float load_q(const PrefillFp8Args& a, uint8_t* operand, int m0, size_t qrow, bool live) {
+  const int lane = threadIdx.x & 31, c = lane & 15;
+  uint4 x[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint4 t = live ? q[i] : make_uint4(0, 0, 0, 0);
-    x[4 * i] = t.x;
-    x[4 * i + 1] = t.y;
-    x[4 * i + 2] = t.z;
-    x[4 * i + 3] = t.w;
+  for (int i = 0; i < 16; ++i) {               // rows 2 i and 2 i + 1
+    const int r = 2 * i + (lane >> 4);
+    const size_t src = __shfl_sync(0xffffffffu, (unsigned long long)qrow, r);
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (__shfl_sync(0xffffffffu, (int)live, r))
+      x[i] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.c.q) + src * 128)[c];
   }
-#pragma unroll
-  for (int i = 0; i < 64; ++i) top = max(top, max(x[i] & 0x7FFFu, (x[i] >> 16) & 0x7FFFu));
-  const int up = min(14 - ((int)(top >> 7) - 127), 127);
-  float mul = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : pow2i(up);
-  if (a.c.scale < 0.f) mul = -mul;
-  uint8_t* dst = operand + m * 128;
+  int mine = 0;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    uint32_t top = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) top = __vmaxu2(top, w[u] & 0x7FFF7FFFu);
+    top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const int up = min(14 - ((int)(top >> 7) - 127), 127);
+    const int theirs = __shfl_sync(0xffffffffu, up, (lane & 1) << 4);
+    if ((lane >> 1) == i) mine = theirs;       // row `lane` is row 2 (lane / 2) + lane % 2
+    float mul = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : pow2i(up);
+    if (a.c.scale < 0.f) mul = -mul;
     uint32_t f[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) f[u] = pack_f16(bf16lo(x[4 * i + u]) * mul, bf16hi(x[4 * i + u]) * mul);
-    *reinterpret_cast<uint4*>(dst + (i >> 3) * (kOperand / 2) + (((i & 7) ^ (m & 7)) << 4)) =
+    for (int u = 0; u < 4; ++u) f[u] = pack_f16(bf16lo(w[u]) * mul, bf16hi(w[u]) * mul);
+    const int m = m0 + 2 * i + (lane >> 4);
+    *reinterpret_cast<uint4*>(operand + (c >> 3) * (kOperand / 2) + m * 128 + (((c & 7) ^ (m & 7)) << 4)) =
         make_uint4(f[0], f[1], f[2], f[3]);
   }
   fence_async();
-  return fabsf(a.c.scale) * 1.4426950408889634f * pow2i(max(-up, -126));
+  return fabsf(a.c.scale) * 1.4426950408889634f * pow2i(max(-mine, -126));
 }
 
 // A row's result: normalised to the output, or as a part of a split.  `stage`:
@@ -797,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
       const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
       uint8_t* operand = sm + kOffQ + tile * kOperand;
-      const float cs = load_q(a, operand, m, qrow, live);
+      const float cs = load_q(a, operand, 32 * (warp & 3), qrow, live);
       arrive(sh->bars + kQFull + tile);
       RowOut ro;
       const bool ok = softmax_rows(a, w, trow, tile, pos, cs, sh, wait, ro);
