@@ -52,6 +52,7 @@ struct DecodeFp8Args {
   unsigned* tickets;
   int* err;
   int polls;
+  int stall;                                   // test hook: warp 0 of CTA 0 never starts its first copy
 };
 
 // The tiles a query at position n - 1 sees: the first `ns`, then those from
@@ -159,7 +160,11 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
 #pragma unroll
   for (int k = 0; k < kStages; ++k) {
     const long long t = __shfl_sync(0xffffffffu, cur, k);
-    if (lane == 0 && k < mine) issue(k, t);
+    if (lane != 0 || k >= mine) continue;
+    if (a.stall && k == 0 && blockIdx.x == 0 && warp == 0)
+      mbar_expect_tx(bar, kFp8TileBytes);
+    else
+      issue(k, t);
   }
   int exps = exps_of(cur);
 
@@ -485,7 +490,7 @@ size_t decode_fp8_workspace(const Pool& p, int B, int max_len) {
 cudaError_t launch_decode_fp8(const Pool& p, const Fp8Store& f, int layer, int B, const AttnCall& c, cudaStream_t s) {
   DecodeFp8Args a{fp8_layer(p, f, layer), c, B, p.cfg.num_q_heads, splits(p, B, c.max_len, c.window, c.n_sink),
                   p.tickets + (size_t)layer * p.cfg.max_seqs * p.cfg.num_kv_heads, p.err,
-                  p.test_wait_polls > 0 ? p.test_wait_polls : kPolls};
+                  p.test_wait_polls > 0 ? p.test_wait_polls : kPolls, p.test_stall_first_copy};
   switch (p.G) {
     case 1: return launch_t<1>(a, s);
     case 2: return launch_t<2>(a, s);

@@ -103,6 +103,7 @@ struct PrefillFp8Args {
   int n_seqs, max_q, Hq, G, n_split, q_blocks;
   int* err;
   int polls;
+  int stall;                                   // test hook: CTA 0's walker never hands over its first pass
 };
 
 // ---- tcgen05 ----------------------------------------------------------------
@@ -693,9 +694,10 @@ __device__ __forceinline__ void write_row(const PrefillFp8Args& a, const Work& w
                                           bool ok, bool live, int token, int hq, const RowOut& ro) {
   const int lane = threadIdx.x & 31;
   const size_t qrow = ((size_t)w.c0 + token) * a.Hq + hq;
-  const bool empty = ro.l == 0.f;
-  const float f = !ok || ro.poison ? __uint_as_float(0x7FC00000u) : (empty ? 0.f : 1.f / ro.l);
-  const float lse = empty ? -INFINITY : (ro.M + log2f(ro.l)) * kLn2;
+  const float nan = __uint_as_float(0x7FC00000u);
+  const bool empty = ok && !ro.poison && ro.l == 0.f;
+  const float f = !ok || ro.poison ? nan : (empty ? 0.f : 1.f / ro.l);
+  const float lse = !ok ? nan : (ro.l == 0.f ? -INFINITY : (ro.M + log2f(ro.l)) * kLn2);
   float* part = static_cast<float*>(a.c.ws) +
                 (((size_t)w.s * a.max_q + token) * a.Hq + hq) * a.n_split * 132 + (size_t)w.split * 132;
   uint4* out = static_cast<uint4*>(a.c.out);
@@ -819,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
       convert_tiles(a, sh->work.keys, sm, sh, wait);
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-      if (warp == 13) walk_tiles(a, sh->work, sh, wait);
+      if (warp == 13 && !(a.stall && blockIdx.x == 0)) walk_tiles(a, sh->work, sh, wait);
       if (warp == 12) issue_products(__shfl_sync(0xffffffffu, tmem, 0), sm, sh, wait);
     }
     __syncwarp();
@@ -899,7 +901,7 @@ cudaError_t launch_prefill_fp8(const Pool& p, const Fp8Store& f, int layer, int 
   if (max_q == 0) return cudaSuccess;
   PrefillFp8Args a{fp8_layer(p, f, layer), c, cu_q, n_seqs, max_q, p.cfg.num_q_heads, p.G,
                    splits(p, n_seqs, max_q, c.max_len, c.window, c.n_sink), (int)q_blocks(p, max_q), p.err,
-                   p.test_wait_polls > 0 ? p.test_wait_polls : kPolls};
+                   p.test_wait_polls > 0 ? p.test_wait_polls : kPolls, p.test_stall_first_copy};
   const long long ctas = (long long)a.q_blocks * n_seqs * a.L.Hkv * a.n_split;
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(prefill_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);

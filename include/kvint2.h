@@ -366,10 +366,13 @@ kv_status_t kv_decode_attention_noalloc(kv_pool_t* pool, int32_t layer, int32_t 
  * KV_DEVERR_TIMEOUT, every warp of that CTA leaves its loop, the CTA waits
  * (bounded) for the loads and products it did start and returns (the
  * history it was to write is left incomplete).  No copy is left in flight,
- * nothing faults and nothing hangs.  max_polls > 0 replaces the default poll
- * limit of those waits (about a second) for the pool's decode and bulk
- * append calls; 0 restores it.  enable = 0 restores normal calls.  Not for
- * production use. */
+ * nothing faults and nothing hangs.  On an FP8 pool the first warp of
+ * kv_decode_attention_fp8's first CTA waits for a copy that is never started,
+ * and kv_prefill_attention_fp8's first CTA for keys that are never handed over;
+ * both end the same way (the prompt rows of that CTA become NaN).  max_polls > 0
+ * replaces the default poll limit of those waits (about a second) for the pool's
+ * decode, prompt and bulk append calls; 0 restores it.  enable = 0 restores
+ * normal calls.  Not for production use. */
 kv_status_t kv_debug_stall_first_copy(kv_pool_t* pool, int32_t enable, int32_t max_polls);
 
 /* ---------------------------------------------------------------------------
