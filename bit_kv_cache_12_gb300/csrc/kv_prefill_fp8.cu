@@ -23,8 +23,9 @@
 //                    (two stages each of K and V)
 //   warp 12          issues the products: S = Q K^T from shared memory, O += P V
 //                    with P from tensor memory and V token-major as it is stored
-//   warp 13          (14, 15 idle) walks the key tiles ahead of the converters:
-//                    page ids, exponents, block addresses into a ring of records
+//   warp 13          (14, 15 idle) walks the items and their key tiles ahead of
+//                    the converters: page ids, exponents, block addresses into a
+//                    ring of records
 // Tensor memory: S0, S1 (P over them), O0, O1, 128 columns each.
 // Hidden keys: a tile that some row sees only in part is masked by select after
 // the product (a NaN in a hidden K row never enters), its V rows that hold NaN
@@ -47,7 +48,7 @@ constexpr int kBlocks = kKeys / kTile;
 constexpr int kThreads = 16 * 32;              // four warpgroups
 // registers per thread of the softmax, converter and issuer warpgroups: they
 // share the launch's 128 each
-constexpr int kSoftRegs = 176, kConvRegs = 120, kIssueRegs = 40;
+constexpr int kSoftRegs = 184, kConvRegs = 96, kIssueRegs = 48;
 static_assert(2 * kSoftRegs + kConvRegs + kIssueRegs <= 4 * 128, "setmaxnreg.inc draws on the launch's registers");
 constexpr int kPolls = 1 << 20;
 constexpr int kMaxSplits = 32;
@@ -66,19 +67,25 @@ struct Pass {
   int t0;                                      // first key
   uint32_t blocks;                             // 16-token blocks present in this pass
   float fk, ev;                                // 2^eK, eV of the operands
-  int last;                                    // no pass follows
+  int last;                                    // the item's last pass
   int partial;                                 // some row sees the tile only in part
-  int pad[2];
+  int keys;                                    // keys from here on are hidden from every row
+  int stop;                                    // not a pass: no item follows
   uint32_t nan[4];                             // its V rows that hold NaN, zeroed (by the converters)
   int tile[kBlocks];                           // stored tile of each block (0 for an absent one)
   uint32_t mulk[kBlocks], mulv[kBlocks];       // fp16x2 2^(e - eK), 2^(e - eV)
 };
 constexpr int kRing = 8;
 
-enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kOFull = 12, kDrain = 13, kQFull = 14, kPass = 16, kBars = 16 + kRing };
+constexpr int kItems = 4;                      // ring of items
 
-// The rows of a CTA and the key tiles they see.
+enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kOFull = 12, kDrain = 13, kQFull = 14,
+       kCancel = 16, kItem = 17, kFree = kItem + kItems, kPass = kFree + kItems, kBars = kPass + kRing };
+
+// An item: a block of rows and the key tiles they see.
+enum { kKeyed = 0, kNoKeys = 1, kStop = 2 };   // rows with keys, rows that see none, no item
 struct Work {
+  int state;
   int s, h, c0, m, n, row0, split;             // sequence, KV head, first q row, queries, keys, first row of the block
   int pos0;                                    // position of the sequence's query 0
   int first, keys;                             // position of the first row; keys from here on are hidden from every row
@@ -88,7 +95,8 @@ struct Work {
 
 struct Shared {
   Pass pass[kRing];
-  Work work;                                   // for the warps with few registers
+  uint4 cancel;                                // what the scheduler answered
+  Work work[kItems];
   uint64_t bars[kBars];
   uint32_t tmem;
   int abort;
@@ -222,9 +230,9 @@ __device__ __forceinline__ uint32_t below(int x, int from) {
   return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
 }
 
-__device__ __forceinline__ bool find_work(const PrefillFp8Args& a, Work& w) {
+// Item x of the grid; false where it has no rows (the whole warp calls this).
+__device__ __forceinline__ bool find_work(const PrefillFp8Args& a, int x, Work& w) {
   // blocks of a sequence from its last (most keys) to its first
-  int x = blockIdx.x;
   w.split = x % a.n_split;
   x /= a.n_split;
   w.h = x % a.L.Hkv;
@@ -234,7 +242,7 @@ __device__ __forceinline__ bool find_work(const PrefillFp8Args& a, Work& w) {
   w.c0 = a.cu[w.s];
   w.m = a.cu[w.s + 1] - w.c0;
   w.n = a.c.seq_len[w.s];
-  const bool first = threadIdx.x == 0 && blk == 0 && w.split == 0 && w.h == 0;
+  const bool first = (threadIdx.x & 31) == 0 && blk == 0 && w.split == 0 && w.h == 0;
   if (w.m < 0 || w.m > a.max_q) {
     if (first) flag_error(a.err, KV_DEVERR_SEQ_RANGE);
     return false;
@@ -258,6 +266,7 @@ __device__ __forceinline__ bool find_work(const PrefillFp8Args& a, Work& w) {
   const int per = (total + a.n_split - 1) / a.n_split;
   w.i0 = min(w.split * per, total);
   w.i1 = min(w.i0 + per, total);
+  w.state = w.i0 < w.i1 ? kKeyed : kNoKeys;
   return true;
 }
 
@@ -301,8 +310,7 @@ __device__ __forceinline__ uint32_t half_pow2(int d) {
 __device__ __forceinline__ bool has_nan(uint32_t w) { return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0; }
 
 // K and V of every pass.
-__device__ __forceinline__ void convert_tiles(const PrefillFp8Args& a, int keys, uint8_t* sm, Shared* sh,
-                                              const Waiter& wait) {
+__device__ __forceinline__ void convert_tiles(const PrefillFp8Args& a, uint8_t* sm, Shared* sh, const Waiter& wait) {
   const int tid = threadIdx.x & 127;
   // this thread's piece of a stored block of K and of V: token and run of 16
   // channels, chosen so that eight lanes store to eight different banks
@@ -312,14 +320,17 @@ __device__ __forceinline__ void convert_tiles(const PrefillFp8Args& a, int keys,
   const uint8_t* vsrc = a.L.codes + 2048 + ((tid & 1) + 2 * (tid >> 6)) * 512 + vrun * 64 + ((tid & 7) >> 1) * 16;
   uint4 k[kBlocks], v[kBlocks];                // a pass ahead
   auto load = [&](uint4 (&x)[kBlocks], const uint8_t* src, const Pass& p) {
-    int t[kBlocks];
 #pragma unroll
-    for (int u = 0; u < kBlocks; u += 4) *reinterpret_cast<int4*>(t + u) = *reinterpret_cast<const int4*>(p.tile + u);
-#pragma unroll
-    for (int u = 0; u < kBlocks; ++u) x[u] = ld_stream_v4(src + (size_t)t[u] * kFp8TileBytes);
+    for (int u = 0; u < kBlocks; u += 4) {
+      const int4 t = *reinterpret_cast<const int4*>(p.tile + u);
+      x[u] = ld_stream_v4(src + (size_t)t.x * kFp8TileBytes);
+      x[u + 1] = ld_stream_v4(src + (size_t)t.y * kFp8TileBytes);
+      x[u + 2] = ld_stream_v4(src + (size_t)t.z * kFp8TileBytes);
+      x[u + 3] = ld_stream_v4(src + (size_t)t.w * kFp8TileBytes);
+    }
   };
   auto ready = [&](int it) { return __all_sync(0xffffffffu, wait(sh->bars + kPass + (it & (kRing - 1)), (it / kRing) & 1)); };
-  if (!ready(0)) return;
+  if (!ready(0) || sh->pass[0].stop) return;
   load(k, ksrc, sh->pass[0]);
   load(v, vsrc, sh->pass[0]);
   for (int it = 0;; ++it) {
@@ -329,17 +340,14 @@ __device__ __forceinline__ void convert_tiles(const PrefillFp8Args& a, int keys,
     const Pass& next = sh->pass[(it + 1) & (kRing - 1)];
     const bool partial = p.partial != 0, last = p.last != 0;
     const uint32_t present = p.blocks;
-    const int t0 = p.t0;
+    const int t0 = p.t0, keys = p.keys;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    uint32_t mul[kBlocks];
     if (it >= 2 && !__all_sync(0xffffffffu, wait(sh->bars + kKEmpty + stage, ph))) return;
     uint8_t* sk = sm + kOffK + stage * kOperand;
 #pragma unroll
-    for (int u = 0; u < kBlocks; u += 4) *reinterpret_cast<uint4*>(mul + u) = *reinterpret_cast<const uint4*>(p.mulk + u);
-#pragma unroll
     for (int u = 0; u < kBlocks; ++u) {
       if (partial && !((present >> u) & 1)) k[u] = zero;
-      store_run(sk, kTile * u + ktok, krun, k[u], mul[u]);
+      store_run(sk, kTile * u + ktok, krun, k[u], p.mulk[u]);
     }
     fence_async();
     arrive(sh->bars + kKFull + stage);
@@ -350,8 +358,6 @@ __device__ __forceinline__ void convert_tiles(const PrefillFp8Args& a, int keys,
     }
     if (it >= 2 && !__all_sync(0xffffffffu, wait(sh->bars + kVEmpty + stage, ph))) return;
     uint8_t* sv = sm + kOffV + stage * kOperand;
-#pragma unroll
-    for (int u = 0; u < kBlocks; u += 4) *reinterpret_cast<uint4*>(mul + u) = *reinterpret_cast<const uint4*>(p.mulv + u);
     if (partial) {
 #pragma unroll
       for (int u = 0; u < kBlocks; ++u) {
@@ -364,21 +370,40 @@ __device__ __forceinline__ void convert_tiles(const PrefillFp8Args& a, int keys,
       }
     }
 #pragma unroll
-    for (int u = 0; u < kBlocks; ++u) store_run(sv, kTile * u + vtok, vrun, v[u], mul[u]);
+    for (int u = 0; u < kBlocks; ++u) store_run(sv, kTile * u + vtok, vrun, v[u], p.mulv[u]);
     fence_async();
     arrive(sh->bars + kVFull + stage);
-    if (last) return;
+    if (last) {                                // the next item's first pass may be long in coming
+      if (!ready(it + 1) || next.stop) return;
+      load(k, ksrc, next);
+    }
     load(v, vsrc, next);
   }
 }
 
 // ---- walker (one warp) ----------------------------------------------------------
 
-// The passes: a tile's blocks whose exponents lie within 7 of the first one left
+// Whether the record of pass n may be written: pass n - 8 was last read by the
+// softmax of pass n - 7, over when K of pass n - 4 has its stage.
+__device__ __forceinline__ bool pass_free(Shared* sh, const Waiter& wait, int n) {
+  bool ok = true;
+  for (int spin = 0; n >= kRing && *reinterpret_cast<volatile int*>(&sh->converted) < n - 3; ++spin) {
+    if (spin >= wait.polls || *reinterpret_cast<volatile int*>(wait.abort)) {
+      ok = false;
+      break;
+    }
+    __nanosleep(100);
+  }
+  ok = __all_sync(0xffffffffu, ok);
+  if (!ok) *reinterpret_cast<volatile int*>(wait.abort) = 1;
+  return ok;
+}
+
+// The passes of an item: a tile's blocks whose exponents lie within 7 of the first one left
 // make a pass.  Lane u < 8 holds block u: its stored tile (-1: absent) and
 // exponents for tile i, its exponents in flight for tile i + 1, its page id in
 // flight for tile i + 2; no load waits where it is issued.
-__device__ __forceinline__ void walk_tiles(const PrefillFp8Args& a, const Work& w, Shared* sh, const Waiter& wait) {
+__device__ __forceinline__ bool walk_item(const PrefillFp8Args& a, const Work& w, Shared* sh, const Waiter& wait, int& n) {
   const int lane = threadIdx.x & 31;
   const int tpp = a.L.P / kTile, shift = tpp >> 1;
   const int32_t* pt = a.c.pt + (size_t)w.s * a.c.max_pages;
@@ -398,7 +423,6 @@ __device__ __forceinline__ void walk_tiles(const PrefillFp8Args& a, const Work& 
   auto exps_of = [&](int st) -> int { return *reinterpret_cast<const uint16_t*>(a.L.exps + (size_t)max(st, 0) * 2); };
   int st1 = stored(w.i0, page_of(w.i0));
   int ex1 = exps_of(st1), pid2 = page_of(w.i0 + 1);
-  int n = 0;                                   // passes written
   for (int i = w.i0; i < w.i1; ++i) {
     const int st = st1, ex = ex1, t0 = w.tile(i) * kKeys;
     st1 = stored(i + 1, pid2);
@@ -418,20 +442,7 @@ __device__ __forceinline__ void walk_tiles(const PrefillFp8Args& a, const Work& 
         mv = __reduce_max_sync(0xffffffffu, in ? ev : -1000);
         left &= ~now;
       }
-      // the record of pass n - 8 was last read by the softmax of pass n - 7,
-      // over when K of pass n - 4 has its stage
-      bool ok = true;
-      for (int spin = 0; n >= kRing && *reinterpret_cast<volatile int*>(&sh->converted) < n - 3; ++spin) {
-        if (spin >= wait.polls || *reinterpret_cast<volatile int*>(wait.abort)) {
-          ok = false;
-          break;
-        }
-        __nanosleep(100);
-      }
-      if (!__all_sync(0xffffffffu, ok)) {
-        *reinterpret_cast<volatile int*>(wait.abort) = 1;
-        return;
-      }
+      if (!pass_free(sh, wait, n)) return false;
       Pass& p = sh->pass[n & (kRing - 1)];
       if (lane < kBlocks) {
         const bool in = (now >> lane) & 1;
@@ -446,6 +457,8 @@ __device__ __forceinline__ void walk_tiles(const PrefillFp8Args& a, const Work& 
         p.fk = pow2i(max(min(mk, 127), -126));
         p.ev = (float)mv;
         p.last = i + 1 == w.i1 && !left;
+        p.keys = w.keys;
+        p.stop = 0;
         p.partial = now != 0xFFu || t0 + kKeys - 1 > w.first ||
                     (a.c.window && t0 < w.keys - a.c.window && t0 + kKeys > w.sinks);
       }
@@ -454,6 +467,65 @@ __device__ __forceinline__ void walk_tiles(const PrefillFp8Args& a, const Work& 
       ++n;
     } while (left);
   }
+  return true;
+}
+
+// The items: this CTA's own, then those of CTAs that have not been launched yet,
+// asked of the hardware's scheduler one ahead.  So a CTA lives as long as there is
+// work, the walker and the converters are at the next item's keys while the
+// softmax writes the last one's rows, and blocks of unequal length even out.
+__device__ __forceinline__ void walk(const PrefillFp8Args& a, Shared* sh, const Waiter& wait) {
+  const int lane = threadIdx.x & 31;
+  auto ready = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(sh->bars + bar, parity)) != 0; };
+  auto publish = [&](const Work& w, int item) -> bool {
+    const int slot = item & (kItems - 1);
+    if (item >= kItems && !ready(kFree + slot, (item / kItems - 1) & 1)) return false;
+    if (lane == 0) {
+      sh->work[slot] = w;
+      arrive(sh->bars + kItem + slot);
+    }
+    __syncwarp();
+    return true;
+  };
+  int x = blockIdx.x, items = 0, passes = 0;
+  bool ok = true;
+  for (int asked = 0;; ++asked) {
+    if (lane == 0) {
+      fence_async();
+      mbar_expect_tx(sh->bars + kCancel, 16);
+      asm volatile(
+          "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+              smem_u32(&sh->cancel)),
+          "r"(smem_u32(sh->bars + kCancel))
+          : "memory");
+    }
+    __syncwarp();
+    Work w;
+    if (find_work(a, x, w)) ok = publish(w, items++) && (w.state != kKeyed || walk_item(a, w, sh, wait, passes));
+    // the answer is waited for even when something failed: it is written to shared memory
+    if (!__all_sync(0xffffffffu, mbar_wait(sh->bars + kCancel, asked & 1, kPolls))) {
+      *reinterpret_cast<volatile int*>(wait.abort) = 1;
+      return;
+    }
+    if (!ok) return;
+    int got;
+    asm volatile(
+        "{ .reg .pred p; .reg .b128 h; ld.shared.b128 h, [%2]; "
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h; selp.b32 %0, 1, 0, p; "
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h; }"
+        : "=r"(got), "+r"(x)
+        : "r"(smem_u32(&sh->cancel))
+        : "memory");
+    if (!__all_sync(0xffffffffu, got)) break;
+  }
+  Work stop{};
+  stop.state = kStop;
+  if (!publish(stop, items) || !pass_free(sh, wait, passes)) return;
+  if (lane == 0) {
+    sh->pass[passes & (kRing - 1)].stop = 1;
+    arrive(sh->bars + kPass + (passes & (kRing - 1)));
+  }
+  __syncwarp();
 }
 
 // ---- product issuer (one warp) ----------------------------------------------------
@@ -488,67 +560,94 @@ __device__ __forceinline__ void issue_products(uint32_t tmem, uint8_t* sm, Share
     }
     __syncwarp();
   };
-  if (!ready(kKFull, 0)) return;
-  for (int tile = 0; tile < 2; ++tile) {
-    if (!ready(kQFull + tile, 0)) return;
-    fence_after();
-    scores(tile, 0);
-  }
-  for (int it = 0;; ++it) {
-    const int stage = it & 1;
-    const bool last = sh->pass[it & (kRing - 1)].last != 0;
-    // V, and the K of the next scores, long since there: looked at before P is due
-    if (!ready(kVFull + stage, (it >> 1) & 1)) return;
-    if (!last && !ready(kKFull + (stage ^ 1), ((it + 1) >> 1) & 1)) return;
+  int g = 0, keyed = 0;                        // passes and items with keys so far
+  for (int item = 0;; ++item) {
+    const int slot = item & (kItems - 1);
+    if (!ready(kItem + slot, (item / kItems) & 1)) return;
+    const int state = sh->work[slot].state;
+    if (state == kStop) return;
+    if (state == kKeyed) {
+      if (!ready(kKFull + (g & 1), (g >> 1) & 1)) return;
 #pragma unroll 1
-    for (int tile = 0; tile < 2; ++tile) {
-      if (!ready(kPFull + tile, it & 1)) return;
-      fence_after();
-      if (elect_one()) {
-        uint64_t v = v0 + ((stage * kOperand) >> 4);
-        uint32_t p = tmem + 128 * tile;
-        const uint32_t d = tmem + 256 + 128 * tile;
+      for (int tile = 0; tile < 2; ++tile) {
+        if (!ready(kQFull + tile, keyed & 1)) return;
+        fence_after();
+        scores(tile, g & 1);
+      }
+      bool last = false;
+      for (int it = 0; !last; ++it, ++g) {
+        const int stage = g & 1;
+        last = sh->pass[g & (kRing - 1)].last != 0;
+        // V, and the K of the next scores, long since there: looked at before P is due
+        if (!ready(kVFull + stage, (g >> 1) & 1)) return;
+        if (!last && !ready(kKFull + (stage ^ 1), ((g + 1) >> 1) & 1)) return;
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
+        for (int tile = 0; tile < 2; ++tile) {
+          if (!ready(kPFull + tile, g & 1)) return;
+          fence_after();
+          if (elect_one()) {
+            uint64_t v = v0 + ((stage * kOperand) >> 4);
+            uint32_t p = tmem + 128 * tile;
+            const uint32_t d = tmem + 256 + 128 * tile;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)       // 16 tokens: 8 columns of P, 16 rows of V
-            mma_ts(d, p + 8 * ks, v + ((ks * 2048) >> 4), it | half | ks);
-          p += 32;
-          v += (4 * 2048) >> 4;
+              for (int ks = 0; ks < 4; ++ks)   // 16 tokens: 8 columns of P, 16 rows of V
+                mma_ts(d, p + 8 * ks, v + ((ks * 2048) >> 4), it | half | ks);
+              p += 32;
+              v += (4 * 2048) >> 4;
+            }
+            if (tile == 1) commit(sh->bars + kVEmpty + stage);
+          }
+          __syncwarp();
+          if (!last) scores(tile, stage ^ 1);
         }
-        if (tile == 1) commit(sh->bars + kVEmpty + stage);
+      }
+      if (elect_one()) {
+        arrive(sh->bars + kOFull);             // a release after this warp saw the last V's record
+        commit(sh->bars + kOFull);
       }
       __syncwarp();
-      if (last) continue;
-      scores(tile, stage ^ 1);
+      ++keyed;
     }
-    if (last) break;
+    if (elect_one()) arrive(sh->bars + kFree + slot);
+    __syncwarp();
   }
-  if (elect_one()) {
-    commit(sh->bars + kOFull);
-    arrive(sh->bars + kOFull);
-  }
-  __syncwarp();
 }
 
 // ---- softmax (a thread owns a row) ---------------------------------------------
+
+// Where row i of an item's block comes from and goes to.
+struct Row {
+  int token, hq;
+  bool live;
+  size_t qrow;
+  __device__ __forceinline__ Row(const PrefillFp8Args& a, const Work& w, int i) {
+    const int row = w.row0 + i;                // of the sequence's rows
+    token = row / a.G;
+    hq = w.h * a.G + row % a.G;
+    live = token < w.m;
+    qrow = ((size_t)w.c0 + token) * a.Hq + hq;
+  }
+};
 
 struct RowOut {
   float M = kNoRef, l = 0.f;
   bool poison = false;
 };
 
-__device__ __forceinline__ bool softmax_rows(const PrefillFp8Args& a, const Work& w, uint32_t trow, int tile, int pos,
-                                             float cs, Shared* sh, const Waiter& wait, RowOut& ro) {
+// g: the pass, counted over the CTA's items; keyed: the items with keys before this one
+__device__ __forceinline__ bool softmax_rows(const PrefillFp8Args& a, int sinks, uint32_t trow, int tile, int pos,
+                                             float cs, Shared* sh, const Waiter& wait, int& g, int keyed, RowOut& ro) {
   const uint32_t ts = trow + 128 * tile, to = trow + 256 + 128 * tile;
   uint32_t see[4] = {0, 0, 0, 0};
   bool check = false;                          // `see` of the previous tile is to be held against its NaN rows
-  for (int it = 0;; ++it) {
-    if (!__all_sync(0xffffffffu, wait(sh->bars + kSFull + tile, it & 1))) return false;
+  for (int it = 0;; ++it, ++g) {
+    if (!__all_sync(0xffffffffu, wait(sh->bars + kSFull + tile, g & 1))) return false;
     fence_after();
-    const Pass& info = sh->pass[it & (kRing - 1)];
+    const Pass& info = sh->pass[g & (kRing - 1)];
     if (check) {
-      const Pass& old = sh->pass[(it - 1) & (kRing - 1)];
+      const Pass& old = sh->pass[(g - 1) & (kRing - 1)];
 #pragma unroll
       for (int q = 0; q < 4; ++q) ro.poison |= (old.nan[q] & see[q]) != 0;
     }
@@ -564,7 +663,7 @@ __device__ __forceinline__ bool softmax_rows(const PrefillFp8Args& a, const Work
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t m = below(pos + 1 - t0, 32 * q);
-        if (a.c.window) m &= ~below(pos + 1 - a.c.window - t0, 32 * q) | below(w.sinks - t0, 32 * q);
+        if (a.c.window) m &= ~below(pos + 1 - a.c.window - t0, 32 * q) | below(sinks - t0, 32 * q);
         m &= ((blocks >> (2 * q)) & 1 ? 0xFFFFu : 0u) | ((blocks >> (2 * q + 1)) & 1 ? 0xFFFF0000u : 0u);
         see[q] = m;
       }
@@ -634,15 +733,28 @@ __device__ __forceinline__ bool softmax_rows(const PrefillFp8Args& a, const Work
     fence_before();
     arrive(sh->bars + kPFull + tile);
     if (last) {
-      if (!__all_sync(0xffffffffu, wait(sh->bars + kOFull, 0))) return false;
+      if (!__all_sync(0xffffffffu, wait(sh->bars + kOFull, keyed & 1))) return false;
       fence_after();
       if (check) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) ro.poison |= (info.nan[q] & see[q]) != 0;
       }
+      ++g;
       return true;
     }
   }
+}
+
+// Whether `ok` holds for the 128 threads of a tile (a barrier for them; every path
+// of the softmax warps comes here once per item).
+__device__ __forceinline__ bool tile_and(int tile, bool ok) {
+  int r;
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.b32 p, %1, 0; bar.red.and.pred q, %2, 128, p; selp.b32 %0, 1, 0, q; }"
+      : "=r"(r)
+      : "r"((int)ok), "r"(1 + tile)
+      : "memory");
+  return r != 0;
 }
 
 // q: the warp's 32 rows, each scaled by a power of two, as fp16 into the swizzled
@@ -691,9 +803,10 @@ __device__ __forceinline__ float load_q(const PrefillFp8Args& a, uint8_t* operan
 // 8 KB of shared memory for the warp's 32 rows, from which they are written
 // 256 bytes at a time (a row per thread straight from registers took 2.6 us).
 __device__ __forceinline__ void write_row(const PrefillFp8Args& a, const Work& w, uint32_t to, uint8_t* stage, bool any,
-                                          bool ok, bool live, int token, int hq, const RowOut& ro) {
-  const int lane = threadIdx.x & 31;
-  const size_t qrow = ((size_t)w.c0 + token) * a.Hq + hq;
+                                          bool ok, const Row& row, const RowOut& ro) {
+  const int lane = threadIdx.x & 31, token = row.token, hq = row.hq;
+  const size_t qrow = row.qrow;
+  const bool live = row.live;
   const float nan = __uint_as_float(0x7FC00000u);
   const bool empty = ok && !ro.poison && ro.l == 0.f;
   const float f = !ok || ro.poison ? nan : (empty ? 0.f : 1.f / ro.l);
@@ -762,8 +875,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   Shared* sh = reinterpret_cast<Shared*>(sm + kOffInfo);
-  Work w;
-  if (!find_work(a, w)) return;                // the same for all threads
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -777,14 +888,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
     }
     mbar_init(sh->bars + kOFull, 2);
     mbar_init(sh->bars + kDrain, 1);
+    mbar_init(sh->bars + kCancel, 1);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(sh->bars + kItem + i, 1);
+      mbar_init(sh->bars + kFree + i, 2 * kRows + 1);
+    }
     for (int i = 0; i < kRing; ++i) mbar_init(sh->bars + kPass + i, 1);
     mbar_fence_init();
     sh->abort = 0;
     sh->converted = 0;
-    sh->work = w;
   }
-  const bool any = w.i0 < w.i1;                // this CTA has keys at all
-  if (warp == 12 && any) {
+  if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh->tmem)),
                  "r"(512)
                  : "memory");
@@ -793,39 +907,46 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = any ? sh->tmem : 0;
-  const int tile = warp >> 2, m = threadIdx.x & 127;
-  const int row = w.row0 + tile * kRows + m;   // of the sequence's rows
-  const int token = row / a.G, hq = w.h * a.G + row % a.G;
-  const bool live = warp < 8 && token < w.m;
-  const size_t qrow = ((size_t)w.c0 + token) * a.Hq + hq;
+  const uint32_t tmem = sh->tmem;
   const Waiter wait{&sh->abort, a.polls};
-  const int pos = w.pos0 + token;
-  if (!any) {
-    if (warp < 8) write_row(a, w, 0, nullptr, false, true, live, token, hq, RowOut());
-    return;
-  }
-  {
-    if (warp < 8) {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-      const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-      uint8_t* operand = sm + kOffQ + tile * kOperand;
-      const float cs = load_q(a, operand, 32 * (warp & 3), qrow, live);
-      arrive(sh->bars + kQFull + tile);
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    const int tile = warp >> 2, m = threadIdx.x & 127;
+    const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    bool ok = true;
+    int g = 0, keyed = 0;
+    for (int item = 0;; ++item) {
+      const int slot = item & (kItems - 1);
+      if (ok) ok = __all_sync(0xffffffffu, wait(sh->bars + kItem + slot, (item / kItems) & 1));
+      // the tile's four warps go on together, their staged rows written: Q takes that place
+      if (!tile_and(tile, ok)) break;
+      const Work& w = sh->work[slot];
+      const int state = w.state;
+      if (state == kStop) break;
       RowOut ro;
-      const bool ok = softmax_rows(a, w, trow, tile, pos, cs, sh, wait, ro);
+      if (state == kKeyed) {
+        const Row r(a, w, tile * kRows + m);
+        const float cs = load_q(a, sm + kOffQ + tile * kOperand, 32 * (warp & 3), r.qrow, r.live);
+        arrive(sh->bars + kQFull + tile);
+        ok = softmax_rows(a, w.sinks, trow, tile, w.pos0 + r.token, cs, sh, wait, g, keyed, ro);
+        ++keyed;
+      }
+      // (worked out again: kept over the passes, they would cost registers there)
+      asm volatile("" ::: "memory");
+      const Row r(a, w, tile * kRows + m);
       // Q has been read: its place holds this warp's 32 rows of output
-      write_row(a, w, trow + 256 + 128 * tile, operand + (warp & 3) * 32 * 256, true, ok, live, token, hq, ro);
-    } else if (warp < 12) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
-      convert_tiles(a, sh->work.keys, sm, sh, wait);
-    } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-      if (warp == 13 && !(a.stall && blockIdx.x == 0)) walk_tiles(a, sh->work, sh, wait);
-      if (warp == 12) issue_products(__shfl_sync(0xffffffffu, tmem, 0), sm, sh, wait);
+      write_row(a, w, trow + 256 + 128 * tile, sm + kOffQ + tile * kOperand + (warp & 3) * 32 * 256, state == kKeyed, ok, r, ro);
+      arrive(sh->bars + kFree + slot);
     }
-    __syncwarp();
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
+    convert_tiles(a, sm, sh, wait);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if (warp == 13 && !(a.stall && blockIdx.x == 0)) walk(a, sh, wait);
+    if (warp == 12) issue_products(__shfl_sync(0xffffffffu, tmem, 0), sm, sh, wait);
   }
+  __syncwarp();
   fence_before();
   __syncthreads();
   fence_after();
