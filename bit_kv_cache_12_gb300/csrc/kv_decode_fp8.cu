@@ -234,8 +234,9 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
       }
       const float ev = (float)(int8_t)(e2 >> 8), fk = exp2f((float)(int8_t)(e2 & 0xFF));
       const float c0 = cs0 * fk, c1 = cs1 * fk;
-      float x0 = fmaf(sa[0] + sb[0], c0, ev), x1 = fmaf(sa[1] + sb[1], c1, ev);   // token r, heads 2j, 2j + 1
-      float x2 = fmaf(sa[2] + sb[2], c0, ev), x3 = fmaf(sa[3] + sb[3], c1, ev);   // token r + 8
+      const float s0 = sa[0] + sb[0], s1 = sa[1] + sb[1];      // token r, heads 2j, 2j + 1
+      const float s2 = sa[2] + sb[2], s3 = sa[3] + sb[3];      // token r + 8
+      float x0 = fmaf(s0, c0, ev), x1 = fmaf(s1, c1, ev), x2 = fmaf(s2, c0, ev), x3 = fmaf(s3, c1, ev);
       if (vis != 0xFFFFu) {                    // hidden tokens: no weight, and codes of zero
         if (!((vis >> r) & 1)) x0 = x1 = -INFINITY;
         if (!((vis >> (r + 8)) & 1)) x2 = x3 = -INFINITY;
@@ -262,7 +263,11 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
           o[i][3] *= f1;
         }
       }
-      const float w0 = exp2_neg(x0 - M0), w1 = exp2_neg(x1 - M1), w2 = exp2_neg(x2 - M0), w3 = exp2_neg(x3 - M1);
+      // once more against M: x was rounded at eV's size, ev - M is exact near the largest weight
+      const float d0 = ev - M0, d1 = ev - M1;
+      auto weight = [](float x, float y) { return x == -INFINITY ? 0.f : exp2_neg(y); };   // -inf: hidden
+      const float w0 = weight(x0, fmaf(s0, c0, d0)), w1 = weight(x1, fmaf(s1, c1, d1));
+      const float w2 = weight(x2, fmaf(s2, c0, d0)), w3 = weight(x3, fmaf(s3, c1, d1));
       const float fv = exp2f(-ev);
       l0 = fmaf(w0 + w2, fv, l0);
       l1 = fmaf(w1 + w3, fv, l1);
@@ -342,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
     if (a.n_split == 1) {
       const float y = l == 0.f ? 0.f : s / l;
       out[g * 128 + c] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
-      if (c == 0 && lse) lse[g] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+      if (c == 0 && lse) lse[g] = lse_of(M, l);
     } else {
       float* p = parts + ((size_t)split * G + g) * kPart;
       p[4 + c] = s;
@@ -407,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
     l = warp_sum_xor(l, 1);
     if (lane == 0) {
       sl[g] = l;
-      if (lse) lse[g] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+      if (lse) lse[g] = lse_of(M, l);
     }
   }
   __syncthreads();

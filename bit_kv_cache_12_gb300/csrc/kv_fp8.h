@@ -66,6 +66,15 @@ struct AttnCall {
   void* ws;
 };
 
+// ln(2^M l): M stands near -eV and log2 l near eV (up to 64), so l's exponent is
+// added to M before its mantissa's logarithm (fp32 near 64 has steps of 2^-18).
+__device__ __forceinline__ float lse_of(float M, float l) {
+  if (l == 0.f) return -INFINITY;
+  int e;
+  const float m = frexpf(l, &e);
+  return ((M + (float)e) + log2f(m)) * 0.6931471805599453f;
+}
+
 size_t decode_fp8_workspace(const Pool& p, int B, int max_len);
 cudaError_t launch_decode_fp8(const Pool& p, const Fp8Store& f, int layer, int B, const AttnCall& c, cudaStream_t s);
 size_t prefill_fp8_workspace(const Pool& p, int n_seqs, int max_q, int max_len);

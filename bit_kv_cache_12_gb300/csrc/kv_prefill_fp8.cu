@@ -54,7 +54,6 @@ constexpr int kPolls = 1 << 20;
 constexpr int kMaxSplits = 32;
 constexpr float kNoRef = -3e38f;
 constexpr float kRaise = 15.f, kHead = 7.f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 constexpr uint32_t kOperand = kKeys * 256;     // 128 x 128 fp16
 constexpr uint32_t kOffQ = 0;                  // two tiles
@@ -810,7 +809,7 @@ __device__ __forceinline__ void write_row(const PrefillFp8Args& a, const Work& w
   const float nan = __uint_as_float(0x7FC00000u);
   const bool empty = ok && !ro.poison && ro.l == 0.f;
   const float f = !ok || ro.poison ? nan : (empty ? 0.f : 1.f / ro.l);
-  const float lse = !ok ? nan : (ro.l == 0.f ? -INFINITY : (ro.M + log2f(ro.l)) * kLn2);
+  const float lse = !ok ? nan : lse_of(ro.M, ro.l);
   float* part = static_cast<float*>(a.c.ws) +
                 (((size_t)w.s * a.max_q + token) * a.Hq + hq) * a.n_split * 132 + (size_t)w.split * 132;
   uint4* out = static_cast<uint4*>(a.c.out);

@@ -289,6 +289,78 @@ def test_prefill_repeats_and_graph(cuda_lib):
     s.pool.close()
 
 
+@pytest.mark.parametrize("n", [100, 1000])
+def test_prefill_of_many_exponents(cuda_lib, n):
+    """Exponents all over the format's range inside a key tile: one pass over the tile for each group of them."""
+    s = Setup(4, 1, 16, 1, n, seed=n + 1)
+    s.fill()
+    s.model.exps[..., 0] = s.rng.integers(-30, -6, s.model.exps.shape[:-1])
+    s.model.exps[..., 1] = s.rng.integers(-64, 8, s.model.exps.shape[:-1])
+    s.upload()
+    q = bf16(s.rng.standard_normal((50, 4, 128)))
+    prefill_and_check(s, q, [50], [n])
+    prefill_and_check(s, q, [50], [n], window=1)
+    prefill_and_check(s, q, [50], [n], window=17, sinks=3)
+    s.pool.close()
+
+
+@pytest.mark.parametrize("n", [40, 1000])
+def test_decode_of_many_exponents(cuda_lib, n):
+    """One visible token, or a few, whose V exponents lie far apart: the lse keeps its precision."""
+    s = Setup(4, 1, 16, 2, n, seed=n + 2)
+    s.fill()
+    s.model.exps[..., 0] = s.rng.integers(-30, -6, s.model.exps.shape[:-1])
+    s.model.exps[..., 1] = s.rng.integers(-64, 8, s.model.exps.shape[:-1])
+    s.upload()
+    q = bf16(s.rng.standard_normal((2, 4, 128)))
+    for m in range(n, n - 33, -1):
+        decode_and_check(s, q, [m, m // 2], window=1)
+        decode_and_check(s, q, [m, m // 2], window=17, sinks=3)
+    s.pool.close()
+
+
+@pytest.mark.parametrize("page", [16, 32])
+def test_pages_given_up_behind_the_window(cuda_lib, page):
+    """Pages that no query sees any more may be gone from the table: no error, the same output."""
+    s = Setup(8, 2, page, 2, 2000, seed=page)
+    s.fill()
+    n, window, sinks = [2000, 1003], 300, 20
+    q1, q2 = bf16(s.rng.standard_normal((2, 8, 128))), bf16(s.rng.standard_normal((110, 8, 128)))
+    want1, want2 = s.decode(q1, n, window, sinks), s.prefill(q2, [60, 50], n, window, sinks)
+    table = s.table.copy()
+    for b, m in ((0, 60), (1, 50)):
+        first = n[b] - m - window + 1                     # the first key that the earliest query's window shows
+        table[b, -(-sinks // page):first // page] = -1
+        table[b, -(-n[b] // page):] = s.pages + 7         # and pages that are not there yet
+    got1, got2 = s.decode(q1, n, window, sinks, table=table), s.prefill(q2, [60, 50], n, window, sinks, table=table)
+    for got, want in ((got1, want1), (got2, want2)):
+        np.testing.assert_array_equal(got[0], want[0])
+        np.testing.assert_array_equal(got[1], want[1])
+    assert s.pool.error() == 0
+    s.pool.close()
+
+
+def test_attention_over_codes_beyond_32_bits(cuda_lib):
+    """Pages past 2^32 bytes of codes attend as the same pages at the pool's start."""
+    s = Setup(8, 8, 16, 2, 700, seed=3, spare=0)
+    s.fill()
+    q1, q2 = bf16(s.rng.standard_normal((2, 8, 128))), bf16(s.rng.standard_normal((150, 8, 128)))
+    want1, want2 = s.decode(q1, [700, 333]), s.prefill(q2, [90, 60], [700, 333])
+    pages = 140000                                        # 8 heads x 4096 B a page: 4.6 GB
+    far = native.KVPool(native.KV_POOL_FP8, 1, 8, 8, 16, pages, 2)
+    codes, exps = far.fp8_views(0)
+    codes[pages - s.pages:].copy_(s.codes)
+    exps[pages - s.pages:].copy_(s.exps)
+    near, s.pool = s.pool, far
+    table = s.table + (pages - s.pages)
+    got1, got2 = s.decode(q1, [700, 333], table=table), s.prefill(q2, [90, 60], [700, 333], table=table)
+    for got, want in ((got1, want1), (got2, want2)):
+        np.testing.assert_array_equal(got[0], want[0])
+        np.testing.assert_array_equal(got[1], want[1])
+    near.close()
+    far.close()
+
+
 @pytest.mark.parametrize("window,sinks", [(0, 0), (100, 12)])
 def test_a_served_sequence(cuda_lib, window, sinks):
     """Prompt chunks and single tokens as a server runs them: append, attend, append, ..."""
