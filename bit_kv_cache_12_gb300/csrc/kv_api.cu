@@ -77,6 +77,12 @@ bool valid_rows(const void* p, int64_t stride, int heads) {
   return aligned16(p) && stride >= (int64_t)heads * 128 && (stride & 7) == 0;
 }
 
+// sequences and queries of a prompt call; its grid: a CTA per 256 rows and KV head
+bool valid_prefill(const Pool& p, int32_t n_seqs, int32_t max_q) {
+  if (n_seqs <= 0 || n_seqs > p.cfg.max_seqs || max_q < 0 || max_q > kvint2::kMaxDecodeLen) return false;
+  return ((int64_t)max_q * p.G + 255) / 256 * n_seqs * p.cfg.num_kv_heads <= INT32_MAX;
+}
+
 }  // namespace
 
 extern "C" {
@@ -522,8 +528,8 @@ kv_status_t kv_decode_attention_fp8(kv_pool_t* pool, int32_t layer, int32_t B, c
 
 size_t kv_prefill_workspace_bytes(const kv_pool_t* pool, int32_t n_seqs, int32_t max_q_per_seq,
                                   int32_t max_seq_len) {
-  if (!pool || pool->p.cfg.kind != KV_POOL_FP8 || n_seqs <= 0 || n_seqs > pool->p.cfg.max_seqs ||
-      max_q_per_seq < 0 || max_seq_len < 0 || max_seq_len > kvint2::kMaxDecodeLen)
+  if (!pool || pool->p.cfg.kind != KV_POOL_FP8 || !valid_prefill(pool->p, n_seqs, max_q_per_seq) ||
+      max_seq_len < 0 || max_seq_len > kvint2::kMaxDecodeLen)
     return 0;
   return kvint2::prefill_fp8_workspace(pool->p, n_seqs, max_q_per_seq, max_seq_len);
 }
@@ -533,10 +539,9 @@ kv_status_t kv_prefill_attention_fp8(kv_pool_t* pool, int32_t layer, int32_t n_s
                                      int32_t max_pages_per_seq, int32_t max_q_per_seq, int32_t max_seq_len,
                                      float softmax_scale, int32_t window, int32_t n_sink, void* out, float* lse,
                                      void* workspace, size_t workspace_bytes, void* stream) {
-  if (!valid_layer(pool, layer) || n_seqs <= 0 || max_pages_per_seq <= 0 || max_q_per_seq < 0 || max_seq_len < 0)
-    return KV_ERR_INVALID_ARG;
+  if (!valid_layer(pool, layer) || max_pages_per_seq <= 0 || max_seq_len < 0) return KV_ERR_INVALID_ARG;
   const Pool& p = pool->p;
-  if (p.cfg.kind != KV_POOL_FP8 || n_seqs > p.cfg.max_seqs) return KV_ERR_INVALID_ARG;
+  if (p.cfg.kind != KV_POOL_FP8 || !valid_prefill(p, n_seqs, max_q_per_seq)) return KV_ERR_INVALID_ARG;
   if (!q || !cu_q || !seq_len || !page_table || !out || !workspace) return KV_ERR_INVALID_ARG;
   if (window < 0 || n_sink < 0 || !std::isfinite(softmax_scale)) return KV_ERR_INVALID_ARG;
   if ((int64_t)max_seq_len > (int64_t)max_pages_per_seq * p.cfg.page_size || max_seq_len > kvint2::kMaxDecodeLen)

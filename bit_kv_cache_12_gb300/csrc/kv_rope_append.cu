@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_fp8_kernel(AppendFp8Args a
     n = min(n, a.max_tokens);
   }
   if (n <= 0) return;
-  if (start < 0 || (long long)start + n > (long long)a.max_pages * a.P) {
+  if (start < 0 || (long long)start + n > min((long long)a.max_pages * a.P, (long long)INT32_MAX)) {
     if (i == 0 && threadIdx.x == 0) flag_error(a.err, KV_DEVERR_SEQ_RANGE);
     return;
   }

@@ -486,7 +486,8 @@ kv_status_t kv_rope_apply(const kv_pool_t* pool, int32_t layer, int32_t n_tokens
  * a token whose k (or v) row of a head has a NaN or an infinity stores NaN in
  * all of that row.  Slots after the last appended token keep their bytes.
  * Sequences must not share a page that is written.  A sequence that would leave
- * the page table's span is skipped (KV_DEVERR_SEQ_RANGE), its q_out rows too; a
+ * the page table's span, or pass position 2^31 - 2, is skipped
+ * (KV_DEVERR_SEQ_RANGE), its q_out rows too; a
  * tile with a bad page id is not stored (KV_DEVERR_PAGE_ID), its q_out rows are
  * written. */
 kv_status_t kv_append_fp8(kv_pool_t* pool, int32_t layer, int32_t n_seqs, const void* q,
@@ -510,7 +511,9 @@ kv_status_t kv_append_fp8(kv_pool_t* pool, int32_t layer, int32_t n_seqs, const 
  *   workspace  device, 16-byte aligned, >= kv_decode_workspace_bytes(pool, B,
  *            max_seq_len)
  * What hidden tokens hold never reaches the output, NaN included.  The tokens
- * of a page with a bad id are hidden (KV_DEVERR_PAGE_ID). */
+ * of a page with a bad id are hidden (KV_DEVERR_PAGE_ID).  Calls for the same
+ * layer must not overlap on the GPU (they share the layer's completion
+ * counters). */
 kv_status_t kv_decode_attention_fp8(kv_pool_t* pool, int32_t layer, int32_t B, const void* q,
                                     const int32_t* seq_len, const int32_t* page_table,
                                     int32_t max_pages_per_seq, int32_t max_seq_len,
@@ -527,13 +530,16 @@ kv_status_t kv_decode_attention_fp8(kv_pool_t* pool, int32_t layer, int32_t B, c
  *   cu_q     device int32 [n_seqs+1] prefix sums; rows from cu_q[n_seqs] on are
  *            neither read nor written
  *   seq_len  device int32 [n_seqs], treated as in kv_decode_attention_fp8
- *   max_q_per_seq, max_seq_len  host bounds; a sequence with more queries (or a
- *            negative count) sets KV_DEVERR_SEQ_RANGE and gets none of its rows
- *            written
+ *   max_q_per_seq, max_seq_len  host bounds, each at most KV_MAX_DECODE_LEN (and
+ *            max_seq_len at most the page table's span; blocks of 256 rows of all
+ *            sequences and KV heads at most 2^31 - 1); a sequence with more
+ *            queries (or a negative count) sets KV_DEVERR_SEQ_RANGE and gets none
+ *            of its rows written
  *   out, lse [T][Hq][128] bf16 and [T][Hq] fp32 (or NULL)
  *   workspace  >= kv_prefill_workspace_bytes(pool, n_seqs, max_q_per_seq,
  *            max_seq_len)
- * Hidden tokens and bad pages as in kv_decode_attention_fp8. */
+ * Hidden tokens and bad pages as in kv_decode_attention_fp8; calls may overlap if
+ * their workspaces and outputs differ. */
 size_t kv_prefill_workspace_bytes(const kv_pool_t* pool, int32_t n_seqs, int32_t max_q_per_seq,
                                   int32_t max_seq_len);
 kv_status_t kv_prefill_attention_fp8(kv_pool_t* pool, int32_t layer, int32_t n_seqs, const void* q,

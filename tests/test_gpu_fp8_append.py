@@ -208,6 +208,25 @@ def test_code_offsets_beyond_32_bits(cuda_lib):
     s.pool.close()
 
 
+def test_the_last_positions(cuda_lib):
+    """Tokens up to position 2^31 - 2 are stored; a run that would pass it is refused, whatever the table spans."""
+    near, far = (Setup(hq=4, hkv=1, page=16, seqs=1, longest=16, spare=0) for _ in range(2))
+    k, v = (bf16(near.rng.standard_normal((8, 1, 128))) for _ in range(2))
+    far.width = (1 << 27) + 1                                  # pages: 2^31 + 16 positions
+    table = torch.zeros(1, far.width, dtype=torch.int32, device="cuda")
+    cu, start = i32([0, 8]), i32([(1 << 31) - 8])
+    call = lambda cu: native.kv_append_fp8(far.pool.handle, 0, 1, None, 0, k, 128, v, 128, cu, start, table, far.width, 8, None)
+    call(cu)
+    torch.cuda.synchronize()
+    assert far.pool.error() == 3 and not far.codes.any()
+    call(i32([0, 7]))
+    near.append(None, k[:7], v[:7], [8], [7])
+    assert far.pool.error() == 0 and near.pool.error() == 0
+    assert near.codes.any() and torch.equal(near.codes, far.codes) and torch.equal(near.exps, far.exps)
+    near.pool.close()
+    far.pool.close()
+
+
 def test_views_keep_their_pool(cuda_lib):
     """A view of the stored codes outlives the last name of its pool."""
     import gc

@@ -99,6 +99,22 @@ def test_attention(rig):
     assert n.kv_prefill_workspace_bytes(pool.handle, 5, 1, 64) == 0
 
 
+def test_prompt_bounds_beyond_the_longest_sequence(rig):
+    """A bound on the queries that no sequence can have is refused: the row numbers it stands for pass 32 bits."""
+    pool, x, i, ws = rig
+    y = torch.empty_like(x)
+    for most_q in (6553601, 1 << 28, (1 << 31) - 1):
+        assert status(n.kv_prefill_attention_fp8, pool.handle, 0, 4, x, i, i, i, 4, most_q, 64, 0.1, 0, 0, y, None, ws,
+                      ws.numel()) == n.KV_ERR_INVALID_ARG
+        assert n.kv_prefill_workspace_bytes(pool.handle, 1, most_q, 64) == 0
+    assert n.kv_prefill_workspace_bytes(pool.handle, 1, 6553600, 64) > 0
+    wide = n.KVPool(n.KV_POOL_FP8, 1, 64, 8, 16, 8, 4096)        # 6553600 queries of 4096 sequences: 2^32.6 blocks
+    assert status(n.kv_prefill_attention_fp8, wide.handle, 0, 4096, x, i, i, i, 4, 6553600, 64, 0.1, 0, 0, y, None, ws,
+                  ws.numel()) == n.KV_ERR_INVALID_ARG
+    assert n.kv_prefill_workspace_bytes(wide.handle, 4096, 6553600, 64) == 0
+    wide.close()
+
+
 def test_other_kinds_of_pool(rig):
     _, x, i, ws = rig
     y = torch.empty_like(x)
