@@ -98,8 +98,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
   if (lane < kStages) mbar_init(bar + lane, 1);
   mbar_fence_init();
   __syncwarp();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  release_successor();
+  after_predecessor();
 
   const int split = blockIdx.x % a.n_split, pair = blockIdx.x / a.n_split;
   const int h = pair % a.L.Hkv, b = pair / a.L.Hkv;
@@ -472,17 +472,8 @@ template <int G>
 cudaError_t launch_t(const DecodeFp8Args& a, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(decode_fp8_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((long long)a.B * a.L.Hkv * a.n_split));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_fp8_kernel<G>, a);
+  return launch_dependent(decode_fp8_kernel<G>, dim3((unsigned)((long long)a.B * a.L.Hkv * a.n_split)), kThreads, kSmem,
+                          s, a);
 }
 
 }  // namespace

@@ -37,6 +37,28 @@ inline Fp8Layer fp8_layer(const Pool& p, const Fp8Store& f, int layer) {
           p.cfg.num_kv_heads, p.cfg.page_size};
 }
 
+// Every kernel of the 8-bit cache is launched as the programmatic dependent of the
+// one before it and lets the next one launch at once: a kernel's CTAs come up while
+// the last ones of its predecessor finish.  Each of its threads passes
+// after_predecessor() before it reads what the caller passes or writes anything,
+// so a grid never ends before its predecessor.
+template <class... P>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const P&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+__device__ __forceinline__ void release_successor() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void after_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // The layer's parameters from a configuration, or the reason it is refused.
 kv_status_t rope_params(const kv_rope_config_t& c, RopeParams* out);
 

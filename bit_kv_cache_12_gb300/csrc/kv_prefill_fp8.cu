@@ -875,6 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   Shared* sh = reinterpret_cast<Shared*>(sm + kOffInfo);
   const int warp = threadIdx.x >> 5;
+  release_successor();
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(sh->bars + kKFull + i, 128);
@@ -906,6 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
   fence_before();
   __syncthreads();
   fence_after();
+  after_predecessor();
   const uint32_t tmem = sh->tmem;
   const Waiter wait{&sh->abort, a.polls};
   if (warp < 8) {
@@ -964,6 +966,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
 
 // Joins the splits of a row: a warp per row, four channels per lane.
 __global__ void __launch_bounds__(256) prefill_join_kernel(PrefillFp8Args a) {
+  release_successor();
+  after_predecessor();
   const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const int hq = (int)(item % a.Hq);
@@ -1026,11 +1030,9 @@ cudaError_t launch_prefill_fp8(const Pool& p, const Fp8Store& f, int layer, int 
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(prefill_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
-  prefill_fp8_kernel<<<(unsigned)ctas, kThreads, kSmem, s>>>(a);
-  e = cudaGetLastError();
+  e = launch_dependent(prefill_fp8_kernel, dim3((unsigned)ctas), kThreads, kSmem, s, a);
   if (e != cudaSuccess || a.n_split == 1) return e;
-  prefill_join_kernel<<<(unsigned)(((long long)n_seqs * max_q * a.Hq + 7) / 8), 256, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(prefill_join_kernel, dim3((unsigned)(((long long)n_seqs * max_q * a.Hq + 7) / 8)), 256, 0, s, a);
 }
 
 }  // namespace kvint2

@@ -278,6 +278,8 @@ template <bool kPairs>
 __global__ void __launch_bounds__(kThreads, 4) rope_kernel(RopeArgs a, const __grid_constant__ RopeParams rp) {
   __shared__ __align__(16) float tab[kTile * kTokStride];
   __shared__ int pos[kTile];
+  release_successor();
+  after_predecessor();
   const int t0 = blockIdx.x * kTile;
   if (threadIdx.x < kTile) pos[threadIdx.x] = t0 + (int)threadIdx.x < a.n_tokens ? a.positions[t0 + threadIdx.x] : -1;
   __syncthreads();
@@ -377,6 +379,8 @@ template <bool kPairs>
 __global__ void __launch_bounds__(kThreads, 4) append_fp8_kernel(AppendFp8Args a, const __grid_constant__ RopeParams rp) {
   __shared__ __align__(16) float tab[kTile * kTokStride];
   __shared__ int pos[kTile];
+  release_successor();
+  after_predecessor();
   const int s = blockIdx.x / a.tiles, i = blockIdx.x - s * a.tiles;
   const int c0 = a.cu[s];
   int n = a.cu[s + 1] - c0;
@@ -510,11 +514,7 @@ cudaError_t launch_rope(const Pool& p, const RopeParams& r, int n_tokens, const 
   a.n_tokens = n_tokens;
   const long long tiles = ((long long)n_tokens + kTile - 1) / kTile;
   const dim3 grid((unsigned)tiles, slices(p, tiles, a.heads[0] + a.heads[1], kRopePerSm));
-  if (r.interleaved)
-    rope_kernel<true><<<grid, kThreads, 0, s>>>(a, r);
-  else
-    rope_kernel<false><<<grid, kThreads, 0, s>>>(a, r);
-  return cudaGetLastError();
+  return launch_dependent(r.interleaved ? rope_kernel<true> : rope_kernel<false>, grid, kThreads, 0, s, a, r);
 }
 
 cudaError_t launch_append_fp8(const Pool& p, const Fp8Store& f, const RopeParams& r, int layer, int n_seqs,
@@ -546,11 +546,7 @@ cudaError_t launch_append_fp8(const Pool& p, const Fp8Store& f, const RopeParams
   a.err = p.err;
   const long long tiles = (long long)n_seqs * a.tiles;
   const dim3 grid((unsigned)tiles, slices(p, tiles, 2 * a.Hkv + (a.q ? a.Hq : 0), kAppendPerSm));
-  if (r.interleaved)
-    append_fp8_kernel<true><<<grid, kThreads, 0, s>>>(a, r);
-  else
-    append_fp8_kernel<false><<<grid, kThreads, 0, s>>>(a, r);
-  return cudaGetLastError();
+  return launch_dependent(r.interleaved ? append_fp8_kernel<true> : append_fp8_kernel<false>, grid, kThreads, 0, s, a, r);
 }
 
 }  // namespace kvint2
