@@ -13,11 +13,17 @@
 // between 2^-31 of the largest and 2^15, M lagging behind the running maximum
 // so that the accumulator is rescaled only when a weight would pass 2^15.
 //
-// Bound: the tensor cores (4 * 128 operations per row and key), with the
-// exponentials close behind.  One CTA per SM: two tiles of 128 rows take turns,
-// one in the tensor cores while the other is in the softmax.
+// Bound: the tensor cores (4 * 128 operations per row and key).  One CTA per SM: two
+// tiles of 128 rows take turns, one in the tensor cores while the other is in the
+// softmax.  8192 tokens (32 query heads, 8 KV heads): 408 us, 1.35 PFLOP/s, 0.68 of
+// the bf16 rate of a large library product; behind 32,768 cached tokens 1.56 PFLOP/s
+// (0.79).  A key tile takes 3,340 clocks, its products 2,048: a tile's own chain
+// (weights seen by the issuer, O += P V, S, scores seen, softmax) fills 3,310 of them,
+// and taking exponentials, maximum or conversions out changes the time by 2% at most.
+// An item's end costs 7 us more (last product, next q, rows written, first scores).
 //   warps 0-3, 4-7   softmax of a tile: a thread owns a row; S is read from
-//                    tensor memory, the weights go back over it as fp16
+//                    tensor memory, the weights go back over it as fp16; then
+//                    the next item's q and this item's rows
 //   warps 8-11       converters: codes from global memory to registers a tile
 //                    ahead, fp16 in the swizzled operand layout to shared memory
 //                    (two stages each of K and V)
@@ -59,7 +65,8 @@ constexpr uint32_t kOperand = kKeys * 256;     // 128 x 128 fp16
 constexpr uint32_t kOffQ = 0;                  // two tiles
 constexpr uint32_t kOffK = 2 * kOperand;       // two stages
 constexpr uint32_t kOffV = 4 * kOperand;       // two stages
-constexpr uint32_t kOffInfo = 6 * kOperand;
+constexpr uint32_t kOffOut = 6 * kOperand;     // 2 KB for each softmax warp
+constexpr uint32_t kOffInfo = kOffOut + 8 * 2048;
 
 // A pass over a key tile: what the walker tells the other warps; a ring of eight.
 struct Pass {
@@ -78,11 +85,11 @@ constexpr int kRing = 8;
 
 constexpr int kItems = 4;                      // ring of items
 
-enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kOFull = 12, kDrain = 13, kQFull = 14,
-       kCancel = 16, kItem = 17, kFree = kItem + kItems, kPass = kFree + kItems, kBars = kPass + kRing };
+enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kOFull = 12, kQFull = 14, kDrain = 16,
+       kCancel = 17, kItem = 18, kFree = kItem + kItems, kPass = kFree + kItems, kBars = kPass + kRing };
 
 // An item: a block of rows and the key tiles they see.
-enum { kKeyed = 0, kNoKeys = 1, kStop = 2 };   // rows with keys, rows that see none, no item
+enum { kKeyed = 0, kNoKeys = 1, kStop = 2, kStart = 3 };   // rows with keys, rows that see none, no item; before the first
 struct Work {
   int state;
   int s, h, c0, m, n, row0, split;             // sequence, KV head, first q row, queries, keys, first row of the block
@@ -597,16 +604,15 @@ __device__ __forceinline__ void issue_products(uint32_t tmem, uint8_t* sm, Share
               v += (4 * 2048) >> 4;
             }
             if (tile == 1) commit(sh->bars + kVEmpty + stage);
+            if (last) {
+              arrive(sh->bars + kOFull + tile);   // a release after this warp saw the last V's record
+              commit(sh->bars + kOFull + tile);
+            }
           }
           __syncwarp();
           if (!last) scores(tile, stage ^ 1);
         }
       }
-      if (elect_one()) {
-        arrive(sh->bars + kOFull);             // a release after this warp saw the last V's record
-        commit(sh->bars + kOFull);
-      }
-      __syncwarp();
       ++keyed;
     }
     if (elect_one()) arrive(sh->bars + kFree + slot);
@@ -623,8 +629,8 @@ struct Row {
   size_t qrow;
   __device__ __forceinline__ Row(const PrefillFp8Args& a, const Work& w, int i) {
     const int row = w.row0 + i;                // of the sequence's rows
-    token = row / a.G;
-    hq = w.h * a.G + row % a.G;
+    token = row >> (__ffs(a.G) - 1);           // G: 1, 2, 4 or 8
+    hq = w.h * a.G + (row & (a.G - 1));
     live = token < w.m;
     qrow = ((size_t)w.c0 + token) * a.Hq + hq;
   }
@@ -635,42 +641,50 @@ struct RowOut {
   bool poison = false;
 };
 
-// g: the pass, counted over the CTA's items; keyed: the items with keys before this one
-__device__ __forceinline__ bool softmax_rows(const PrefillFp8Args& a, int sinks, uint32_t trow, int tile, int pos,
-                                             float cs, Shared* sh, const Waiter& wait, int& g, int keyed, RowOut& ro) {
+// The keys of a pass that row i of the block sees.
+__device__ __forceinline__ void sees(const PrefillFp8Args& a, const Work& w, int i, const Pass& p, uint32_t (&see)[4]) {
+  const int pos = w.pos0 + Row(a, w, i).token, t0 = p.t0;
+  const uint32_t blocks = p.blocks;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t m = below(pos + 1 - t0, 32 * q);
+    if (a.c.window) m &= ~below(pos + 1 - a.c.window - t0, 32 * q) | below(w.sinks - t0, 32 * q);
+    m &= ((blocks >> (2 * q)) & 1 ? 0xFFFFu : 0u) | ((blocks >> (2 * q + 1)) & 1 ? 0xFFFF0000u : 0u);
+    see[q] = m;
+  }
+}
+// Whether it sees a key whose V row holds NaN (known once V is there).
+__device__ __forceinline__ bool poisoned(const PrefillFp8Args& a, const Work& w, int i, const Pass& p) {
+  if (!p.partial) return false;
+  uint32_t see[4];
+  sees(a, w, i, p, see);
+  return ((p.nan[0] & see[0]) | (p.nan[1] & see[1]) | (p.nan[2] & see[2]) | (p.nan[3] & see[3])) != 0;
+}
+
+// The passes of an item, up to its last weights.  g: the pass, counted over the CTA's
+// items; left at the last one.
+__device__ __forceinline__ bool softmax_rows(const PrefillFp8Args& a, const Work& w, uint32_t trow, int tile, Shared* sh,
+                                             const Waiter& wait, float cs, int& g, RowOut& ro) {
   const uint32_t ts = trow + 128 * tile, to = trow + 256 + 128 * tile;
-  uint32_t see[4] = {0, 0, 0, 0};
-  bool check = false;                          // `see` of the previous tile is to be held against its NaN rows
+  const int i0 = tile * kRows + (threadIdx.x & 127);
+  bool check = false;                          // the pass before was partial
   for (int it = 0;; ++it, ++g) {
     if (!__all_sync(0xffffffffu, wait(sh->bars + kSFull + tile, g & 1))) return false;
     fence_after();
     const Pass& info = sh->pass[g & (kRing - 1)];
-    if (check) {
-      const Pass& old = sh->pass[(g - 1) & (kRing - 1)];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) ro.poison |= (old.nan[q] & see[q]) != 0;
-    }
+    if (check) ro.poison |= poisoned(a, w, i0, sh->pass[(g - 1) & (kRing - 1)]);
     const bool partial = info.partial != 0, last = info.last != 0;
+    check = partial;
     // above 0, so that a hidden key's -inf stays one
     const float c = fmaxf(cs * info.fk, 1.17549435e-38f), ev = info.ev;
     float v[kKeys];
 #pragma unroll
     for (int q = 0; q < 4; ++q) ld32(ts + 32 * q, v + 32 * q);
-    if (partial) {
-      const int t0 = info.t0;
-      const uint32_t blocks = info.blocks;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t m = below(pos + 1 - t0, 32 * q);
-        if (a.c.window) m &= ~below(pos + 1 - a.c.window - t0, 32 * q) | below(sinks - t0, 32 * q);
-        m &= ((blocks >> (2 * q)) & 1 ? 0xFFFFu : 0u) | ((blocks >> (2 * q + 1)) & 1 ? 0xFFFF0000u : 0u);
-        see[q] = m;
-      }
-    }
-    check = partial;
 #pragma unroll
     for (int q = 0; q < 4; ++q) settle(v + 32 * q);
     if (partial) {
+      uint32_t see[4];
+      sees(a, w, i0, info, see);
 #pragma unroll
       for (int i = 0; i < kKeys; ++i)
         if (!((see[i >> 5] >> (i & 31)) & 1)) v[i] = -INFINITY;
@@ -730,48 +744,32 @@ __device__ __forceinline__ bool softmax_rows(const PrefillFp8Args& a, int sinks,
     ro.l = fmaf(sa + sb, exp2f(-ev), ro.l);
     wait_st();
     fence_before();
-    arrive(sh->bars + kPFull + tile);
-    if (last) {
-      if (!__all_sync(0xffffffffu, wait(sh->bars + kOFull, keyed & 1))) return false;
-      fence_after();
-      if (check) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) ro.poison |= (info.nan[q] & see[q]) != 0;
-      }
-      ++g;
-      return true;
-    }
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) arrive(sh->bars + kPFull + tile);
+    if (last) return true;
   }
 }
 
-// Whether `ok` holds for the 128 threads of a tile (a barrier for them; every path
-// of the softmax warps comes here once per item).
-__device__ __forceinline__ bool tile_and(int tile, bool ok) {
-  int r;
-  asm volatile(
-      "{ .reg .pred p, q; setp.ne.b32 p, %1, 0; bar.red.and.pred q, %2, 128, p; selp.b32 %0, 1, 0, q; }"
-      : "=r"(r)
-      : "r"((int)ok), "r"(1 + tile)
-      : "memory");
-  return r != 0;
-}
-
-// q: the warp's 32 rows, each scaled by a power of two, as fp16 into the swizzled
-// operand (`operand` + 128 bytes per row of the tile, first row m0); returns the
-// factor that brings a score of this thread's row back to base-2 logits (without
-// 2^eK).  Sixteen lanes read a row together (a row per thread cost eight times the
-// wavefronts).
-__device__ __forceinline__ float load_q(const PrefillFp8Args& a, uint8_t* operand, int m0, size_t qrow, bool live) {
-  const int lane = threadIdx.x & 31, c = lane & 15;
-  uint4 x[16];
+// The warp's 32 rows of q (first row m0 of the block), half a warp to a row: on their
+// way to registers.
+__device__ __forceinline__ void fetch_q(const PrefillFp8Args& a, const Work& w, int m0, uint4 (&x)[16]) {
+  const int lane = threadIdx.x & 31, half = lane >> 4, shift = __ffs(a.G) - 1;   // G: 1, 2, 4 or 8, and rows a multiple
+  const int token = (w.row0 + m0) >> shift, live = (w.m - token) << shift;
+  const uint8_t* src = static_cast<const uint8_t*>(a.c.q) + (lane & 15) * 16 +
+                       ((long long)(w.c0 + token) * a.Hq + w.h * a.G) * 256;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {               // rows 2 i and 2 i + 1
-    const int r = 2 * i + (lane >> 4);
-    const size_t src = __shfl_sync(0xffffffffu, (unsigned long long)qrow, r);
+    const int r = 2 * i + half;
     x[i] = make_uint4(0, 0, 0, 0);
-    if (__shfl_sync(0xffffffffu, (int)live, r))
-      x[i] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.c.q) + src * 128)[c];
+    if (r < live)
+      x[i] = *reinterpret_cast<const uint4*>(src + (long long)((r >> shift) * a.Hq + (r & (a.G - 1))) * 256);
   }
+}
+
+// Those rows, each scaled by a power of two, as fp16 into the swizzled operand; returns
+// the factor that brings a score of this thread's row back to base-2 logits (without 2^eK).
+__device__ __forceinline__ float store_q(const PrefillFp8Args& a, uint8_t* operand, int m0, const uint4 (&x)[16]) {
+  const int lane = threadIdx.x & 31, half = lane >> 4, c = lane & 15;
   int mine = 0;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -780,29 +778,29 @@ __device__ __forceinline__ float load_q(const PrefillFp8Args& a, uint8_t* operan
 #pragma unroll
     for (int u = 0; u < 4; ++u) top = __vmaxu2(top, w[u] & 0x7FFF7FFFu);
     top = max(top & 0xFFFFu, top >> 16);
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const int up = min(14 - ((int)(top >> 7) - 127), 127);
-    const int theirs = __shfl_sync(0xffffffffu, up, (lane & 1) << 4);
-    if ((lane >> 1) == i) mine = theirs;       // row `lane` is row 2 (lane / 2) + lane % 2
-    float mul = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : pow2i(up);
+    const uint32_t t0 = __reduce_max_sync(0xffffffffu, half ? 0u : top);
+    const uint32_t t1 = __reduce_max_sync(0xffffffffu, half ? top : 0u);
+    if ((lane >> 1) == i) mine = (lane & 1) ? t1 : t0;   // row `lane` is row 2 (lane / 2) + lane % 2
+    top = half ? t1 : t0;
+    float mul = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : pow2i(min(14 - ((int)(top >> 7) - 127), 127));
     if (a.c.scale < 0.f) mul = -mul;
     uint32_t f[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) f[u] = pack_f16(bf16lo(w[u]) * mul, bf16hi(w[u]) * mul);
-    const int m = m0 + 2 * i + (lane >> 4);
+    const int m = m0 + 2 * i + half;
     *reinterpret_cast<uint4*>(operand + (c >> 3) * (kOperand / 2) + m * 128 + (((c & 7) ^ (m & 7)) << 4)) =
         make_uint4(f[0], f[1], f[2], f[3]);
   }
   fence_async();
-  return fabsf(a.c.scale) * 1.4426950408889634f * pow2i(max(-mine, -126));
+  const int up = min(14 - ((mine >> 7) - 127), 127);
+  return fabsf(a.c.scale) * 1.4426950408889634f * pow2i(max(-up, -126));
 }
 
 // A row's result: normalised to the output, or as a part of a split.  `stage`:
-// 8 KB of shared memory for the warp's 32 rows, from which they are written
-// 256 bytes at a time (a row per thread straight from registers took 2.6 us).
-__device__ __forceinline__ void write_row(const PrefillFp8Args& a, const Work& w, uint32_t to, uint8_t* stage, bool any,
-                                          bool ok, const Row& row, const RowOut& ro) {
+// 2 KB of shared memory for 32 channels of the warp's 32 rows, from which they are
+// written 64 bytes at a time.
+__device__ __forceinline__ void write_row(const PrefillFp8Args& a, const Work& w, uint32_t to, uint8_t* stage, int row0,
+                                          bool any, bool ok, const Row& row, const RowOut& ro) {
   const int lane = threadIdx.x & 31, token = row.token, hq = row.hq;
   const size_t qrow = row.qrow;
   const bool live = row.live;
@@ -812,54 +810,52 @@ __device__ __forceinline__ void write_row(const PrefillFp8Args& a, const Work& w
   const float lse = !ok ? nan : lse_of(ro.M, ro.l);
   float* part = static_cast<float*>(a.c.ws) +
                 (((size_t)w.s * a.max_q + token) * a.Hq + hq) * a.n_split * 132 + (size_t)w.split * 132;
-  uint4* out = static_cast<uint4*>(a.c.out);
-  const bool staged = any && a.n_split == 1;
+  // where this lane's 16 bytes of the warp's rows 8 i + lane / 4 go
+  uint4* dst[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const Row r(a, w, row0 + 8 * i + (lane >> 2));
+    dst[i] = r.live ? static_cast<uint4*>(a.c.out) + r.qrow * 16 + (lane & 3) : nullptr;
+  }
+  const bool read = any && ok;                 // the same for the whole warp
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    float v[32];
-    __syncwarp();
-    if (any && ok) {                           // the same for the whole warp
-      ld32(to + 32 * q, v);
-      settle(v);
+    float o[32];
+    if (read) {
+      ld32(to + 32 * q, o);
+      settle(o);
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = 0.f;
+      for (int i = 0; i < 32; ++i) o[i] = 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = empty ? 0.f : v[i] * f;
+    for (int i = 0; i < 32; ++i) o[i] = empty ? 0.f : o[i] * f;
     if (a.n_split > 1) {
       if (live) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           *reinterpret_cast<float4*>(part + 4 + 32 * q + 4 * i) =
-              make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
       }
     } else {
+      __syncwarp();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t u[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const __nv_bfloat162 y = __floats2bfloat162_rn(v[8 * i + 2 * e], v[8 * i + 2 * e + 1]);
+          const __nv_bfloat162 y = __floats2bfloat162_rn(o[8 * i + 2 * e], o[8 * i + 2 * e + 1]);
           u[e] = *reinterpret_cast<const uint32_t*>(&y);
         }
-        const uint4 y = make_uint4(u[0], u[1], u[2], u[3]);
-        if (staged)                            // 16-byte chunk c of row r at c ^ (r % 16): no bank conflicts either way
-          *reinterpret_cast<uint4*>(stage + lane * 256 + (((4 * q + i) ^ (lane & 15)) << 4)) = y;
-        else if (live)
-          out[qrow * 16 + 4 * q + i] = y;
+        // 16-byte chunk i of row r at i ^ (r / 2 % 4): no bank conflicts either way
+        *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
       }
-    }
-  }
-  if (staged) {
-    __syncwarp();
-    // two rows per step, 16 lanes each
-    const int half = lane >> 4, c = lane & 15;
-#pragma unroll 4
-    for (int r = half; r < 32; r += 2) {
-      const bool to_write = __shfl_sync(0xffffffffu, (int)live, r);
-      const size_t dst = __shfl_sync(0xffffffffu, (unsigned long long)qrow, r);
-      if (to_write) out[dst * 16 + c] = *reinterpret_cast<const uint4*>(stage + r * 256 + ((c ^ (r & 15)) << 4));
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {            // eight rows per step, four lanes each
+        const int r = 8 * i + (lane >> 2);
+        if (dst[i]) dst[i][4 * q] = *reinterpret_cast<const uint4*>(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+      }
     }
   }
   if (live) {
@@ -883,10 +879,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
       mbar_init(sh->bars + kKEmpty + i, 1);
       mbar_init(sh->bars + kVEmpty + i, 1);
       mbar_init(sh->bars + kSFull + i, 2);
-      mbar_init(sh->bars + kPFull + i, 128);
+      mbar_init(sh->bars + kPFull + i, 4);
       mbar_init(sh->bars + kQFull + i, 128);
+      mbar_init(sh->bars + kOFull + i, 2);
     }
-    mbar_init(sh->bars + kOFull, 2);
     mbar_init(sh->bars + kDrain, 1);
     mbar_init(sh->bars + kCancel, 1);
     for (int i = 0; i < kItems; ++i) {
@@ -914,30 +910,51 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int tile = warp >> 2, m = threadIdx.x & 127;
     const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const int m0 = 32 * (warp & 3);            // this warp's rows of the tile
+    auto given = [&](int item) {
+      return __all_sync(0xffffffffu, wait(sh->bars + kItem + (item & (kItems - 1)), (item / kItems) & 1)) != 0;
+    };
     bool ok = true;
-    int g = 0, keyed = 0;
-    for (int item = 0;; ++item) {
-      const int slot = item & (kItems - 1);
-      if (ok) ok = __all_sync(0xffffffffu, wait(sh->bars + kItem + slot, (item / kItems) & 1));
-      // the tile's four warps go on together, their staged rows written: Q takes that place
-      if (!tile_and(tile, ok)) break;
-      const Work& w = sh->work[slot];
-      const int state = w.state;
-      if (state == kStop) break;
+    int g = 0, keyed = 0, state = kStart;
+    float cs = 0.f;
+    for (int item = -1; state != kStop; ++item) {
+      const Work& w = sh->work[item & (kItems - 1)];
       RowOut ro;
-      if (state == kKeyed) {
-        const Row r(a, w, tile * kRows + m);
-        const float cs = load_q(a, sm + kOffQ + tile * kOperand, 32 * (warp & 3), r.qrow, r.live);
+      if (state == kKeyed) ok = softmax_rows(a, w, trow, tile, sh, wait, cs, g, ro);
+      // The next item's q takes this one's place, whose last scores are read, while
+      // the last product runs; its first scores form while this item's rows are written.
+      const Work& next = sh->work[(item + 1) & (kItems - 1)];
+      int next_state = kStop;
+      uint4 x[16];
+      if (ok && given(item + 1)) {
+        next_state = next.state;
+        if (next_state == kKeyed) {            // one line each of the warp's 32 rows
+          const Row r(a, next, tile * kRows + m);
+          if (r.live) {
+            const uint8_t* line = static_cast<const uint8_t*>(a.c.q) + r.qrow * 256;
+            prefetch_l2(line);
+            prefetch_l2(line + 128);
+          }
+        }
+      }
+      if (next_state == kKeyed) {
+        fetch_q(a, next, tile * kRows + m0, x);
+        cs = store_q(a, sm + kOffQ + tile * kOperand, m0, x);
         arrive(sh->bars + kQFull + tile);
-        ok = softmax_rows(a, w.sinks, trow, tile, w.pos0 + r.token, cs, sh, wait, g, keyed, ro);
+      }
+      if (ok && state == kKeyed) {
+        ok = __all_sync(0xffffffffu, wait(sh->bars + kOFull + tile, keyed & 1)) != 0;
+        fence_after();
+        ro.poison |= poisoned(a, w, tile * kRows + m, sh->pass[g & (kRing - 1)]);
+        ++g;
         ++keyed;
       }
-      // (worked out again: kept over the passes, they would cost registers there)
-      asm volatile("" ::: "memory");
-      const Row r(a, w, tile * kRows + m);
-      // Q has been read: its place holds this warp's 32 rows of output
-      write_row(a, w, trow + 256 + 128 * tile, sm + kOffQ + tile * kOperand + (warp & 3) * 32 * 256, state == kKeyed, ok, r, ro);
-      arrive(sh->bars + kFree + slot);
+      if (state != kStart) {
+        write_row(a, w, trow + 256 + 128 * tile, sm + kOffOut + warp * 2048, tile * kRows + m0, state == kKeyed, ok,
+                  Row(a, w, tile * kRows + m), ro);
+        arrive(sh->bars + kFree + (item & (kItems - 1)));
+      }
+      state = ok ? next_state : kStop;
     }
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
