@@ -20,9 +20,12 @@
 // (tile, head) it quantizes, so the tile's maximum is one warp reduction, no
 // atomics, and a tile that already holds tokens has one writer.  A lane holds
 // both members of its pairs (two chunks of eight channels), so nothing crosses
-// lanes but the maximum; what counted was the number of instructions (269 per 16
-// channels with pairs fetched from other lanes: 47 us for a prompt of 8192
-// tokens, 39 us now, 4.7 TB/s) and of registers (64: four CTAs per SM).
+// lanes but the maximum.  What counted for a prompt of 8192 tokens (32 query heads,
+// 8 KV heads): registers (64, four CTAs per SM: 76 -> 47 us), instructions (pairs in
+// a lane, paired arithmetic: 39), starting before the kernel in front has ended
+// (37.3), the first rows on their way while the table is formed (35.3 us, 5.2 TB/s:
+// 0.78 of a plain copy; issue slots 54% and memory both in use).  Rotary rows alone,
+// 8192 tokens of 64 + 8 heads: 52 us, 5.8 TB/s, 0.86 of a plain copy.
 #include <cuda_fp8.h>
 
 #include <cmath>
@@ -399,6 +402,16 @@ __global__ void __launch_bounds__(kThreads, 4) append_fp8_kernel(AppendFp8Args a
   const long long lo = max(base, (long long)start), hi = min(base + kTile, (long long)start + n);
   if (lo >= hi) return;
   const int t0 = (int)(lo - base), t1 = (int)(hi - base);
+  const int lane = threadIdx.x & 31, nkv = 2 * a.Hkv, units = nkv + (a.q ? a.Hq : 0);
+  const int first = blockIdx.y * kWarps + (threadIdx.x >> 5);   // this warp's units: first, + gridDim.y * kWarps, ..
+  const int64_t row0 = (int64_t)c0 + (base - start);       // input row of slot 0 (rows t0 .. t1 - 1 exist)
+  // its first rows (half a row per lane) come from memory while the table is formed
+  if (first < units && (lane >> 1) >= t0 && (lane >> 1) < t1) {
+    const int64_t stride = first < a.Hkv ? a.k_stride : (first < nkv ? a.v_stride : a.q_stride);
+    const uint16_t* in =
+        first < a.Hkv ? a.k + first * 128 : (first < nkv ? a.v + (first - a.Hkv) * 128 : a.q + (first - nkv) * 128);
+    prefetch_l2(in + (row0 + (lane >> 1)) * stride + (lane & 1) * 64);
+  }
   if (threadIdx.x < kTile) {
     const bool in = (int)threadIdx.x >= t0 && (int)threadIdx.x < t1;
     pos[threadIdx.x] = in ? (int)(base + threadIdx.x) : -1;
@@ -409,10 +422,8 @@ __global__ void __launch_bounds__(kThreads, 4) append_fp8_kernel(AppendFp8Args a
   const bool page_ok = pid >= 0 && pid < a.num_pages;
   if (!page_ok && threadIdx.x == 0) flag_error(a.err, KV_DEVERR_PAGE_ID);
   __syncthreads();
-  const int lane = threadIdx.x & 31, nkv = 2 * a.Hkv, units = nkv + (a.q ? a.Hq : 0);
   const int per = a.P / kTile, sub = (int)(base / kTile % per);
-  const int64_t row0 = (int64_t)c0 + (base - start);       // input row of slot 0 (rows t0 .. t1 - 1 exist)
-  for (int u = blockIdx.y * kWarps + (threadIdx.x >> 5); u < units; u += gridDim.y * kWarps) {
+  for (int u = first; u < units; u += gridDim.y * kWarps) {
     if (u < nkv) {
       if (!page_ok) continue;
       const int tensor = u >= a.Hkv, h = u - (tensor ? a.Hkv : 0);
@@ -434,8 +445,8 @@ __global__ void __launch_bounds__(kThreads, 4) append_fp8_kernel(AppendFp8Args a
 
 // Slices of the heads per tile: about `per_sm` CTAs per SM, at most one unit per
 // warp.  A slice forms the tile's table again, so the append, whose units are
-// longer, takes fewer (8: ragged chunks 59 us, with 4: 63; a prompt of 8192: 39,
-// with 16: 43) than the rotary rows (16: 54 us, with 4: 57).
+// longer, takes fewer (8: ragged chunks 56 us, with 4: 61; a prompt of 8192 35,
+// with 16: 38) than the rotary rows (16: 52 us, with 8 or 32: 55).
 constexpr int kRopePerSm = 16, kAppendPerSm = 8;
 unsigned slices(const Pool& p, long long tiles, int units, int per_sm) {
   const long long want = ((long long)per_sm * p.sm_count + tiles - 1) / tiles;
