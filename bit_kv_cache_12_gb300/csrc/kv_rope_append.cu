@@ -23,9 +23,10 @@
 // lanes but the maximum.  What counted for a prompt of 8192 tokens (32 query heads,
 // 8 KV heads): registers (64, four CTAs per SM: 76 -> 47 us), instructions (pairs in
 // a lane, paired arithmetic: 39), starting before the kernel in front has ended
-// (37.3), the first rows on their way while the table is formed (35.3 us, 5.2 TB/s:
-// 0.78 of a plain copy; issue slots 54% and memory both in use).  Rotary rows alone,
-// 8192 tokens of 64 + 8 heads: 52 us, 5.8 TB/s, 0.86 of a plain copy.
+// (37.3), rows on their way while the table is formed or the unit before is worked
+// on (35.0 us, 5.3 TB/s: 0.79 of a plain copy; issue slots half in use).  Rotary
+// rows alone, 8192 tokens of 64 + 8 heads: 52 us, 5.8 TB/s, 0.86 of a plain copy
+// (54 to 57 with such prefetches).
 #include <cuda_fp8.h>
 
 #include <cmath>
@@ -405,13 +406,16 @@ __global__ void __launch_bounds__(kThreads, 4) append_fp8_kernel(AppendFp8Args a
   const int lane = threadIdx.x & 31, nkv = 2 * a.Hkv, units = nkv + (a.q ? a.Hq : 0);
   const int first = blockIdx.y * kWarps + (threadIdx.x >> 5);   // this warp's units: first, + gridDim.y * kWarps, ..
   const int64_t row0 = (int64_t)c0 + (base - start);       // input row of slot 0 (rows t0 .. t1 - 1 exist)
-  // its first rows (half a row per lane) come from memory while the table is formed
-  if (first < units && (lane >> 1) >= t0 && (lane >> 1) < t1) {
-    const int64_t stride = first < a.Hkv ? a.k_stride : (first < nkv ? a.v_stride : a.q_stride);
-    const uint16_t* in =
-        first < a.Hkv ? a.k + first * 128 : (first < nkv ? a.v + (first - a.Hkv) * 128 : a.q + (first - nkv) * 128);
-    prefetch_l2(in + (row0 + (lane >> 1)) * stride + (lane & 1) * 64);
-  }
+  // A unit's rows (half a row per lane) come from memory while the table is formed or
+  // the unit before is worked on.
+  auto prefetch = [&](int u) {
+    const int t = lane >> 1;
+    if (u >= units || t < t0 || t >= t1) return;
+    const int64_t stride = u < a.Hkv ? a.k_stride : (u < nkv ? a.v_stride : a.q_stride);
+    const uint16_t* in = u < a.Hkv ? a.k + u * 128 : (u < nkv ? a.v + (u - a.Hkv) * 128 : a.q + (u - nkv) * 128);
+    prefetch_l2(in + (row0 + t) * stride + (lane & 1) * 64);
+  };
+  prefetch(first);
   if (threadIdx.x < kTile) {
     const bool in = (int)threadIdx.x >= t0 && (int)threadIdx.x < t1;
     pos[threadIdx.x] = in ? (int)(base + threadIdx.x) : -1;
@@ -424,6 +428,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_fp8_kernel(AppendFp8Args a
   __syncthreads();
   const int per = a.P / kTile, sub = (int)(base / kTile % per);
   for (int u = first; u < units; u += gridDim.y * kWarps) {
+    prefetch(u + gridDim.y * kWarps);
     if (u < nkv) {
       if (!page_ok) continue;
       const int tensor = u >= a.Hkv, h = u - (tensor ? a.Hkv : 0);
@@ -445,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_fp8_kernel(AppendFp8Args a
 
 // Slices of the heads per tile: about `per_sm` CTAs per SM, at most one unit per
 // warp.  A slice forms the tile's table again, so the append, whose units are
-// longer, takes fewer (8: ragged chunks 56 us, with 4: 61; a prompt of 8192 35,
+// longer, takes fewer (8: ragged chunks 55 us, with 4: 61; a prompt of 8192 35,
 // with 16: 38) than the rotary rows (16: 52 us, with 8 or 32: 55).
 constexpr int kRopePerSm = 16, kAppendPerSm = 8;
 unsigned slices(const Pool& p, long long tiles, int units, int per_sm) {
