@@ -20,8 +20,15 @@
 // barrier in the loop); the stored order is the operand order, so every lane
 // reads its fragments as 16-byte pieces without bank conflicts.  The work of a
 // (sequence, KV head) is split over CTAs by the sequence's own count of visible
-// tiles; the last CTA to finish joins the parts in split order.
+// tiles.  Up to eight splits of a pair, all on the device at once, are a cluster and
+// read one another's parts from shared memory (1024 tokens 4.8 us, of which 3.0 are an
+// empty call's; 6.7 through global memory); else the last CTA to finish joins the
+// parts.  Both go in split order: the result does not depend on timing.
+// 100,000 tokens (32 query heads, 8 KV heads): 37.9 us, 5.4 TB/s, 0.81 of a plain
+// copy's rate (4 us to the first tile, 4 for the join); 64 sequences of 8k to 32k
+// tokens: 397 us, 6.97 TB/s, 1.04 of it (a copy also writes).
 #include <algorithm>
+#include <atomic>
 
 #include "kv_device.cuh"
 #include "kv_fp8.h"
@@ -35,6 +42,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;                     // 4 KB tiles in flight per warp
 constexpr int kPolls = 1 << 22;                // bound of a copy's wait (about a second)
 constexpr int kMaxSplits = 64;
+constexpr int kMaxCluster = 8;                 // the portable cluster size
 constexpr int kPart = 132;                     // floats of a partial head: M, l, 2 unused, 128 sums
 constexpr float kNoRef = -3e38f;               // below every logit
 constexpr float kRaise = 15.f, kHead = 7.f;    // M moves when x > M + 15, to the largest x - 7
@@ -53,6 +61,7 @@ struct DecodeFp8Args {
   int* err;
   int polls;
   int stall;                                   // test hook: warp 0 of CTA 0 never starts its first copy
+  int cluster;                                 // the splits of a pair are a cluster
 };
 
 // The tiles a query at position n - 1 sees: the first `ns`, then those from
@@ -88,6 +97,29 @@ __device__ __forceinline__ uint32_t cvt_hi(uint32_t w) {   // bytes 2, 3
 }
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) { return h2_as_u32(__floats2half2_rn(a, b)); }
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// p of the cluster's CTA `rank`
+__device__ __forceinline__ uint32_t remote(const void* p, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float2 ld_remote2(uint32_t p) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_remote4(uint32_t p) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(p)
+               : "memory");
+  return v;
+}
 
 template <int G>
 __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a) {
@@ -332,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
   uint16_t* out = static_cast<uint16_t*>(a.c.out) + ((size_t)b * a.Hq + h * G) * 128;
   float* lse = a.c.lse ? a.c.lse + (size_t)b * a.Hq + h * G : nullptr;
   float* parts = static_cast<float*>(a.c.ws) + (size_t)pair * a.n_split * G * kPart;
+  float* own = wl + ((kWarps * G + 3) & ~3);   // cluster: this split's part
   for (int idx = threadIdx.x; idx < G * 128; idx += kThreads) {
     const int g = idx >> 7, c = idx & 127;
     float M = kNoRef;
@@ -349,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
       out[g * 128 + c] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
       if (c == 0 && lse) lse[g] = lse_of(M, l);
     } else {
-      float* p = parts + ((size_t)split * G + g) * kPart;
+      float* p = a.cluster ? own + g * kPart : parts + ((size_t)split * G + g) * kPart;
       p[4 + c] = s;
       if (c == 0) {
         p[0] = M;
@@ -358,6 +391,42 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
     }
   }
   if (a.n_split == 1) return;
+  if (a.cluster) {                             // each split joins some columns of all, in split order
+    cluster_barrier();
+    for (int col = split + a.n_split * threadIdx.x; col < G * 32; col += a.n_split * kThreads) {
+      const int g = col >> 5;
+      float2 ml[kMaxCluster];
+      float4 s[kMaxCluster];
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k) {
+        const uint32_t p = remote(own + g * kPart, min(k, a.n_split - 1));
+        ml[k] = ld_remote2(p);
+        s[k] = ld_remote4(p + 16 + 16 * (col & 31));
+      }
+      float M = kNoRef, l = 0.f;
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k) M = fmaxf(M, ml[k].x);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k) {
+        if (k >= a.n_split || ml[k].y == 0.f) continue;   // saw no token
+        const float f = exp2_neg(ml[k].x - M);
+        l = fmaf(f, ml[k].y, l);
+        acc.x = fmaf(f, s[k].x, acc.x);
+        acc.y = fmaf(f, s[k].y, acc.y);
+        acc.z = fmaf(f, s[k].z, acc.z);
+        acc.w = fmaf(f, s[k].w, acc.w);
+      }
+      const float r = l == 0.f ? 0.f : 1.f / l;
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * r, acc.y * r);
+      const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * r, acc.w * r);
+      *reinterpret_cast<uint2*>(out + g * 128 + 4 * (col & 31)) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      if ((col & 31) == 0 && lse) lse[g] = lse_of(M, l);
+    }
+    cluster_barrier();                         // the others may still be reading this CTA's part
+    return;
+  }
 
   // ---- the last CTA of the pair joins the splits, in their order ----
   __shared__ int last;
@@ -452,28 +521,65 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
   }
 }
 
-// Splits per (sequence, KV head), from the host's bound on visible tiles; a split
-// has at least a tile per warp.  Few pairs: one wave with one CTA per SM (8 pairs
-// of 100,000 tokens: 37.7 us against 39.9 with two per SM, whose join reads twice
-// the parts).  Enough pairs that this would leave SMs idle: two per SM (128 pairs
-// of 4,160 tokens: 29.3 us against 35.9).  More pairs than that: about six waves,
-// so that sequences of different lengths even out (512 pairs of 8k to 32k tokens:
-// 398 us, with four waves 408).
+// Splits per (sequence, KV head), from the host's bound on visible tiles (times by
+// graph replay where below 15 us).
+// - Up to two tiles per warp: none (256 tokens: 4.1 us, in two splits 6.2 through
+//   memory; 512 tokens: 5.3 us, in four splits of a cluster 4.9).
+// - Else a tile per warp at least, at most one wave of one CTA per SM where pairs are
+//   few (8 pairs of 100,000 tokens: 37.9 us against 39.9 with two per SM, whose join
+//   reads twice the parts), two per SM where that would leave SMs idle (128 pairs of
+//   4,160 tokens: 29.3 us against 35.9), and about six waves for more pairs, so that
+//   sequences of different lengths even out (512 pairs of 8k to 32k tokens: 398 us,
+//   with four waves 408).
+// - Up to sixteen tiles per warp in a cluster's worth of splits: no more than that
+//   (2048 tokens: 5.5 us; in 16 splits, joined through memory, 7.1; 4096 tokens of 8
+//   pairs: 8.2 capped, 7.6 not).
 int splits(const Pool& p, int B, long long max_len, int window, int n_sink) {
   long long tokens = max_len;
   if (window) tokens = std::min(tokens, (long long)window + n_sink + 2 * kTile);
   const long long tiles = (tokens + kTile - 1) / kTile, pairs = (long long)B * p.cfg.num_kv_heads, sms = p.sm_count;
   const long long want = sms >= 4 * pairs ? sms / pairs : (pairs <= sms ? 2 * sms / pairs : (12 * sms + pairs - 1) / pairs);
+  if (tiles <= 2 * kWarps) return 1;
   const long long most = std::min<long long>((tiles + kWarps - 1) / kWarps, kMaxSplits);
-  return (int)std::max(1ll, std::min(want, most));
+  const long long n = std::max(1ll, std::min(want, most));
+  return (int)(tiles <= 2 * kMaxCluster * kWarps ? std::min<long long>(n, kMaxCluster) : n);
+}
+
+// Clusters of n CTAs that the device holds at once.
+template <int G>
+int resident_clusters(int n) {
+  static std::atomic<int> known[kMaxCluster + 1];            // + 1; 0: not asked yet
+  int have = known[n].load(std::memory_order_relaxed);
+  if (have == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)n, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int count = 0;
+    if (cudaOccupancyMaxActiveClusters(&count, decode_fp8_kernel<G>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      count = 0;
+    }
+    have = count + 1;
+    known[n].store(have, std::memory_order_relaxed);
+  }
+  return have - 1;
 }
 
 template <int G>
 cudaError_t launch_t(const DecodeFp8Args& a, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(decode_fp8_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(decode_fp8_kernel<G>, dim3((unsigned)((long long)a.B * a.L.Hkv * a.n_split)), kThreads, kSmem,
-                          s, a);
+  const long long pairs = (long long)a.B * a.L.Hkv;
+  DecodeFp8Args b = a;
+  b.cluster = a.n_split > 1 && a.n_split <= kMaxCluster && pairs <= resident_clusters<G>(a.n_split);
+  return launch_dependent(decode_fp8_kernel<G>, dim3((unsigned)(pairs * a.n_split)), kThreads, kSmem, s,
+                          b.cluster ? a.n_split : 1, b);
 }
 
 }  // namespace

@@ -1047,9 +1047,9 @@ cudaError_t launch_prefill_fp8(const Pool& p, const Fp8Store& f, int layer, int 
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(prefill_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(prefill_fp8_kernel, dim3((unsigned)ctas), kThreads, kSmem, s, a);
+  e = launch_dependent(prefill_fp8_kernel, dim3((unsigned)ctas), kThreads, kSmem, s, 1, a);
   if (e != cudaSuccess || a.n_split == 1) return e;
-  return launch_dependent(prefill_join_kernel, dim3((unsigned)(((long long)n_seqs * max_q * a.Hq + 7) / 8)), 256, 0, s, a);
+  return launch_dependent(prefill_join_kernel, dim3((unsigned)(((long long)n_seqs * max_q * a.Hq + 7) / 8)), 256, 0, s, 1, a);
 }
 
 }  // namespace kvint2

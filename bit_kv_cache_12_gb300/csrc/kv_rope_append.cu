@@ -530,7 +530,7 @@ cudaError_t launch_rope(const Pool& p, const RopeParams& r, int n_tokens, const 
   a.n_tokens = n_tokens;
   const long long tiles = ((long long)n_tokens + kTile - 1) / kTile;
   const dim3 grid((unsigned)tiles, slices(p, tiles, a.heads[0] + a.heads[1], kRopePerSm));
-  return launch_dependent(r.interleaved ? rope_kernel<true> : rope_kernel<false>, grid, kThreads, 0, s, a, r);
+  return launch_dependent(r.interleaved ? rope_kernel<true> : rope_kernel<false>, grid, kThreads, 0, s, 1, a, r);
 }
 
 cudaError_t launch_append_fp8(const Pool& p, const Fp8Store& f, const RopeParams& r, int layer, int n_seqs,
@@ -562,7 +562,7 @@ cudaError_t launch_append_fp8(const Pool& p, const Fp8Store& f, const RopeParams
   a.err = p.err;
   const long long tiles = (long long)n_seqs * a.tiles;
   const dim3 grid((unsigned)tiles, slices(p, tiles, 2 * a.Hkv + (a.q ? a.Hq : 0), kAppendPerSm));
-  return launch_dependent(r.interleaved ? append_fp8_kernel<true> : append_fp8_kernel<false>, grid, kThreads, 0, s, a, r);
+  return launch_dependent(r.interleaved ? append_fp8_kernel<true> : append_fp8_kernel<false>, grid, kThreads, 0, s, 1, a, r);
 }
 
 }  // namespace kvint2
