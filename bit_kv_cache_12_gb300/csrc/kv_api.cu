@@ -522,7 +522,8 @@ kv_status_t kv_decode_attention_fp8(kv_pool_t* pool, int32_t layer, int32_t B, c
   if (kv_status_t st = on_pool_device(p); st != KV_OK) return st;
   return cuda_status(kvint2::launch_decode_fp8(p, pool->fp8, layer, B,
                                                {q, seq_len, page_table, max_pages_per_seq, max_seq_len, softmax_scale,
-                                                window, n_sink, out, lse, workspace},
+                                                kvint2::effective_window(window, max_seq_len), n_sink, out, lse,
+                                                workspace},
                                                static_cast<cudaStream_t>(stream)));
 }
 
@@ -551,8 +552,9 @@ kv_status_t kv_prefill_attention_fp8(kv_pool_t* pool, int32_t layer, int32_t n_s
   if (need == 0 || workspace_bytes < need) return KV_ERR_INVALID_ARG;
   if (kv_status_t st = on_pool_device(p); st != KV_OK) return st;
   return cuda_status(kvint2::launch_prefill_fp8(p, pool->fp8, layer, n_seqs, cu_q, max_q_per_seq,
-                                                {q, seq_len, page_table, max_pages_per_seq, max_seq_len,
-                                                 softmax_scale, window, n_sink, out, lse, workspace},
+                                                {q, seq_len, page_table, max_pages_per_seq, max_seq_len, softmax_scale,
+                                                 kvint2::effective_window(window, max_seq_len), n_sink, out, lse,
+                                                 workspace},
                                                 static_cast<cudaStream_t>(stream)));
 }
 

@@ -91,6 +91,9 @@ struct AttnCall {
   float* lse;                // or NULL
   void* ws;
 };
+// A window that reaches from the last position back to the first hides nothing: none
+// (and what is left keeps the kernels' positions minus windows in 32 bits).
+inline int effective_window(int window, int max_len) { return window >= max_len ? 0 : window; }
 
 // ln(2^M l): M stands near -eV and log2 l near eV (up to 64), so l's exponent is
 // added to M before its mantissa's logarithm (fp32 near 64 has steps of 2^-18).

@@ -340,6 +340,61 @@ def test_pages_given_up_behind_the_window(cuda_lib, page):
     s.pool.close()
 
 
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31 - 300, 5), (900, 0), (899, 0),
+                                          (50, 2 ** 31 - 1), (50, 800)])
+def test_windows_and_first_tokens_beyond_the_sequence(cuda_lib, window, sinks):
+    """Windows and counts of first tokens up to the largest integer, with queries before the first position too."""
+    s = Setup(8, 2, 16, 2, 900, seed=12)
+    s.fill()
+    n = [900, 333]
+    decode_and_check(s, bf16(s.rng.standard_normal((2, 8, 128))), n, window, sinks)
+    count = [300, 340]                                    # the second sequence's first seven see nothing
+    prefill_and_check(s, bf16(s.rng.standard_normal((640, 8, 128))), count, n, window, sinks, sample=150)
+    s.pool.close()
+
+
+def test_a_graph_with_copies_and_two_streams(cuda_lib):
+    """Append, decode and prompt attention captured behind copies, one of them on another stream."""
+    s = Setup(8, 2, 16, 1, 1100, seed=8, rope=dict(theta=1e4))
+    s.fill()
+    new_q, new_k = bf16(s.rng.standard_normal((40, 8, 128))), bf16(s.rng.standard_normal((40, 2, 128)))
+    q, k, q_out = torch.zeros_like(new_q), torch.zeros_like(new_k), torch.zeros_like(new_q)
+    out1, out2 = torch.zeros_like(new_q[:1]), torch.zeros_like(new_q)
+    cu, start, n, table = i32([0, 40]), i32([1060]), i32([1100]), i32(s.table)
+    pool, side, scale = s.pool.handle, torch.cuda.Stream(), 1 / math.sqrt(128)
+    need = max(native.kv_decode_workspace_bytes(pool, 1, 1100), native.kv_prefill_workspace_bytes(pool, 1, 40, 1100))
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+
+    def step():
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        q.copy_(new_q)
+        with torch.cuda.stream(side):
+            k.copy_(new_k)
+        here.wait_stream(side)
+        native.kv_append_fp8(pool, 0, 1, q, 1024, k, 256, k, 256, cu, start, table, s.width, 40, q_out)
+        native.kv_decode_attention_fp8(pool, 0, 1, q_out[39:], n, table, s.width, 1100, scale, 0, 0, out1, None, ws, need)
+        native.kv_prefill_attention_fp8(pool, 0, 1, q_out, cu, n, table, s.width, 40, 1100, scale, 0, 0, out2, None, ws, need)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):                         # before any eager call of these shapes
+        step()
+    for _ in range(5):
+        for x in (q, k, q_out, out1, out2):
+            x.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    got = out1.clone(), out2.clone()
+    for x in (q, k, q_out, out1, out2):
+        x.zero_()
+    step()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], out1) and torch.equal(got[1], out2) and out1.any() and s.pool.error() == 0
+    s.model.codes[...], s.model.exps[...] = s.codes.cpu().numpy(), s.exps.cpu().numpy()
+    s.check_rows(q_out[39:], [(0, 1099)], f64(out1), s.decode(q_out[39:], [1100])[1], 0, 0, lens=[1100])
+    s.pool.close()
+
+
 def test_attention_over_codes_beyond_32_bits(cuda_lib):
     """Pages past 2^32 bytes of codes attend as the same pages at the pool's start."""
     s = Setup(8, 8, 16, 2, 700, seed=3, spare=0)
