@@ -531,9 +531,9 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
 //   4,160 tokens: 29.3 us against 35.9), and about six waves for more pairs, so that
 //   sequences of different lengths even out (512 pairs of 8k to 32k tokens: 398 us,
 //   with four waves 408).
-// - Up to sixteen tiles per warp in a cluster's worth of splits: no more than that
-//   (2048 tokens: 5.5 us; in 16 splits, joined through memory, 7.1; 4096 tokens of 8
-//   pairs: 8.2 capped, 7.6 not).
+// - Where a cluster's worth of splits has up to two tiles per warp: no more than those
+//   (2048 tokens: 5.5 us; in 16 splits, joined through memory, 7.1; beyond, 4096
+//   tokens of 8 pairs: 8.2 so, 7.6 in 19).
 int splits(const Pool& p, int B, long long max_len, int window, int n_sink) {
   long long tokens = max_len;
   if (window) tokens = std::min(tokens, (long long)window + n_sink + 2 * kTile);
