@@ -40,7 +40,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;                     // 4 KB tiles in flight per warp
-constexpr int kPolls = 1 << 22;                // bound of a copy's wait (about a second)
+constexpr int kPolls = 1 << 18;                // bound of a copy's wait: a poll suspends for up to 3.7 us, so about a second
 constexpr int kMaxSplits = 64;
 constexpr int kMaxCluster = 8;                 // the portable cluster size
 constexpr int kPart = 132;                     // floats of a partial head: M, l, 2 unused, 128 sums
@@ -242,7 +242,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
       next = stored(k + 32 + lane, next_pid);
       next_pid = page_of(k + 64 + lane);
     }
-    if (!mbar_wait(bar + stage, phase, a.polls)) {
+    // the lanes vote: a copy that lands just as the limit runs out must not part them
+    if (!__all_sync(0xffffffffu, mbar_wait(bar + stage, phase, a.polls))) {
       ok = false;
       break;
     }
@@ -324,15 +325,19 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
       phase ^= 1;
     }
   }
-  if (!ok) {                                   // a copy did not arrive: wait (bounded) for those in flight
+  if (!ok) {
+    // A copy did not arrive in time.  Those in flight, this one among them, would land on
+    // what is written over the ring: they are waited for, by the full limit (but not for
+    // one that the test hook never started).
     if (lane == 0) flag_error(a.err, KV_DEVERR_TIMEOUT);
-    for (int kk = k + 1; kk < min(mine, k + kStages); ++kk) {
+    for (int kk = k; kk < min(mine, k + kStages); ++kk) {
+      if (!(a.stall && kk == 0 && blockIdx.x == 0 && warp == 0)) mbar_wait(bar + stage, phase, kPolls);
       if (++stage == kStages) {
         stage = 0;
         phase ^= 1;
       }
-      mbar_wait(bar + stage, phase, a.polls);
     }
+    __syncwarp();
     M0 = M1 = kNoRef;
     l0 = l1 = 0.f;
   }
