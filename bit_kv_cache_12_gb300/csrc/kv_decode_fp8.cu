@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 
-  bool ok = true;
+  bool ok = true, large = false;               // large: some head's reference is
   int k = 0, stage = 0, phase = 0;
   for (; k < mine; ++k) {
     if ((k & 31) == 0) {                       // the next 32: their page ids have been on the way since the last batch
@@ -266,9 +266,9 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
         mma_f16(sb, cvt_lo(b0), cvt_lo(b1), cvt_hi(b0), cvt_hi(b1), qf[1][2 * w], qf[1][2 * w + 1]);
       }
       const float ev = (float)(int8_t)(e2 >> 8), fk = exp2f((float)(int8_t)(e2 & 0xFF));
-      const float c0 = cs0 * fk, c1 = cs1 * fk;
-      const float s0 = sa[0] + sb[0], s1 = sa[1] + sb[1];      // token r, heads 2j, 2j + 1
-      const float s2 = sa[2] + sb[2], s3 = sa[3] + sb[3];      // token r + 8
+      float c0 = cs0 * fk, c1 = cs1 * fk;
+      float s0 = sa[0] + sb[0], s1 = sa[1] + sb[1];      // token r, heads 2j, 2j + 1
+      float s2 = sa[2] + sb[2], s3 = sa[3] + sb[3];      // token r + 8
       float x0 = fmaf(s0, c0, ev), x1 = fmaf(s1, c1, ev), x2 = fmaf(s2, c0, ev), x3 = fmaf(s3, c1, ev);
       if (vis != 0xFFFFu) {                    // hidden tokens: no weight, and codes of zero
         if (!((vis >> r) & 1)) x0 = x1 = -INFINITY;
@@ -280,9 +280,11 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
         if (!(v5 & 1)) vw[2] = z;
         if (!(v5 & 2)) vw[3] = z;
       }
-      if (__any_sync(0xffffffffu, fmaxf(x0, x2) > M0 + kRaise || fmaxf(x1, x3) > M1 + kRaise)) {
+      float d0 = ev - M0, d1 = ev - M1;
+      if (__any_sync(0xffffffffu, large || fmaxf(x0, x2) > M0 + kRaise || fmaxf(x1, x3) > M1 + kRaise)) {
+        // as differences: where M is large, M + 15 is rounded by as much as that
         const float t0 = warp_max_xor(fmaxf(x0, x2), 4), t1 = warp_max_xor(fmaxf(x1, x3), 4);
-        const float n0 = t0 > M0 + kRaise ? t0 - kHead : M0, n1 = t1 > M1 + kRaise ? t1 - kHead : M1;
+        const float n0 = t0 - M0 > kRaise ? t0 - kHead : M0, n1 = t1 - M1 > kRaise ? t1 - kHead : M1;
         const float f0 = exp2_neg(M0 - n0), f1 = exp2_neg(M1 - n1);
         M0 = n0;
         M1 = n1;
@@ -295,9 +297,16 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
           o[i][2] *= f0;
           o[i][3] *= f1;
         }
+        d0 = ev - M0;
+        d1 = ev - M1;
+        const bool g0 = large_reference(M0), g1 = large_reference(M1);
+        large = __any_sync(0xffffffffu, g0 || g1);
+        // weights from the rounded logits; in here, so that the usual tile has no more to
+        // do (100,000 tokens: 39.0 us; with a choice at each weight 39.4 to 40.2)
+        if (g0) s0 = x0 - M0, s2 = x2 - M0, c0 = 1.f, d0 = 0.f;
+        if (g1) s1 = x1 - M1, s3 = x3 - M1, c1 = 1.f, d1 = 0.f;
       }
       // once more against M: x was rounded at eV's size, ev - M is exact near the largest weight
-      const float d0 = ev - M0, d1 = ev - M1;
       auto weight = [](float x, float y) { return x == -INFINITY ? 0.f : exp2_neg(y); };   // -inf: hidden
       const float w0 = weight(x0, fmaf(s0, c0, d0)), w1 = weight(x1, fmaf(s1, c1, d1));
       const float w2 = weight(x2, fmaf(s2, c0, d0)), w3 = weight(x3, fmaf(s3, c1, d1));

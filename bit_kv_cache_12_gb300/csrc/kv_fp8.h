@@ -95,6 +95,13 @@ struct AttnCall {
 // (and what is left keeps the kernels' positions minus windows in 32 bits).
 inline int effective_window(int window, int max_len) { return window >= max_len ? 0 : window; }
 
+// Whether a reference M (base 2) is so large that the roundings of logits and reference,
+// each half a step of |M|, could carry a weight out of fp16's range: from there on weights
+// come from the logit as it was rounded when it was compared with M, so that the largest
+// one is in [2^0, 2^15] whatever the steps are.  Below, where a step is 2^-3 at most, they
+// come from the product and ev - M in one rounding, which is closer.
+__device__ __forceinline__ bool large_reference(float M) { return fabsf(M) > 0x1p20f && M > -2.9e38f; }
+
 // ln(2^M l): M stands near -eV and log2 l near eV (up to 64), so l's exponent is
 // added to M before its mantissa's logarithm (fp32 near 64 has steps of 2^-18).
 __device__ __forceinline__ float lse_of(float M, float l) {

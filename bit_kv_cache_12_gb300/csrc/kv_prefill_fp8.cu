@@ -668,6 +668,7 @@ __device__ __forceinline__ bool softmax_rows(const PrefillFp8Args& a, const Work
   const uint32_t ts = trow + 128 * tile, to = trow + 256 + 128 * tile;
   const int i0 = tile * kRows + (threadIdx.x & 127);
   bool check = false;                          // the pass before was partial
+  bool large = false;                          // this row's reference is
   for (int it = 0;; ++it, ++g) {
     if (!__all_sync(0xffffffffu, wait(sh->bars + kSFull + tile, g & 1))) return false;
     fence_after();
@@ -676,7 +677,8 @@ __device__ __forceinline__ bool softmax_rows(const PrefillFp8Args& a, const Work
     const bool partial = info.partial != 0, last = info.last != 0;
     check = partial;
     // above 0, so that a hidden key's -inf stays one
-    const float c = fmaxf(cs * info.fk, 1.17549435e-38f), ev = info.ev;
+    float c = fmaxf(cs * info.fk, 1.17549435e-38f);
+    const float ev = info.ev;
     float v[kKeys];
 #pragma unroll
     for (int q = 0; q < 4; ++q) ld32(ts + 32 * q, v + 32 * q);
@@ -697,8 +699,9 @@ __device__ __forceinline__ bool softmax_rows(const PrefillFp8Args& a, const Work
       for (int i = 2; i < 32; i += 2) top[q] = max3(top[q], v[32 * q + i], v[32 * q + i + 1]);
     }
     const float x = fmaf(max3(fmaxf(top[0], top[1]), top[2], top[3]), c, ev);
-    const bool raise = x > ro.M + kRaise;
-    if (__any_sync(0xffffffffu, raise)) {
+    const bool raise = x - ro.M > kRaise;      // as a difference: where M is large, M + 15 is rounded by as much as that
+    float d = ev - ro.M;
+    if (__any_sync(0xffffffffu, raise || large)) {
       const float n = raise ? x - kHead : ro.M;
       const float f = exp2_neg(ro.M - n);
       ro.M = n;
@@ -718,8 +721,16 @@ __device__ __forceinline__ bool softmax_rows(const PrefillFp8Args& a, const Work
           st16(to + 32 * q + 16, u);
         }
       }
+      d = ev - n;
+      large = large_reference(n);
+      if (large) {                             // weights from the rounded logits; in here, where no usual pass comes by
+        const uint64_t cc = f2(c, c), ee = f2(ev, ev), mm = f2(-n, -n);
+#pragma unroll
+        for (int i = 0; i < kKeys; i += 2) f2_split(f2_add(f2_fma(f2(v[i], v[i + 1]), cc, ee), mm), v[i], v[i + 1]);
+        c = 1.f;
+        d = 0.f;
+      }
     }
-    const float d = ev - ro.M;
     const uint64_t c2 = f2(c, c), d2 = f2(d, d);
     uint64_t s0 = f2(0.f, 0.f), s1 = s0;
 #pragma unroll
