@@ -107,6 +107,9 @@ struct Shared {
   uint32_t tmem;
   int abort;
   int converted;                               // passes whose K is in shared memory
+  int given;                                   // items published so far
+  int taken;                                   // an item taken on but not published yet, else -1
+  int next[8];                                 // softmax warps, at their end: the item whose rows would have come next
 };
 constexpr uint32_t kSmem = kOffInfo + sizeof(Shared) + 1024;
 
@@ -117,7 +120,7 @@ struct PrefillFp8Args {
   int n_seqs, max_q, Hq, G, n_split, q_blocks;
   int* err;
   int polls;
-  int stall;                                   // test hook: CTA 0's walker never hands over its first pass
+  int stall;                                   // test hook: CTA 0's walker withholds its first item's last pass
 };
 
 // ---- tcgen05 ----------------------------------------------------------------
@@ -457,18 +460,20 @@ __device__ __forceinline__ bool walk_item(const PrefillFp8Args& a, const Work& w
         p.mulv[lane] = half_pow2(ev - mv);
         if (lane < 4) p.nan[lane] = 0;
       }
+      const bool last = i + 1 == w.i1 && !left;
       if (lane == 0) {
         p.t0 = t0;
         p.blocks = now;
         p.fk = pow2i(max(min(mk, 127), -126));
         p.ev = (float)mv;
-        p.last = i + 1 == w.i1 && !left;
+        p.last = last;
         p.keys = w.keys;
         p.stop = 0;
         p.partial = now != 0xFFu || t0 + kKeys - 1 > w.first ||
                     (a.c.window && t0 < w.keys - a.c.window && t0 + kKeys > w.sinks);
       }
       __syncwarp();
+      if (a.stall && last && blockIdx.x == 0) return false;
       if (lane == 0) arrive(sh->bars + kPass + (n & (kRing - 1)));
       ++n;
     } while (left);
@@ -488,6 +493,8 @@ __device__ __forceinline__ void walk(const PrefillFp8Args& a, Shared* sh, const 
     if (item >= kItems && !ready(kFree + slot, (item / kItems - 1) & 1)) return false;
     if (lane == 0) {
       sh->work[slot] = w;
+      sh->given = item + 1;
+      sh->taken = -1;
       arrive(sh->bars + kItem + slot);
     }
     __syncwarp();
@@ -513,7 +520,6 @@ __device__ __forceinline__ void walk(const PrefillFp8Args& a, Shared* sh, const 
       *reinterpret_cast<volatile int*>(wait.abort) = 1;
       return;
     }
-    if (!ok) return;
     int got;
     asm volatile(
         "{ .reg .pred p; .reg .b128 h; ld.shared.b128 h, [%2]; "
@@ -522,6 +528,8 @@ __device__ __forceinline__ void walk(const PrefillFp8Args& a, Shared* sh, const 
         : "=r"(got), "+r"(x)
         : "r"(smem_u32(&sh->cancel))
         : "memory");
+    if (lane == 0) sh->taken = got ? x : -1;
+    if (!ok) return;
     if (!__all_sync(0xffffffffu, got)) break;
   }
   Work stop{};
@@ -877,6 +885,33 @@ __device__ __forceinline__ void write_row(const PrefillFp8Args& a, const Work& w
   }
 }
 
+// Rows of items that a CTA took on and did not get to before it gave up: not a number
+// (in a split, the row's part: the join would read what the workspace held before).
+// first: the first item whose rows this warp has not written.
+__device__ __forceinline__ void abandon(const PrefillFp8Args& a, const Shared* sh, int first) {
+  const int i = threadIdx.x, given = sh->given;   // this thread's row of a block
+  const float nan = __uint_as_float(0x7FC00000u);
+#pragma unroll 1
+  for (int item = first; item <= given; ++item) {
+    Work w;
+    if (item < given)
+      w = sh->work[item & (kItems - 1)];
+    else if (sh->taken < 0 || !find_work(a, sh->taken, w))
+      return;
+    if (w.state == kStop) return;
+    const Row row(a, w, i);
+    if (!row.live) continue;
+    if (a.n_split > 1) {
+      static_cast<float*>(a.c.ws)[((((size_t)w.s * a.max_q + row.token) * a.Hq + row.hq) * a.n_split + w.split) * 132] = nan;
+    } else {
+      uint4* out = static_cast<uint4*>(a.c.out) + row.qrow * 16;
+#pragma unroll 1
+      for (int c = 0; c < 16; ++c) out[c] = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+      if (a.c.lse) a.c.lse[row.qrow] = nan;
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args a) {
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -904,6 +939,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
     mbar_fence_init();
     sh->abort = 0;
     sh->converted = 0;
+    sh->given = 0;
+    sh->taken = blockIdx.x;
   }
   if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh->tmem)),
@@ -928,7 +965,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
     bool ok = true;
     int g = 0, keyed = 0, state = kStart;
     float cs = 0.f;
-    for (int item = -1; state != kStop; ++item) {
+    int item = -1;
+    for (; state != kStop; ++item) {
       const Work& w = sh->work[item & (kItems - 1)];
       RowOut ro;
       if (state == kKeyed) ok = softmax_rows(a, w, trow, tile, sh, wait, cs, g, ro);
@@ -967,18 +1005,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
       }
       state = ok ? next_state : kStop;
     }
+    if ((threadIdx.x & 31) == 0) sh->next[warp] = item;   // kept there: held in a register to the end it costs spills
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
     convert_tiles(a, sm, sh, wait);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-    if (warp == 13 && !(a.stall && blockIdx.x == 0)) walk(a, sh, wait);
+    if (warp == 13) walk(a, sh, wait);
     if (warp == 12) issue_products(__shfl_sync(0xffffffffu, tmem, 0), sm, sh, wait);
   }
   __syncwarp();
   fence_before();
   __syncthreads();
   fence_after();
+  if (warp < 8 && sh->abort) abandon(a, sh, sh->next[warp]);
   if (warp == 12) {
     if (sh->abort) {                           // products may be in flight: wait (bounded) before giving back the memory
       if (elect_one()) {                       // the lane that issued them

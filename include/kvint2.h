@@ -369,8 +369,8 @@ kv_status_t kv_decode_attention_noalloc(kv_pool_t* pool, int32_t layer, int32_t 
  * nothing faults and nothing hangs.  On an FP8 pool the first warp of
  * kv_decode_attention_fp8's first CTA waits for a copy that is never started,
  * and kv_prefill_attention_fp8's first CTA for keys that are never handed over;
- * both end the same way (prompt rows of that CTA become NaN or are left as they
- * were).  max_polls > 0 replaces the default poll limit of those waits (about a
+ * both end the same way (the decode skips that warp's share of the tokens, the
+ * prompt rows that CTA had taken on and not finished become NaN).  max_polls > 0 replaces the default poll limit of those waits (about a
  * second) for the pool's decode, prompt and bulk append calls; 0 restores it.
  * enable = 0 restores normal calls.  Not for production use. */
 kv_status_t kv_debug_stall_first_copy(kv_pool_t* pool, int32_t enable, int32_t max_polls);
