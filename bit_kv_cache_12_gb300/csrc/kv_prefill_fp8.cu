@@ -56,7 +56,7 @@ constexpr int kThreads = 16 * 32;              // four warpgroups
 // share the launch's 128 each
 constexpr int kSoftRegs = 184, kConvRegs = 96, kIssueRegs = 48;
 static_assert(2 * kSoftRegs + kConvRegs + kIssueRegs <= 4 * 128, "setmaxnreg.inc draws on the launch's registers");
-constexpr int kPolls = 1 << 20;
+constexpr int kPolls = 1 << 18;                // bound of a wait: a poll suspends for up to 3.7 us, so about a second
 constexpr int kMaxSplits = 32;
 constexpr float kNoRef = -3e38f;
 constexpr float kRaise = 15.f, kHead = 7.f;
@@ -107,6 +107,7 @@ struct Shared {
   uint32_t tmem;
   int abort;
   int converted;                               // passes whose K is in shared memory
+  int steps;                                   // items looked at so far
   int given;                                   // items published so far
   int taken;                                   // an item taken on but not published yet, else -1
   int next[8];                                 // softmax warps, at their end: the item whose rows would have come next
@@ -282,6 +283,7 @@ __device__ __forceinline__ bool find_work(const PrefillFp8Args& a, int x, Work& 
 struct Waiter {
   int* abort;
   int polls;
+  const int* steps;                            // of the walker
   // whether the phase with `parity` completed; a wait that runs out ends every role
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
     for (int i = 0; !mbar_wait(bar, parity, 1); ++i) {
@@ -289,6 +291,22 @@ struct Waiter {
         *reinterpret_cast<volatile int*>(abort) = 1;
         return false;
       }
+    }
+    return true;
+  }
+  // The same for what the walker hands over: the limit starts again while it passes blocks
+  // without rows (3 ns each over the device: 6 s for the largest grid).
+  __device__ __forceinline__ bool handed(uint64_t* bar, uint32_t parity) const {
+    int seen = -1;
+    for (int i = 0; !mbar_wait(bar, parity, 1); ++i) {
+      if ((i & 63) != 63) continue;
+      const int now = *reinterpret_cast<const volatile int*>(steps);
+      if (*reinterpret_cast<volatile int*>(abort) || (i >= polls && now == seen)) {
+        *reinterpret_cast<volatile int*>(abort) = 1;
+        return false;
+      }
+      if (now != seen) i = 0;
+      seen = now;
     }
     return true;
   }
@@ -338,7 +356,7 @@ __device__ __forceinline__ void convert_tiles(const PrefillFp8Args& a, uint8_t* 
       x[u + 3] = ld_stream_v4(src + (size_t)t.w * kFp8TileBytes);
     }
   };
-  auto ready = [&](int it) { return __all_sync(0xffffffffu, wait(sh->bars + kPass + (it & (kRing - 1)), (it / kRing) & 1)); };
+  auto ready = [&](int it) { return __all_sync(0xffffffffu, wait.handed(sh->bars + kPass + (it & (kRing - 1)), (it / kRing) & 1)); };
   if (!ready(0) || sh->pass[0].stop) return;
   load(k, ksrc, sh->pass[0]);
   load(v, vsrc, sh->pass[0]);
@@ -397,11 +415,11 @@ __device__ __forceinline__ void convert_tiles(const PrefillFp8Args& a, uint8_t* 
 __device__ __forceinline__ bool pass_free(Shared* sh, const Waiter& wait, int n) {
   bool ok = true;
   for (int spin = 0; n >= kRing && *reinterpret_cast<volatile int*>(&sh->converted) < n - 3; ++spin) {
-    if (spin >= wait.polls || *reinterpret_cast<volatile int*>(wait.abort)) {
+    if (spin / 32 >= wait.polls || *reinterpret_cast<volatile int*>(wait.abort)) {
       ok = false;
       break;
     }
-    __nanosleep(100);
+    __nanosleep(100);                          // 32 of these to a poll of a barrier
   }
   ok = __all_sync(0xffffffffu, ok);
   if (!ok) *reinterpret_cast<volatile int*>(wait.abort) = 1;
@@ -512,6 +530,7 @@ __device__ __forceinline__ void walk(const PrefillFp8Args& a, Shared* sh, const 
           "r"(smem_u32(sh->bars + kCancel))
           : "memory");
     }
+    if (lane == 0) *reinterpret_cast<volatile int*>(&sh->steps) = asked + 1;
     __syncwarp();
     Work w;
     if (find_work(a, x, w)) ok = publish(w, items++) && (w.state != kKeyed || walk_item(a, w, sh, wait, passes));
@@ -577,7 +596,7 @@ __device__ __forceinline__ void issue_products(uint32_t tmem, uint8_t* sm, Share
   int g = 0, keyed = 0;                        // passes and items with keys so far
   for (int item = 0;; ++item) {
     const int slot = item & (kItems - 1);
-    if (!ready(kItem + slot, (item / kItems) & 1)) return;
+    if (!__all_sync(0xffffffffu, wait.handed(sh->bars + kItem + slot, (item / kItems) & 1))) return;
     const int state = sh->work[slot].state;
     if (state == kStop) return;
     if (state == kKeyed) {
@@ -939,6 +958,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
     mbar_fence_init();
     sh->abort = 0;
     sh->converted = 0;
+    sh->steps = 0;
     sh->given = 0;
     sh->taken = blockIdx.x;
   }
@@ -953,14 +973,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
   fence_after();
   after_predecessor();
   const uint32_t tmem = sh->tmem;
-  const Waiter wait{&sh->abort, a.polls};
+  const Waiter wait{&sh->abort, a.polls, &sh->steps};
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int tile = warp >> 2, m = threadIdx.x & 127;
     const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const int m0 = 32 * (warp & 3);            // this warp's rows of the tile
     auto given = [&](int item) {
-      return __all_sync(0xffffffffu, wait(sh->bars + kItem + (item & (kItems - 1)), (item / kItems) & 1)) != 0;
+      return __all_sync(0xffffffffu, wait.handed(sh->bars + kItem + (item & (kItems - 1)), (item / kItems) & 1)) != 0;
     };
     bool ok = true;
     int g = 0, keyed = 0, state = kStart;

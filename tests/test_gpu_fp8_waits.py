@@ -100,3 +100,21 @@ def test_prefill_blocks_taken_on_and_given_up(cuda_lib):
     assert (heads.all(-1) == heads.any(-1)).all()              # whole groups of heads,
     assert 0 < heads.any(-1).sum() <= 24 + 32                  # of two blocks of 32 queries at most
     s.pool.close()
+
+
+def test_prefill_bound_on_queries_far_above_their_number(cuda_lib):
+    """Blocks without rows take longer to pass over than a wait may last (here by a short limit; with the usual one from
+    about 10^9 blocks on, which the calls allow): no wait runs out, and every row is written."""
+    s = Setup(8, 8, 16, 16, 300, seed=5)
+    s.fill()
+    count = s.rng.integers(1, 40, 16).tolist()
+    n = [int(s.rng.integers(c, 301)) for c in count]
+    q = bf16(s.rng.standard_normal((sum(count), 8, 128)))
+    want = s.prefill(q, count, n)
+    native.kv_debug_stall_first_copy(s.pool.handle, 0, 300)    # about a millisecond
+    for _ in range(2):
+        out, lse = s.prefill(q, count, n, most=6553600)        # 3.3 million blocks: about ten
+        assert s.pool.error() == 0
+        np.testing.assert_array_equal(out, want[0])
+        np.testing.assert_array_equal(lse, want[1])
+    s.pool.close()
