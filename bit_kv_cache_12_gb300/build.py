@@ -29,7 +29,7 @@ def nvcc():
 
 def _compile(src, obj, verbose):
     cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
-           "-Xcompiler", "-O3", "-c", os.path.join(CSRC, src), "-o", obj]
+           "-Xcompiler", "-O3,-ffp-contract=off", "-c", os.path.join(CSRC, src), "-o", obj]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -4,8 +4,9 @@
 //   (a cos - b sin, b cos + a sin) * att,  angle = p * w_i,
 // in fp32, rounded once (bf16 for q and k rows, e4m3 for cached K).  The angle
 // is formed as a fraction of a turn in 64-bit integers, p * (w_i / 2 pi) modulo
-// one turn: the product wraps by itself, so the reduction is exact at any
-// position and costs one integer multiply; sincospif then sees [-1, 1).
+// one turn: the product wraps by itself, so the reduction costs one integer
+// multiply and adds nothing to the speed's own 2^-65 of a turn per position;
+// sincospif then sees an eighth of a turn to either side.
 //
 // Append: e = the smallest exponent whose range (448 * 2^e) holds the 16 x 128
 // values of a tile, codes = e4m3(value * 2^-e).  The K exponent goes by the
@@ -72,8 +73,9 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
 }
 
 // cos and sin of `turns` (units of 2^-64 of a turn), times att.  The nearest
-// quarter turn is taken off in integers, so the fp32 argument is at most a
-// quarter of pi and its rounding moves the angle by at most 2^-26.
+// quarter turn is taken off in integers, so the fp32 argument is at most an eighth
+// of a turn and its rounding moves the angle by at most 2^-28 of a turn (2^-25.3
+// radians), and by less the nearer it is to a quarter.
 __device__ __forceinline__ float2 turn_cos_sin(unsigned long long turns, float att) {
   const unsigned long long quarter = (turns + (1ull << 61)) >> 62;
   const int r = (int)((long long)(turns - (quarter << 62)) >> 30);   // in 2^-34 of a turn
@@ -458,6 +460,23 @@ unsigned slices(const Pool& p, long long tiles, int units, int per_sm) {
   return (unsigned)std::max(1ll, std::min<long long>((units + kWarps - 1) / kWarps, want));
 }
 
+// A speed in radians per position (taken as the double that it is) as turns per position
+// modulo one turn, in units of 2^-64, for |w| up to 2^40: 1 / 2 pi in two doubles, the
+// product's rounding by fma.
+unsigned long long turns_of(double w) {
+  constexpr double kInvHi = 0x1.45f306dc9c883p-3, kInvLo = -0x1.6b01ec5417056p-57;
+  const double v = std::fabs(w);
+  volatile double product = v * kInvHi;          // rounded here, whatever the compiler fuses below
+  const double p = product;
+  double rest = std::fma(v, kInvHi, -p) + v * kInvLo;
+  rest -= std::rint(rest);
+  if (rest == 0.5) rest = -0.5;
+  const double f = p - std::floor(p), hi = std::floor(std::ldexp(f, 32));
+  const double lo = std::ldexp(f, 64) - std::ldexp(hi, 32);
+  const unsigned long long t = ((unsigned long long)hi << 32) + (unsigned long long)std::llrint(lo + std::ldexp(rest, 64));
+  return w < 0 ? 0ull - t : t;
+}
+
 }  // namespace
 
 kv_status_t rope_params(const kv_rope_config_t& c, RopeParams* out) {
@@ -504,12 +523,7 @@ kv_status_t rope_params(const kv_rope_config_t& c, RopeParams* out) {
   r.interleaved = c.style == KV_ROPE_INTERLEAVED;
   r.att = (float)(att == 0 ? 1.0 : att);
   r.att2 = (float)((double)r.att * (double)r.att);
-  for (int i = 0; i < d / 2; ++i) {
-    double f = w[i] / (2 * M_PI);
-    f -= std::floor(f);                          // [0, 1]: turns per position modulo one turn
-    const double hi = std::floor(std::ldexp(f, 32)), lo = std::ldexp(f, 64) - std::ldexp(hi, 32);
-    r.turn[i] = ((unsigned long long)hi << 32) + (unsigned long long)lo;
-  }
+  for (int i = 0; i < d / 2; ++i) r.turn[i] = turns_of(w[i]);
   *out = r;
   return KV_OK;
 }

@@ -445,9 +445,11 @@ typedef struct {
 
 /* Set the rotary positions of one layer (any pool kind; none until set).  A
  * host call: it holds for the calls made after it, and a captured graph keeps
- * what was set when it was captured.  Angles are formed as 64-bit fractions of
- * a turn (position times speed, modulo one turn), so they are exact to 2^-32 of
- * a turn at any int32 position. */
+ * what was set when it was captured.  Speeds are doubles (given, or theta and
+ * scaling in double arithmetic).  Angles are formed as 64-bit fractions of a
+ * turn (position times speed, modulo one turn), within 2^-32 of a turn of that
+ * product at any int32 position for speeds up to 2^40; cos and sin are taken in
+ * fp32 of the distance to the nearest quarter turn (2^-28 of a turn at most). */
 kv_status_t kv_pool_set_rope(kv_pool_t* pool, int32_t layer, const kv_rope_config_t* cfg);
 
 /* Rotate q and k rows by `layer`'s rotary positions, for callers that append to
