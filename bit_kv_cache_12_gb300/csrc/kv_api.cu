@@ -304,7 +304,7 @@ kv_status_t kv_append_step(kv_pool_t* pool, int32_t layer, int32_t B, const void
 size_t kv_decode_workspace_bytes(const kv_pool_t* pool, int32_t B, int32_t max_len) {
   if (!pool || B <= 0 || max_len < 0 || max_len > kvint2::kMaxDecodeLen || B > pool->p.cfg.max_seqs) return 0;
   const Pool& p = pool->p;
-  if (p.cfg.kind == KV_POOL_FP8) return kvint2::decode_fp8_workspace(p, B, max_len);
+  if (p.cfg.kind == KV_POOL_FP8) return kvint2::decode_fp8_workspace_up_to(p, B, max_len);
   kvint2::DecodePlan pl = p.cfg.kind == KV_POOL_INT2_3TIER ? kvint2::plan_decode_int2(p, B, max_len)
                                                            : kvint2::plan_decode_bf16(p, B, max_len);
   return pl.bytes;
@@ -532,7 +532,7 @@ size_t kv_prefill_workspace_bytes(const kv_pool_t* pool, int32_t n_seqs, int32_t
   if (!pool || pool->p.cfg.kind != KV_POOL_FP8 || !valid_prefill(pool->p, n_seqs, max_q_per_seq) ||
       max_seq_len < 0 || max_seq_len > kvint2::kMaxDecodeLen)
     return 0;
-  return kvint2::prefill_fp8_workspace(pool->p, n_seqs, max_q_per_seq, max_seq_len);
+  return kvint2::prefill_fp8_workspace_up_to(pool->p, n_seqs, max_q_per_seq, max_seq_len);
 }
 
 kv_status_t kv_prefill_attention_fp8(kv_pool_t* pool, int32_t layer, int32_t n_seqs, const void* q,

@@ -603,6 +603,13 @@ size_t decode_fp8_workspace(const Pool& p, int B, int max_len) {
   return n == 1 ? 16 : (size_t)B * p.cfg.num_q_heads * n * kPart * sizeof(float);
 }
 
+// Fewer sequences are split further: the most that any batch up to B needs.
+size_t decode_fp8_workspace_up_to(const Pool& p, int B, int max_len) {
+  size_t most = 0;
+  for (int b = 1; b <= B; ++b) most = std::max(most, decode_fp8_workspace(p, b, max_len));
+  return most;
+}
+
 cudaError_t launch_decode_fp8(const Pool& p, const Fp8Store& f, int layer, int B, const AttnCall& c, cudaStream_t s) {
   DecodeFp8Args a{fp8_layer(p, f, layer), c, B, p.cfg.num_q_heads, splits(p, B, c.max_len, c.window, c.n_sink),
                   p.tickets + (size_t)layer * p.cfg.max_seqs * p.cfg.num_kv_heads, p.err,

@@ -111,9 +111,12 @@ __device__ __forceinline__ float lse_of(float M, float l) {
   return ((M + (float)e) + log2f(m)) * 0.6931471805599453f;
 }
 
+// What a call needs, and what every call up to these bounds does.
 size_t decode_fp8_workspace(const Pool& p, int B, int max_len);
+size_t decode_fp8_workspace_up_to(const Pool& p, int B, int max_len);
 cudaError_t launch_decode_fp8(const Pool& p, const Fp8Store& f, int layer, int B, const AttnCall& c, cudaStream_t s);
 size_t prefill_fp8_workspace(const Pool& p, int n_seqs, int max_q, int max_len);
+size_t prefill_fp8_workspace_up_to(const Pool& p, int n_seqs, int max_q, int max_len);
 cudaError_t launch_prefill_fp8(const Pool& p, const Fp8Store& f, int layer, int n_seqs, const int32_t* cu_q,
                                int max_q, const AttnCall& c, cudaStream_t s);
 

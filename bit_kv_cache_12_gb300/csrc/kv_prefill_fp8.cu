@@ -1108,6 +1108,18 @@ size_t prefill_fp8_workspace(const Pool& p, int n_seqs, int max_q, int max_len) 
   return n == 1 ? 16 : (size_t)n_seqs * max_q * p.cfg.num_q_heads * n * 132 * sizeof(float);
 }
 
+// Fewer blocks of rows are split further: the most that any call up to these bounds
+// needs.  Only calls of up to half as many blocks as SMs are split; among those of as
+// many blocks of queries the one with the most queries needs the most.
+size_t prefill_fp8_workspace_up_to(const Pool& p, int n_seqs, int max_q, int max_len) {
+  size_t most = 16;
+  const int few = p.sm_count / 2;
+  for (int b = 1; b <= std::min<long long>(few, q_blocks(p, max_q)); ++b)
+    for (int s = 1; s <= std::min(few / b, n_seqs); ++s)
+      most = std::max(most, prefill_fp8_workspace(p, s, std::min(max_q, b * 2 * kRows / p.G), max_len));
+  return most;
+}
+
 cudaError_t launch_prefill_fp8(const Pool& p, const Fp8Store& f, int layer, int n_seqs, const int32_t* cu_q,
                                int max_q, const AttnCall& c, cudaStream_t s) {
   if (max_q == 0) return cudaSuccess;

@@ -270,9 +270,11 @@ kv_status_t kv_append_step(kv_pool_t* pool, int32_t layer, int32_t B, const void
 
 /* Bytes of device workspace kv_decode_attention / kv_decode_attention_bf16
  * / kv_decode_attention_fp8 need for a batch of B sequences whose history (INT2
- * pool) or total length (BF16 and FP8 pools) is at most max_len tokens.  0 on invalid arguments.  Every
- * decode call takes max_hist_len / max_seq_len <= KV_MAX_DECODE_LEN
- * (else KV_ERR_INVALID_ARG). */
+ * pool) or total length (BF16 and FP8 pools) is at most max_len tokens.  0 on
+ * invalid arguments.  Of an FP8 pool the size covers smaller batches too, which
+ * are split further: a workspace for the largest B and max_len serves every
+ * call up to them.  Every decode call takes max_hist_len / max_seq_len <=
+ * KV_MAX_DECODE_LEN (else KV_ERR_INVALID_ARG). */
 #define KV_MAX_DECODE_LEN 6553600
 size_t kv_decode_workspace_bytes(const kv_pool_t* pool, int32_t B, int32_t max_len);
 
@@ -539,7 +541,7 @@ kv_status_t kv_decode_attention_fp8(kv_pool_t* pool, int32_t layer, int32_t B, c
  *            of its rows written
  *   out, lse [T][Hq][128] bf16 and [T][Hq] fp32 (or NULL)
  *   workspace  >= kv_prefill_workspace_bytes(pool, n_seqs, max_q_per_seq,
- *            max_seq_len)
+ *            max_seq_len); one for the largest bounds serves every call up to them
  * Hidden tokens and bad pages as in kv_decode_attention_fp8; calls may overlap if
  * their workspaces and outputs differ. */
 size_t kv_prefill_workspace_bytes(const kv_pool_t* pool, int32_t n_seqs, int32_t max_q_per_seq,
