@@ -140,11 +140,13 @@ __device__ __forceinline__ void load_run(Run& r, const uint16_t* row, int a, int
 
 __device__ __forceinline__ uint64_t f2_of(uint32_t w) { return f2(bf16lo(w), bf16hi(w)); }
 
-// The rotated values, chunk a then chunk b, as fp32 pairs.
-template <bool kPairs>
-__device__ __forceinline__ void rotate_run(const Run& r, const float* tok, int lane, bool rotated, uint64_t (&y)[8]) {
+// The rotated values, chunk a then chunk b, as fp32 pairs.  kScaled: of the row times
+// `scale` (a pair of the same power of two).
+template <bool kPairs, bool kScaled>
+__device__ __forceinline__ void rotate_run(const Run& r, uint64_t scale, const float* tok, int lane, bool rotated,
+                                           uint64_t (&y)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = f2_of(r.w[i]);
+  for (int i = 0; i < 8; ++i) y[i] = kScaled ? f2_mul(f2_of(r.w[i]), scale) : f2_of(r.w[i]);
   if (!rotated) return;
   const float4* t = reinterpret_cast<const float4*>(tok) + (lane & 7);
   const float4 c0 = t[0], c1 = t[8], s0 = t[16], s1 = t[24];
@@ -256,7 +258,7 @@ __device__ __forceinline__ void rows_unit(const RopeParams& rp, const float* tab
     const int t = 4 * u + (lane >> 3);
     if (pos[t] < 0) continue;
     uint64_t y[8];
-    rotate_run<kPairs>(r[u], tab + t * kTokStride, lane, ch.rotated, y);
+    rotate_run<kPairs, false>(r[u], 0, tab + t * kTokStride, lane, ch.rotated, y);
     uint32_t o[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -362,12 +364,13 @@ __device__ __forceinline__ void quant_unit(const RopeParams& rp, const float* ta
     uint32_t c[4] = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
     if (!((bad >> u) & 1)) {
       uint64_t y[8];
-      rotate_run<kPairs>(r[u], tab + t * kTokStride, lane, !kV && ch.rotated, y);
+      // scaled first: at e = 7 even the largest finite row stays in fp32 while it is rotated
+      rotate_run<kPairs, true>(r[u], inv2, tab + t * kTokStride, lane, !kV && ch.rotated, y);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float x0, x1, x2, x3;
-        f2_split(f2_mul(y[2 * i], inv2), x0, x1);
-        f2_split(f2_mul(y[2 * i + 1], inv2), x2, x3);
+        f2_split(y[2 * i], x0, x1);
+        f2_split(y[2 * i + 1], x2, x3);
         c[i] = e4m3x4(x0, x1, x2, x3);
       }
     }
@@ -486,7 +489,10 @@ kv_status_t rope_params(const kv_rope_config_t& c, RopeParams* out) {
   if (d % 32) return KV_ERR_UNSUPPORTED;
   if (c.style != KV_ROPE_HALF && c.style != KV_ROPE_INTERLEAVED) return KV_ERR_INVALID_ARG;
   if (c.scaling < KV_ROPE_SCALE_NONE || c.scaling > KV_ROPE_SCALE_YARN) return KV_ERR_INVALID_ARG;
-  if (!(c.attention_factor >= 0) || !std::isfinite(c.attention_factor)) return KV_ERR_INVALID_ARG;
+  // K's exponent goes by its raw rows' squares in fp32 times the factor's, and a row is
+  // rotated in units of its tile's scale: within these bounds no square that counts has
+  // under- or overflowed, and no finite row passes fp32's range
+  if (!(c.attention_factor == 0 || (c.attention_factor >= 1e-12 && c.attention_factor <= 64))) return KV_ERR_INVALID_ARG;
   double att = c.attention_factor;
   double w[64] = {};
   if (d > 0 && c.inv_freq) {
@@ -517,6 +523,7 @@ kv_status_t rope_params(const kv_rope_config_t& c, RopeParams* out) {
         w[i] = w[i] / c.factor * ramp + w[i] * (1.0 - ramp);
       }
       if (att == 0) att = 0.1 * std::log(c.factor) + 1.0;
+      if (att > 64) return KV_ERR_INVALID_ARG;   // as above: a factor beyond e^630
     }
   }
   r.rd = d;

@@ -440,7 +440,8 @@ typedef struct {
   double theta;                   /* > 1                                          */
   double factor;                  /* >= 1; ignored for NONE                       */
   double beta_fast, beta_slow;    /* YARN: 0 means 32 and 1                       */
-  double attention_factor;        /* on cos and sin; 0 means 1 (YARN: see above)  */
+  double attention_factor;        /* on cos and sin, 1e-12 to 64; 0 means 1
+                                     (YARN: see above)                            */
   const double* inv_freq;         /* host [rotary_dim/2] or NULL: these speeds
                                      replace theta, scaling and factor            */
 } kv_rope_config_t;
@@ -462,7 +463,8 @@ kv_status_t kv_pool_set_rope(kv_pool_t* pool, int32_t layer, const kv_rope_confi
  *              128 channels contiguous; either may be NULL (with its output)
  *   q_out, k_out  the same with their own strides; may be the input itself
  *              (same pointer and stride), else must not overlap it
- * Strides in elements.  Pointers 16-byte aligned, strides multiples of 8 and at
+ * Rotated in fp32, rounded once to bf16 (a value beyond fp32's range is not
+ * finite).  Strides in elements.  Pointers 16-byte aligned, strides multiples of 8 and at
  * least a token's channels, else KV_ERR_INVALID_ARG. */
 kv_status_t kv_rope_apply(const kv_pool_t* pool, int32_t layer, int32_t n_tokens,
                           const int32_t* positions, const void* q, int64_t q_stride,
