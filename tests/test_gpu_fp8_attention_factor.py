@@ -39,3 +39,15 @@ def test_exponents_and_codes(cuda_lib, factor):
     s.append(None, k, v, [0], [960])
     check_codes(s, fc.append(s.model, s.rope, f64(k), f64(v), [0], [960], s.table))
     s.pool.close()
+
+
+@pytest.mark.parametrize("style", ["half", "interleaved"])
+@pytest.mark.parametrize("factor", [1.0, 1.3, 64.0])
+def test_the_largest_finite_rows_saturate(cuda_lib, style, factor):
+    """Rows of +-3.3e38 at every angle: products with the factor would pass fp32's range, the stored values saturate."""
+    s = Setup(hq=1, hkv=1, page=16, seqs=1, longest=200, rope=dict(rotary_dim=128, style=style, attention_factor=factor))
+    k = bf16(3.3e38 * np.sign(s.rng.standard_normal((200, 1, 128))))
+    s.append(None, k, k, [0], [200])
+    check_codes(s, fc.append(s.model, s.rope, f64(k), f64(k), [0], [200], s.table))
+    assert s.pool.error() == 0
+    s.pool.close()
