@@ -559,11 +559,12 @@ int splits(const Pool& p, int B, long long max_len, int window, int n_sink) {
   return (int)(tiles <= 2 * kMaxCluster * kWarps ? std::min<long long>(n, kMaxCluster) : n);
 }
 
-// Clusters of n CTAs that the device holds at once.
+// Clusters of n CTAs that the pool's device (the current one) holds at once.
+constexpr int kDevices = 16;                                 // remembered: the first 16 devices
 template <int G>
-int resident_clusters(int n) {
-  static std::atomic<int> known[kMaxCluster + 1];            // + 1; 0: not asked yet
-  int have = known[n].load(std::memory_order_relaxed);
+int resident_clusters(int device, int n) {
+  static std::atomic<int> known[kDevices][kMaxCluster + 1];  // + 1; 0: not asked yet
+  int have = device < kDevices ? known[device][n].load(std::memory_order_relaxed) : 0;
   if (have == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(n);
@@ -580,18 +581,18 @@ int resident_clusters(int n) {
       count = 0;
     }
     have = count + 1;
-    known[n].store(have, std::memory_order_relaxed);
+    if (device < kDevices) known[device][n].store(have, std::memory_order_relaxed);
   }
   return have - 1;
 }
 
 template <int G>
-cudaError_t launch_t(const DecodeFp8Args& a, cudaStream_t s) {
+cudaError_t launch_t(const DecodeFp8Args& a, int device, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(decode_fp8_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
   const long long pairs = (long long)a.B * a.L.Hkv;
   DecodeFp8Args b = a;
-  b.cluster = a.n_split > 1 && a.n_split <= kMaxCluster && pairs <= resident_clusters<G>(a.n_split);
+  b.cluster = a.n_split > 1 && a.n_split <= kMaxCluster && pairs <= resident_clusters<G>(device, a.n_split);
   return launch_dependent(decode_fp8_kernel<G>, dim3((unsigned)(pairs * a.n_split)), kThreads, kSmem, s,
                           b.cluster ? a.n_split : 1, b);
 }
@@ -615,10 +616,10 @@ cudaError_t launch_decode_fp8(const Pool& p, const Fp8Store& f, int layer, int B
                   p.tickets + (size_t)layer * p.cfg.max_seqs * p.cfg.num_kv_heads, p.err,
                   p.test_wait_polls > 0 ? p.test_wait_polls : kPolls, p.test_stall_first_copy};
   switch (p.G) {
-    case 1: return launch_t<1>(a, s);
-    case 2: return launch_t<2>(a, s);
-    case 4: return launch_t<4>(a, s);
-    default: return launch_t<8>(a, s);
+    case 1: return launch_t<1>(a, p.device, s);
+    case 2: return launch_t<2>(a, p.device, s);
+    case 4: return launch_t<4>(a, p.device, s);
+    default: return launch_t<8>(a, p.device, s);
   }
 }
 

@@ -464,8 +464,8 @@ kv_status_t kv_pool_set_rope(kv_pool_t* pool, int32_t layer, const kv_rope_confi
  *   q_out, k_out  the same with their own strides; may be the input itself
  *              (same pointer and stride), else must not overlap it
  * Rotated in fp32, rounded once to bf16 (a value beyond fp32's range is not
- * finite).  Strides in elements.  Pointers 16-byte aligned, strides multiples of 8 and at
- * least a token's channels, else KV_ERR_INVALID_ARG. */
+ * finite).  Strides in elements.  Pointers 16-byte aligned, strides multiples of
+ * 8 and at least a token's channels, else KV_ERR_INVALID_ARG. */
 kv_status_t kv_rope_apply(const kv_pool_t* pool, int32_t layer, int32_t n_tokens,
                           const int32_t* positions, const void* q, int64_t q_stride,
                           const void* k, int64_t k_stride, void* q_out, int64_t q_out_stride,
