@@ -24,9 +24,10 @@
 // read one another's parts from shared memory (1024 tokens 4.8 us, of which 3.0 are an
 // empty call's; 6.7 through global memory); else the last CTA to finish joins the
 // parts.  Both go in split order: the result does not depend on timing.
-// 100,000 tokens (32 query heads, 8 KV heads): 37.9 us, 5.4 TB/s, 0.81 of a plain
-// copy's rate (4 us to the first tile, 4 for the join); 64 sequences of 8k to 32k
-// tokens: 397 us, 6.97 TB/s, 1.04 of it (a copy also writes).
+// 100,000 tokens (32 query heads, 8 KV heads): 39.1 us, 5.2 TB/s, 0.78 of a plain
+// copy's rate (4 us to the first tile, 4 for the join, 1.4 since large logits are
+// kept in range); 64 sequences of 8k to 32k tokens: 399 us, 6.9 TB/s, 1.03 of it (a
+// copy also writes).
 #include <algorithm>
 #include <atomic>
 
@@ -548,6 +549,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
 // - Where a cluster's worth of splits has up to two tiles per warp: no more than those
 //   (2048 tokens: 5.5 us; in 16 splits, joined through memory, 7.1; beyond, 4096
 //   tokens of 8 pairs: 8.2 so, 7.6 in 19).
+// These are the times that the rule was made by; batches of 16 to 128 sequences of 512
+// to 8,192 tokens, of which a warp may get a tile or two, were not measured.
 int splits(const Pool& p, int B, long long max_len, int window, int n_sink) {
   long long tokens = max_len;
   if (window) tokens = std::min(tokens, (long long)window + n_sink + 2 * kTile);

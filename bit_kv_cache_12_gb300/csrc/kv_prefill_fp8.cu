@@ -15,7 +15,7 @@
 //
 // Bound: the tensor cores (4 * 128 operations per row and key).  One CTA per SM: two
 // tiles of 128 rows take turns, one in the tensor cores while the other is in the
-// softmax.  8192 tokens (32 query heads, 8 KV heads): 408 us, 1.35 PFLOP/s, 0.68 of
+// softmax.  8192 tokens (32 query heads, 8 KV heads): 409 us, 1.35 PFLOP/s, 0.68 of
 // the bf16 rate of a large library product; behind 32,768 cached tokens 1.56 PFLOP/s
 // (0.79).  A key tile takes 3,340 clocks, its products 2,048: a tile's own chain
 // (weights seen by the issuer, O += P V, S, scores seen, softmax) fills 3,310 of them,

@@ -22,8 +22,9 @@
 // atomics, and a tile that already holds tokens has one writer.  A lane holds
 // both members of its pairs (two chunks of eight channels), so nothing crosses
 // lanes but the maximum.  What counted for a prompt of 8192 tokens (32 query heads,
-// 8 KV heads): registers (64, four CTAs per SM: 76 -> 47 us), instructions (pairs in
-// a lane, paired arithmetic: 39), starting before the kernel in front has ended
+// 8 KV heads): registers (180 -> 80, one -> three CTAs per SM: 76 -> 47 us),
+// instructions (pairs in a lane, paired arithmetic), now with 64 registers and four
+// CTAs (39; the append spills 12 to 24 bytes for it), starting before the kernel in front has ended
 // (37.3), rows on their way while the table is formed or the unit before is worked
 // on (35.0 us, 5.3 TB/s: 0.79 of a plain copy; issue slots half in use).  Rotary
 // rows alone, 8192 tokens of 64 + 8 heads: 52 us, 5.8 TB/s, 0.86 of a plain copy

@@ -516,10 +516,10 @@ kv_status_t kv_append_fp8(kv_pool_t* pool, int32_t layer, int32_t n_seqs, const 
  *   lse      device fp32 [B][Hq] or NULL: ln sum_j exp(softmax_scale * q.k_j)
  *   workspace  device, 16-byte aligned, >= kv_decode_workspace_bytes(pool, B,
  *            max_seq_len)
- * What hidden tokens hold never reaches the output, NaN included.  The tokens
- * of a page with a bad id are hidden (KV_DEVERR_PAGE_ID).  Calls for the same
- * layer must not overlap on the GPU (they share the layer's completion
- * counters). */
+ * Logits are fp32: one beyond its range is not a number.  What hidden tokens
+ * hold never reaches the output, NaN included.  The tokens of a page with a bad
+ * id are hidden (KV_DEVERR_PAGE_ID).  Calls for the same layer must not overlap
+ * on the GPU (they share the layer's completion counters). */
 kv_status_t kv_decode_attention_fp8(kv_pool_t* pool, int32_t layer, int32_t B, const void* q,
                                     const int32_t* seq_len, const int32_t* page_table,
                                     int32_t max_pages_per_seq, int32_t max_seq_len,
