@@ -366,6 +366,8 @@ kv_status_t kv_decode_attention_noalloc(kv_pool_t* pool, int32_t layer, int32_t 
 
 kv_status_t kv_debug_stall_first_copy(kv_pool_t* pool, int32_t enable, int32_t max_polls) {
   if (!pool || max_polls < 0) return KV_ERR_INVALID_ARG;
+  // those decodes wait for their copies in flight with the same limit: it has to outlast them
+  if (pool->p.cfg.kind != KV_POOL_FP8 && max_polls > 0 && max_polls < 1024) return KV_ERR_INVALID_ARG;
   pool->p.test_stall_first_copy = enable ? 1 : 0;
   pool->p.test_wait_polls = max_polls;
   return KV_OK;

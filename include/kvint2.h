@@ -372,8 +372,11 @@ kv_status_t kv_decode_attention_noalloc(kv_pool_t* pool, int32_t layer, int32_t 
  * kv_decode_attention_fp8's first CTA waits for a copy that is never started,
  * and kv_prefill_attention_fp8's first CTA for keys that are never handed over;
  * both end the same way (the decode skips that warp's share of the tokens, the
- * prompt rows that CTA had taken on and not finished become NaN).  max_polls > 0 replaces the default poll limit of those waits (about a
- * second) for the pool's decode, prompt and bulk append calls; 0 restores it.
+ * prompt rows that CTA had taken on and not finished become NaN).  max_polls > 0
+ * replaces the default poll limit of those waits (one to four seconds; a poll
+ * takes up to 3.7 us) for the pool's decode, prompt and bulk append calls; 0
+ * restores it.  INT2 and BF16 pools, whose decodes wait for copies in flight with
+ * the same limit, take none below 1024 (KV_ERR_INVALID_ARG).
  * enable = 0 restores normal calls.  Not for production use. */
 kv_status_t kv_debug_stall_first_copy(kv_pool_t* pool, int32_t enable, int32_t max_polls);
 

@@ -102,3 +102,19 @@ def test_all_logits_large_and_negative(cuda_lib, power):
     out, lse = s.prefill(q, [60], [300], 0, 0, SCALE)
     check(s, q, [(0, 240 + i) for i in range(60)], out, lse, 0, SCALE)
     s.pool.close()
+
+
+@pytest.mark.parametrize("n,hkv", [(3000, 1), (9000, 2)])
+def test_split_over_the_cache(cuda_lib, n, hkv):
+    """The parts of a split join by references and log-sum-exps that are as large."""
+    s = Setup(4 * hkv, hkv, 16, 1, n, seed=n)
+    s.length = n
+    s.fill(spread=2)
+    q = bf16(s.rng.standard_normal((6, 4 * hkv, 128)) * powers(s.rng, (6, 4 * hkv, 1)))
+    for i in range(6):
+        one = q[i:i + 1].contiguous()
+        out, lse = s.decode(one, [n])
+        check(s, one, [(0, n - 1)], out, lse, 0, SCALE)
+    out, lse = s.prefill(q, [6], [n])
+    check(s, q, [(0, n - 6 + i) for i in range(6)], out, lse, 0, SCALE)
+    s.pool.close()

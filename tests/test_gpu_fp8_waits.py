@@ -118,3 +118,17 @@ def test_prefill_bound_on_queries_far_above_their_number(cuda_lib):
         np.testing.assert_array_equal(out, want[0])
         np.testing.assert_array_equal(lse, want[1])
     s.pool.close()
+
+
+def test_limits_too_short_to_outlast_copies_are_refused(cuda_lib):
+    """The INT2 and BF16 decodes wait for copies in flight with the hook's limit."""
+    for kind in (native.KV_POOL_INT2_3TIER, native.KV_POOL_BF16):
+        pool = native.KVPool(kind, 1, 4, 2, 16, 4, 1)
+        for polls in (1, 100, 1023):
+            for enable in (0, 1):
+                with pytest.raises(native.KVError) as e:
+                    native.kv_debug_stall_first_copy(pool.handle, enable, polls)
+                assert e.value.status == native.KV_ERR_INVALID_ARG
+        native.kv_debug_stall_first_copy(pool.handle, 1, 1024)
+        native.kv_debug_stall_first_copy(pool.handle, 0, 0)
+        pool.close()
