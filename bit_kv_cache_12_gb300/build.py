@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIBDIR, "libkvint2.so")
 SOURCES = ["kv_api.cu", "kv_append.cu", "kv_append_tc.cu", "kv_decode.cu", "kv_rope_append.cu",
-           "kv_decode_fp8.cu", "kv_prefill_fp8.cu"]
+           "kv_decode_fp8.cu", "kv_prefill_fp8.cu", "kv_fp4_cache.cu", "kv_decode_fp4.cu", "kv_prompt.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -5,7 +5,7 @@
 #include <cmath>
 #include <new>
 
-#include "kv_fp8.h"
+#include "kv_fp4.h"
 #include "kv_internal.h"
 
 using kvint2::Pool;
@@ -13,7 +13,10 @@ using kvint2::Pool;
 struct kv_pool {
   Pool p;
   kvint2::Fp8Store fp8;
-  kvint2::RopeParams* rope = nullptr;   // host, one per layer
+  kvint2::Fp4Store fp4;
+  kvint2::RopeParams* rope = nullptr;   // host, one per layer, as the two below
+  kvint2::RopeAxes* axes = nullptr;
+  kvint2::Fp4Range* range = nullptr;
 };
 
 namespace {
@@ -41,10 +44,12 @@ void free_pool(kv_pool* pool) {
   Pool& p = pool->p;
   void* ptrs[] = {p.hist, p.sink_k, p.sink_v, p.rec_k,   p.rec_v,        p.bk,  p.bv,  p.Rk,
                   p.RvT,  p.clip,   p.rfrag,  p.tickets, p.step_tickets, p.arrive, p.err,
-                  pool->fp8.codes, pool->fp8.exps};
+                  pool->fp8.codes, pool->fp8.exps, pool->fp4.tiles};
   for (void* q : ptrs)
     if (q) cudaFree(q);
   delete[] pool->rope;
+  delete[] pool->axes;
+  delete[] pool->range;
   delete pool;
 }
 
@@ -83,6 +88,51 @@ bool valid_prefill(const Pool& p, int32_t n_seqs, int32_t max_q) {
   return ((int64_t)max_q * p.G + 255) / 256 * n_seqs * p.cfg.num_kv_heads <= INT32_MAX;
 }
 
+// the arguments the two rotary calls share
+kv_status_t check_rope(const kv_pool_t* pool, int layer, int n_tokens, const int32_t* positions,
+                       const kvint2::RopeRows& q, const kvint2::RopeRows& k) {
+  if (!valid_layer(pool, layer) || n_tokens < 0) return KV_ERR_INVALID_ARG;
+  const Pool& p = pool->p;
+  if ((q.in == nullptr) != (q.out == nullptr) || (k.in == nullptr) != (k.out == nullptr)) return KV_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (!positions || (!q.in && !k.in))) return KV_ERR_INVALID_ARG;
+  const int Hq = p.cfg.num_q_heads, Hkv = p.cfg.num_kv_heads;
+  if (q.in && (!valid_rows(q.in, q.in_stride, Hq) || !valid_rows(q.out, q.out_stride, Hq))) return KV_ERR_INVALID_ARG;
+  if (k.in && (!valid_rows(k.in, k.in_stride, Hkv) || !valid_rows(k.out, k.out_stride, Hkv))) return KV_ERR_INVALID_ARG;
+  if ((q.in && q.in == q.out && q.in_stride != q.out_stride) || (k.in && k.in == k.out && k.in_stride != k.out_stride))
+    return KV_ERR_INVALID_ARG;
+  return on_pool_device(p);
+}
+
+// the arguments the 8-bit and the 4-bit decode share
+kv_status_t check_decode(const kv_pool_t* pool, int kind, int layer, int B, const void* q, const int32_t* seq_len,
+                         const int32_t* pt, int max_pages, int max_len, float scale, int window, int n_sink,
+                         const void* out, const float* lse, const void* ws) {
+  if (!valid_layer(pool, layer) || B <= 0 || max_pages <= 0 || max_len < 0) return KV_ERR_INVALID_ARG;
+  const Pool& p = pool->p;
+  if (p.cfg.kind != kind || B > p.cfg.max_seqs) return KV_ERR_INVALID_ARG;
+  if (!q || !seq_len || !pt || !out || !ws) return KV_ERR_INVALID_ARG;
+  if (window < 0 || n_sink < 0 || !std::isfinite(scale)) return KV_ERR_INVALID_ARG;
+  if ((int64_t)max_len > (int64_t)max_pages * p.cfg.page_size || max_len > kvint2::kMaxDecodeLen)
+    return KV_ERR_INVALID_ARG;
+  if (!aligned16(ws) || !aligned16(q) || !aligned16(out) || ((uintptr_t)lse & 3)) return KV_ERR_INVALID_ARG;
+  return KV_OK;
+}
+
+// the ragged tokens of a 4-bit append or read
+kv_status_t check_fp4_tokens(const kv_pool_t* pool, int layer, int n_seqs, const int32_t* cu, const int32_t* start,
+                             const int32_t* pt, int max_pages, int max_tokens) {
+  if (!valid_layer(pool, layer) || n_seqs < 0 || max_pages <= 0 || max_tokens < 0) return KV_ERR_INVALID_ARG;
+  if (pool->p.cfg.kind != KV_POOL_FP4) return KV_ERR_INVALID_ARG;
+  if (n_seqs > 0 && (!cu || !start || !pt)) return KV_ERR_INVALID_ARG;
+  if ((int64_t)n_seqs * (((int64_t)max_tokens + 30) / kvint2::kTile) > INT32_MAX) return KV_ERR_INVALID_ARG;
+  return KV_OK;
+}
+
+// queries and keys of a prompt call; its grid: a CTA per 256 rows and KV head
+bool valid_prompt(const Pool& p, int32_t n_seqs, int32_t max_q, int32_t max_k) {
+  return valid_prefill(p, n_seqs, max_q) && max_k >= 0 && max_k <= kvint2::kMaxDecodeLen;
+}
+
 }  // namespace
 
 extern "C" {
@@ -91,7 +141,8 @@ kv_status_t kv_pool_create(const kv_pool_config_t* cfg, void* stream, kv_pool_t*
   if (!cfg || !out) return KV_ERR_INVALID_ARG;
   *out = nullptr;
   const kv_pool_config_t c = *cfg;
-  if (c.kind != KV_POOL_INT2_3TIER && c.kind != KV_POOL_BF16 && c.kind != KV_POOL_FP8) return KV_ERR_INVALID_ARG;
+  if (c.kind != KV_POOL_INT2_3TIER && c.kind != KV_POOL_BF16 && c.kind != KV_POOL_FP8 && c.kind != KV_POOL_FP4)
+    return KV_ERR_INVALID_ARG;
   if (c.num_layers <= 0 || c.num_kv_heads <= 0 || c.num_q_heads <= 0 || c.max_seqs <= 0 ||
       c.num_pages <= 0 || c.num_pages > (int64_t)INT32_MAX)
     return KV_ERR_INVALID_ARG;
@@ -118,7 +169,9 @@ kv_status_t kv_pool_create(const kv_pool_config_t* cfg, void* stream, kv_pool_t*
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const size_t L = c.num_layers, H = c.num_kv_heads;
   pool->rope = new (std::nothrow) kvint2::RopeParams[L]();
-  bool ok = pool->rope != nullptr;
+  pool->axes = new (std::nothrow) kvint2::RopeAxes[L]();
+  pool->range = new (std::nothrow) kvint2::Fp4Range[L]();
+  bool ok = pool->rope && pool->axes && pool->range;
   if (c.kind == KV_POOL_INT2_3TIER) {
     p.tile_bytes = 1024 + kvint2::kTile * 8 * (128 / c.group_size);
     p.page_bytes = H * (c.page_size / kvint2::kTile) * p.tile_bytes;
@@ -140,6 +193,9 @@ kv_status_t kv_pool_create(const kv_pool_config_t* cfg, void* stream, kv_pool_t*
     pool->fp8.exp_layer_stride = tiles * 2;
     ok = ok && dev_alloc(&pool->fp8.codes, L * pool->fp8.layer_stride);
     ok = ok && dev_alloc(&pool->fp8.exps, L * pool->fp8.exp_layer_stride);
+  } else if (c.kind == KV_POOL_FP4) {
+    pool->fp4.layer_stride = (size_t)c.num_pages * H * (c.page_size / kvint2::kTile) * kvint2::kFp4TileBytes;
+    ok = ok && dev_alloc(&pool->fp4.tiles, L * pool->fp4.layer_stride);
   } else {
     p.bf16_layer_stride = (size_t)c.num_pages * H * c.page_size * 128;
     ok = ok && dev_alloc(&p.bk, L * p.bf16_layer_stride * 2);
@@ -166,6 +222,7 @@ kv_status_t kv_pool_create(const kv_pool_config_t* cfg, void* stream, kv_pool_t*
   zero(p.bv, L * p.bf16_layer_stride * 2);
   zero(pool->fp8.codes, L * pool->fp8.layer_stride);
   zero(pool->fp8.exps, L * pool->fp8.exp_layer_stride);
+  zero(pool->fp4.tiles, L * pool->fp4.layer_stride);
   zero(p.tickets, L * c.max_seqs * H * sizeof(unsigned));
   zero(p.arrive, L * c.max_seqs * H * kvint2::kMaskWords * sizeof(unsigned));
   zero(p.step_tickets, L * ((c.max_seqs + 127) / 128) * sizeof(unsigned));
@@ -305,6 +362,7 @@ size_t kv_decode_workspace_bytes(const kv_pool_t* pool, int32_t B, int32_t max_l
   if (!pool || B <= 0 || max_len < 0 || max_len > kvint2::kMaxDecodeLen || B > pool->p.cfg.max_seqs) return 0;
   const Pool& p = pool->p;
   if (p.cfg.kind == KV_POOL_FP8) return kvint2::decode_fp8_workspace_up_to(p, B, max_len);
+  if (p.cfg.kind == KV_POOL_FP4) return kvint2::decode_fp4_workspace_up_to(p, B, max_len);
   kvint2::DecodePlan pl = p.cfg.kind == KV_POOL_INT2_3TIER ? kvint2::plan_decode_int2(p, B, max_len)
                                                            : kvint2::plan_decode_bf16(p, B, max_len);
   return pl.bytes;
@@ -367,7 +425,8 @@ kv_status_t kv_decode_attention_noalloc(kv_pool_t* pool, int32_t layer, int32_t 
 kv_status_t kv_debug_stall_first_copy(kv_pool_t* pool, int32_t enable, int32_t max_polls) {
   if (!pool || max_polls < 0) return KV_ERR_INVALID_ARG;
   // those decodes wait for their copies in flight with the same limit: it has to outlast them
-  if (pool->p.cfg.kind != KV_POOL_FP8 && max_polls > 0 && max_polls < 1024) return KV_ERR_INVALID_ARG;
+  const int kind = pool->p.cfg.kind;
+  if (kind != KV_POOL_FP8 && kind != KV_POOL_FP4 && max_polls > 0 && max_polls < 1024) return KV_ERR_INVALID_ARG;
   pool->p.test_stall_first_copy = enable ? 1 : 0;
   pool->p.test_wait_polls = max_polls;
   return KV_OK;
@@ -464,26 +523,45 @@ kv_status_t kv_pool_set_rope(kv_pool_t* pool, int32_t layer, const kv_rope_confi
   if (!valid_layer(pool, layer) || !cfg) return KV_ERR_INVALID_ARG;
   kvint2::RopeParams r;
   const kv_status_t st = kvint2::rope_params(*cfg, &r);
-  if (st == KV_OK) pool->rope[layer] = r;
+  if (st == KV_OK) {
+    pool->rope[layer] = r;
+    pool->axes[layer] = kvint2::RopeAxes{};
+  }
   return st;
+}
+
+kv_status_t kv_pool_set_rope_axes(kv_pool_t* pool, int32_t layer, int32_t n_axes, const int32_t* axis,
+                                  int32_t n_pairs) {
+  if (!valid_layer(pool, layer) || !axis || n_axes < 1 || n_axes > 4) return KV_ERR_INVALID_ARG;
+  const int pairs = pool->rope[layer].rd / 2;
+  if (pairs == 0 || n_pairs != pairs) return KV_ERR_INVALID_ARG;
+  kvint2::RopeAxes x{};
+  x.n = n_axes;
+  for (int i = 0; i < pairs; ++i) {
+    if (axis[i] < 0 || axis[i] >= n_axes) return KV_ERR_INVALID_ARG;
+    x.axis[i] = (uint8_t)axis[i];
+  }
+  pool->axes[layer] = x;
+  return KV_OK;
 }
 
 kv_status_t kv_rope_apply(const kv_pool_t* pool, int32_t layer, int32_t n_tokens, const int32_t* positions,
                           const void* q, int64_t q_stride, const void* k, int64_t k_stride, void* q_out,
                           int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream) {
-  if (!valid_layer(pool, layer) || n_tokens < 0) return KV_ERR_INVALID_ARG;
-  const Pool& p = pool->p;
-  if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr)) return KV_ERR_INVALID_ARG;
-  if (n_tokens > 0 && (!positions || (!q && !k))) return KV_ERR_INVALID_ARG;
-  const int Hq = p.cfg.num_q_heads, Hkv = p.cfg.num_kv_heads;
-  if (q && (!valid_rows(q, q_stride, Hq) || !valid_rows(q_out, q_out_stride, Hq))) return KV_ERR_INVALID_ARG;
-  if (k && (!valid_rows(k, k_stride, Hkv) || !valid_rows(k_out, k_out_stride, Hkv))) return KV_ERR_INVALID_ARG;
-  if ((q && q == q_out && q_stride != q_out_stride) || (k && k == k_out && k_stride != k_out_stride))
-    return KV_ERR_INVALID_ARG;
-  if (kv_status_t st = on_pool_device(p); st != KV_OK) return st;
-  return cuda_status(kvint2::launch_rope(p, pool->rope[layer], n_tokens, positions,
-                                         {q, q_stride, q_out, q_out_stride}, {k, k_stride, k_out, k_out_stride},
+  const kvint2::RopeRows rq{q, q_stride, q_out, q_out_stride}, rk{k, k_stride, k_out, k_out_stride};
+  if (kv_status_t st = check_rope(pool, layer, n_tokens, positions, rq, rk); st != KV_OK) return st;
+  return cuda_status(kvint2::launch_rope(pool->p, pool->rope[layer], n_tokens, positions, rq, rk,
                                          static_cast<cudaStream_t>(stream)));
+}
+
+kv_status_t kv_rope_apply_axes(const kv_pool_t* pool, int32_t layer, int32_t n_tokens, const int32_t* positions,
+                               int64_t pos_stride, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                               void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream) {
+  const kvint2::RopeRows rq{q, q_stride, q_out, q_out_stride}, rk{k, k_stride, k_out, k_out_stride};
+  if (kv_status_t st = check_rope(pool, layer, n_tokens, positions, rq, rk); st != KV_OK) return st;
+  if (pos_stride < n_tokens) return KV_ERR_INVALID_ARG;
+  return cuda_status(kvint2::launch_rope_axes(pool->p, pool->rope[layer], pool->axes[layer], n_tokens, positions,
+                                              pos_stride, rq, rk, static_cast<cudaStream_t>(stream)));
 }
 
 kv_status_t kv_append_fp8(kv_pool_t* pool, int32_t layer, int32_t n_seqs, const void* q, int64_t q_stride,
@@ -512,14 +590,11 @@ kv_status_t kv_decode_attention_fp8(kv_pool_t* pool, int32_t layer, int32_t B, c
                                     const int32_t* seq_len, const int32_t* page_table, int32_t max_pages_per_seq,
                                     int32_t max_seq_len, float softmax_scale, int32_t window, int32_t n_sink,
                                     void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
-  if (!valid_layer(pool, layer) || B <= 0 || max_pages_per_seq <= 0 || max_seq_len < 0) return KV_ERR_INVALID_ARG;
+  if (kv_status_t st = check_decode(pool, KV_POOL_FP8, layer, B, q, seq_len, page_table, max_pages_per_seq, max_seq_len,
+                                    softmax_scale, window, n_sink, out, lse, workspace);
+      st != KV_OK)
+    return st;
   const Pool& p = pool->p;
-  if (p.cfg.kind != KV_POOL_FP8 || B > p.cfg.max_seqs) return KV_ERR_INVALID_ARG;
-  if (!q || !seq_len || !page_table || !out || !workspace) return KV_ERR_INVALID_ARG;
-  if (window < 0 || n_sink < 0 || !std::isfinite(softmax_scale)) return KV_ERR_INVALID_ARG;
-  if ((int64_t)max_seq_len > (int64_t)max_pages_per_seq * p.cfg.page_size || max_seq_len > kvint2::kMaxDecodeLen)
-    return KV_ERR_INVALID_ARG;
-  if (!aligned16(workspace) || !aligned16(q) || !aligned16(out) || ((uintptr_t)lse & 3)) return KV_ERR_INVALID_ARG;
   if (workspace_bytes < kvint2::decode_fp8_workspace(p, B, max_seq_len)) return KV_ERR_INVALID_ARG;
   if (kv_status_t st = on_pool_device(p); st != KV_OK) return st;
   return cuda_status(kvint2::launch_decode_fp8(p, pool->fp8, layer, B,
@@ -558,6 +633,112 @@ kv_status_t kv_prefill_attention_fp8(kv_pool_t* pool, int32_t layer, int32_t n_s
                                                  kvint2::effective_window(window, max_seq_len), n_sink, out, lse,
                                                  workspace},
                                                 static_cast<cudaStream_t>(stream)));
+}
+
+kv_status_t kv_pool_get_fp4_layout(const kv_pool_t* pool, int32_t layer, kv_fp4_layout_t* out) {
+  if (!valid_layer(pool, layer) || !out || pool->p.cfg.kind != KV_POOL_FP4) return KV_ERR_INVALID_ARG;
+  const Pool& p = pool->p;
+  out->tiles = pool->fp4.tiles + (size_t)layer * pool->fp4.layer_stride;
+  out->tile_bytes = kvint2::kFp4TileBytes;
+  out->layer_stride = pool->fp4.layer_stride;
+  out->head_stride = (size_t)(p.cfg.page_size / kvint2::kTile) * kvint2::kFp4TileBytes;
+  out->page_stride = out->head_stride * p.cfg.num_kv_heads;
+  return KV_OK;
+}
+
+kv_status_t kv_pool_set_fp4_range(kv_pool_t* pool, int32_t layer, int32_t k_exp, int32_t v_exp) {
+  if (!valid_layer(pool, layer) || pool->p.cfg.kind != KV_POOL_FP4) return KV_ERR_INVALID_ARG;
+  constexpr int most = kvint2::kFp4ExpMax;
+  if (k_exp < -most || k_exp > most || v_exp < -most || v_exp > most) return KV_ERR_INVALID_ARG;
+  pool->range[layer] = {k_exp, v_exp};
+  return KV_OK;
+}
+
+kv_status_t kv_append_fp4(kv_pool_t* pool, int32_t layer, int32_t n_seqs, const void* k, int64_t k_stride,
+                          const void* v, int64_t v_stride, const int32_t* cu_tokens, const int32_t* start_pos,
+                          const int32_t* page_table, int32_t max_pages_per_seq, int32_t max_tokens_per_seq,
+                          void* stream) {
+  if (kv_status_t st = check_fp4_tokens(pool, layer, n_seqs, cu_tokens, start_pos, page_table, max_pages_per_seq,
+                                        max_tokens_per_seq);
+      st != KV_OK)
+    return st;
+  const Pool& p = pool->p;
+  const int Hkv = p.cfg.num_kv_heads;
+  if (n_seqs > 0 && (!k || !v || !valid_rows(k, k_stride, Hkv) || !valid_rows(v, v_stride, Hkv)))
+    return KV_ERR_INVALID_ARG;
+  if (kv_status_t st = on_pool_device(p); st != KV_OK) return st;
+  return cuda_status(kvint2::launch_append_fp4(
+      p, kvint2::fp4_layer(p, pool->fp4, pool->range[layer], layer),
+      {n_seqs, cu_tokens, start_pos, page_table, max_pages_per_seq, max_tokens_per_seq},
+      {const_cast<void*>(k), const_cast<void*>(v), k_stride, v_stride}, static_cast<cudaStream_t>(stream)));
+}
+
+kv_status_t kv_read_fp4(const kv_pool_t* pool, int32_t layer, int32_t n_seqs, const int32_t* cu_tokens,
+                        const int32_t* start_pos, const int32_t* page_table, int32_t max_pages_per_seq,
+                        int32_t max_tokens_per_seq, void* k_out, int64_t k_out_stride, void* v_out,
+                        int64_t v_out_stride, void* stream) {
+  if (kv_status_t st = check_fp4_tokens(pool, layer, n_seqs, cu_tokens, start_pos, page_table, max_pages_per_seq,
+                                        max_tokens_per_seq);
+      st != KV_OK)
+    return st;
+  const Pool& p = pool->p;
+  const int Hkv = p.cfg.num_kv_heads;
+  if (n_seqs > 0 && !k_out && !v_out) return KV_ERR_INVALID_ARG;
+  if ((k_out && !valid_rows(k_out, k_out_stride, Hkv)) || (v_out && !valid_rows(v_out, v_out_stride, Hkv)))
+    return KV_ERR_INVALID_ARG;
+  if (kv_status_t st = on_pool_device(p); st != KV_OK) return st;
+  return cuda_status(kvint2::launch_read_fp4(p, kvint2::fp4_layer(p, pool->fp4, pool->range[layer], layer),
+                                             {n_seqs, cu_tokens, start_pos, page_table, max_pages_per_seq,
+                                              max_tokens_per_seq},
+                                             {k_out, v_out, k_out_stride, v_out_stride},
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+kv_status_t kv_decode_attention_fp4(kv_pool_t* pool, int32_t layer, int32_t B, const void* q,
+                                    const int32_t* seq_len, const int32_t* page_table, int32_t max_pages_per_seq,
+                                    int32_t max_seq_len, float softmax_scale, int32_t window, int32_t n_sink,
+                                    void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (kv_status_t st = check_decode(pool, KV_POOL_FP4, layer, B, q, seq_len, page_table, max_pages_per_seq, max_seq_len,
+                                    softmax_scale, window, n_sink, out, lse, workspace);
+      st != KV_OK)
+    return st;
+  const Pool& p = pool->p;
+  if (workspace_bytes < kvint2::decode_fp4_workspace(p, B, max_seq_len)) return KV_ERR_INVALID_ARG;
+  if (kv_status_t st = on_pool_device(p); st != KV_OK) return st;
+  return cuda_status(kvint2::launch_decode_fp4(p, kvint2::fp4_layer(p, pool->fp4, pool->range[layer], layer), layer, B,
+                                               {q, seq_len, page_table, max_pages_per_seq, max_seq_len, softmax_scale,
+                                                kvint2::effective_window(window, max_seq_len), n_sink, out, lse,
+                                                workspace},
+                                               static_cast<cudaStream_t>(stream)));
+}
+
+size_t kv_prompt_workspace_bytes(const kv_pool_t* pool, int32_t n_seqs, int32_t max_q_per_seq, int32_t max_k_per_seq) {
+  if (!pool || !valid_prompt(pool->p, n_seqs, max_q_per_seq, max_k_per_seq)) return 0;
+  return kvint2::prompt_workspace_up_to(pool->p, n_seqs, max_q_per_seq, max_k_per_seq);
+}
+
+kv_status_t kv_prompt_attention(kv_pool_t* pool, int32_t n_seqs, const void* q, int64_t q_stride, int64_t q_rows,
+                                const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t kv_rows,
+                                const int32_t* cu_q, const int32_t* cu_k, int32_t max_q_per_seq,
+                                int32_t max_k_per_seq, float softmax_scale, int32_t window, int32_t n_sink, void* out,
+                                float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!pool || !valid_prompt(pool->p, n_seqs, max_q_per_seq, max_k_per_seq)) return KV_ERR_INVALID_ARG;
+  const Pool& p = pool->p;
+  if (!q || !k || !v || !cu_q || !cu_k || !out || !workspace) return KV_ERR_INVALID_ARG;
+  if (q_rows < 0 || q_rows > INT32_MAX || kv_rows < 1 || kv_rows > INT32_MAX) return KV_ERR_INVALID_ARG;
+  const int Hkv = p.cfg.num_kv_heads;
+  if (!valid_rows(q, q_stride, p.cfg.num_q_heads) || !valid_rows(k, k_stride, Hkv) || !valid_rows(v, v_stride, Hkv))
+    return KV_ERR_INVALID_ARG;
+  if (q_stride > INT32_MAX || k_stride > INT32_MAX || v_stride > INT32_MAX) return KV_ERR_INVALID_ARG;
+  if (window < 0 || n_sink < 0 || !std::isfinite(softmax_scale)) return KV_ERR_INVALID_ARG;
+  if (!aligned16(workspace) || !aligned16(out) || ((uintptr_t)lse & 3)) return KV_ERR_INVALID_ARG;
+  if (workspace_bytes < kvint2::prompt_workspace(p, n_seqs, max_q_per_seq, max_k_per_seq)) return KV_ERR_INVALID_ARG;
+  if (kv_status_t st = on_pool_device(p); st != KV_OK) return st;
+  return cuda_status(kvint2::launch_prompt(p,
+                                           {q, k, v, q_stride, k_stride, v_stride, q_rows, kv_rows, cu_q, cu_k, n_seqs,
+                                            max_q_per_seq, max_k_per_seq, softmax_scale,
+                                            kvint2::effective_window(window, max_k_per_seq), n_sink, out, lse, workspace},
+                                           static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,351 @@
+// Single-token attention over the 4-bit cache, split over the cache.
+//
+// With code values k, v (e2m1), block scales sK, sV (e4m3), the layer's exponents and
+// base-2 logits
+//   x_j = scale log2(e) 2^eK sum_c q_c k_jc sK_j(c / 16),   w_j = 2^(x_j - M),
+// a head's output is  2^eV sum_j w_j sV_j v_j / sum_j w_j.
+//
+// Both products are m16n8k16 tensor-core steps with the cached tile as the A operand and
+// the (up to 8) query heads of the KV head as the 8 columns.  A code pair becomes an fp16
+// register by one conversion.  K's scales multiply the operand (code * scale has 6 bits:
+// exact); which channels a step takes is free as long as q's rows agree, and with 32
+// neighbouring ones to a lane it needs two scales per token.  V's scales ride on the
+// weights, the B operand: 16 rows of A are 16 channels of one block.  q enters as fp16
+// scaled per head by a power of two (largest element in [2^14, 2^15)): exact for bf16's 8
+// bits down to 2^-32 of it.  The weights are rounded to fp16, and again times sV; M lags
+// so that the largest is between 2^3 and 2^7 (2^7 * 448 is in fp16's range), and weights
+// below 2^-28 of the largest are dropped.
+#include <algorithm>
+
+#include "kv_decode_split.cuh"
+#include "kv_fp4.h"
+
+namespace kvint2 {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 4;                     // 2304-byte tiles in flight per warp
+constexpr int kPolls = 1 << 18;                // bound of a copy's wait: a poll suspends for up to 3.7 us, so about a second
+constexpr float kRaise = 7.f, kHead = 3.f;     // M moves when x > M + 7, to the largest x - 3
+constexpr uint32_t kRing = kWarps * kStages * kFp4TileBytes;
+constexpr uint32_t kSmem = kRing + kWarps * kStages * 8;
+// Results of the warps in shared memory (over the ring): heads 136 floats apart, so that a
+// half warp's pairs of channels fall into different banks.
+constexpr int kHeadStride = 136;
+static_assert(kWarps * 8 * (kHeadStride + 2) * 4 + 8 * kPart * 4 <= (int)kRing, "the results fit over the ring");
+static_assert(kMaxSplits * 8 * 4 + 64 + kThreads * 16 <= (int)kRing, "and the join's weights and sums");
+
+struct DecodeFp4Args {
+  Fp4Layer L;
+  AttnCall c;
+  int B, Hq, n_split;
+  unsigned* tickets;
+  int* err;
+  int polls;
+  int stall;                                   // test hook: warp 0 of CTA 0 never starts its first copy
+  int cluster;                                 // the splits of a pair are a cluster
+};
+
+// The four code pairs of a word as fp16 pairs.
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm("{ .reg .b8 p, q, r, s; mov.b32 {p, q, r, s}, %4; cvt.rn.f16x2.e2m1x2 %0, p; cvt.rn.f16x2.e2m1x2 %1, q; "
+      "cvt.rn.f16x2.e2m1x2 %2, r; cvt.rn.f16x2.e2m1x2 %3, s; }"
+      : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) { return h2_as_u32(__hmul2(u32_as_h2(a), u32_as_h2(b))); }
+
+template <int G>
+__global__ void __launch_bounds__(kThreads, 2) decode_fp4_kernel(DecodeFp4Args a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
+  uint8_t* ring = smem + warp * kStages * kFp4TileBytes;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + kRing) + warp * kStages;
+  if (lane < kStages) mbar_init(bar + lane, 1);
+  mbar_fence_init();
+  __syncwarp();
+  release_successor();
+  after_predecessor();
+
+  const int split = blockIdx.x % a.n_split, pair = blockIdx.x / a.n_split;
+  const int h = pair % a.L.Hkv, b = pair / a.L.Hkv;
+  int n = a.c.seq_len[b];
+  // lane (r, j) holds head r, channels 32 j ..; on its way with the length
+  uint32_t qf[16];
+  {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.c.q) +
+                                                    ((size_t)b * a.Hq + h * G + (r < G ? r : 0)) * 128 + 32 * j);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 x = q[i];
+      qf[4 * i] = x.x, qf[4 * i + 1] = x.y, qf[4 * i + 2] = x.z, qf[4 * i + 3] = x.w;
+    }
+  }
+  if (n < 0 || n > a.c.max_len) {
+    if (split == 0 && threadIdx.x == 0) flag_error(a.err, KV_DEVERR_LENGTH);
+    n = min(max(n, 0), a.c.max_len);
+  }
+  const Span sp(n, a.c.window, a.c.n_sink);
+  const int per = (sp.total + a.n_split - 1) / a.n_split;
+  const int i0 = split * per, count = max(min(per, sp.total - i0), 0);
+  const int mine = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;   // tiles i0 + warp, + kWarps, ..
+  const int tpp = a.L.P / kTile, tpp_shift = tpp >> 1;
+  const int32_t* pt = a.c.pt + (size_t)b * a.c.max_pages;
+
+  // The warp's k-th tile: its page id is read a batch of 32 tiles ahead and not looked at
+  // before its turn (no load below waits for another where it is issued).
+  auto page_of = [&](int k) -> int {
+    return pt[k < mine ? sp.tile(i0 + warp + k * kWarps) >> tpp_shift : 0];
+  };
+  auto stored = [&](int k, int pid) -> long long {   // -1: no such tile, or behind a bad page id
+    if (k >= mine) return -1;
+    if (pid < 0 || pid >= a.L.num_pages) {
+      flag_error(a.err, KV_DEVERR_PAGE_ID);
+      return -1;
+    }
+    return ((long long)pid * a.L.Hkv + h) * tpp + (sp.tile(i0 + warp + k * kWarps) & (tpp - 1));
+  };
+  const uint64_t policy = l2_evict_first_policy();
+  auto issue = [&](int stage, long long t) {     // lane 0
+    if (t < 0) {
+      mbar_expect_tx(bar + stage, 0);
+    } else {
+      mbar_expect_tx(bar + stage, kFp4TileBytes);
+      bulk_g2s_hint(ring + stage * kFp4TileBytes, a.L.tiles + t * kFp4TileBytes, kFp4TileBytes, bar + stage, policy);
+    }
+  };
+  // lane l knows the l-th tile of the current 32 and the page id of the next
+  const int pid0 = page_of(lane);
+  int next_pid = page_of(32 + lane);
+  long long cur = stored(lane, pid0), next = -1;
+#pragma unroll
+  for (int k = 0; k < kStages; ++k) {
+    const long long t = __shfl_sync(0xffffffffu, cur, k);
+    if (lane != 0 || k >= mine) continue;
+    if (a.stall && k == 0 && blockIdx.x == 0 && warp == 0)
+      mbar_expect_tx(bar, kFp4TileBytes);
+    else
+      issue(k, t);
+  }
+
+  // q as the B operand: scaled per head by a power of two, fp16
+  float cs0, cs1;
+  {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (r >= G) qf[i] = 0;                   // columns without a head
+      top = max(top, max(qf[i] & 0x7FFFu, (qf[i] >> 16) & 0x7FFFu));
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int up = min(14 - ((int)(top >> 7) - 127), 126);
+    const float mul = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : pow2i(up);   // not finite: NaN
+#pragma unroll
+    for (int i = 0; i < 16; ++i) qf[i] = pack_f16(bf16lo(qf[i]) * mul, bf16hi(qf[i]) * mul);
+    const float cs = a.c.scale * 1.4426950408889634f * pow2i(a.L.k_exp) * pow2i(-up);
+    cs0 = __shfl_sync(0xffffffffu, cs, 8 * j);          // heads 2j, 2j + 1
+    cs1 = __shfl_sync(0xffffffffu, cs, 8 * j + 4);
+  }
+
+  float M0 = kNoRef, M1 = kNoRef, l0 = 0.f, l1 = 0.f;
+  float o[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+
+  bool ok = true;
+  int k = 0, stage = 0, phase = 0;
+  for (; k < mine; ++k) {
+    if ((k & 31) == 0) {                       // the next 32: their page ids have been on the way since the last batch
+      if (k) cur = next;
+      next = stored(k + 32 + lane, next_pid);
+      next_pid = page_of(k + 64 + lane);
+    }
+    // the lanes vote: a copy that lands just as the limit runs out must not part them
+    if (!__all_sync(0xffffffffu, mbar_wait(bar + stage, phase, a.polls))) {
+      ok = false;
+      break;
+    }
+    const bool have = __shfl_sync(0xffffffffu, (int)(cur >= 0), k & 31);
+    if (have) {
+      const int tile = sp.tile(i0 + warp + k * kWarps);
+      const uint32_t vis = sp.mask(tile);
+      const uint8_t* st = ring + stage * kFp4TileBytes;
+      const uint4 ka = *reinterpret_cast<const uint4*>(st + r * 64 + j * 16);
+      const uint4 kb = *reinterpret_cast<const uint4*>(st + (r + 8) * 64 + j * 16);
+      const uint32_t sa2 = cvt_lo(*reinterpret_cast<const uint16_t*>(st + kFp4KScale + r * 8 + j * 2));
+      const uint32_t sb2 = cvt_lo(*reinterpret_cast<const uint16_t*>(st + kFp4KScale + (r + 8) * 8 + j * 2));
+      const uint4 va = *reinterpret_cast<const uint4*>(st + kFp4V + lane * 16);
+      const uint4 vb = *reinterpret_cast<const uint4*>(st + kFp4V + 512 + lane * 16);
+      uint4 ga = *reinterpret_cast<const uint4*>(st + kFp4VScale + j * 32);
+      uint4 gb = *reinterpret_cast<const uint4*>(st + kFp4VScale + j * 32 + 16);
+      float acc[2][4] = {};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {   // channels 32 j + 16 half ..: one scale for each token
+        const uint32_t ma = __byte_perm(sa2, sa2, half ? 0x3232 : 0x1010), mb = __byte_perm(sb2, sb2, half ? 0x3232 : 0x1010);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          uint32_t a0, a2, a4, a6, a1, a3, a5, a7;
+          codes4((&ka.x)[2 * half + w], a0, a2, a4, a6);
+          codes4((&kb.x)[2 * half + w], a1, a3, a5, a7);
+          const int s = 4 * half + 2 * w;
+          mma_f16(acc[half], mul2(a0, ma), mul2(a1, mb), mul2(a2, ma), mul2(a3, mb), qf[2 * s], qf[2 * s + 1]);
+          mma_f16(acc[half], mul2(a4, ma), mul2(a5, mb), mul2(a6, ma), mul2(a7, mb), qf[2 * s + 2], qf[2 * s + 3]);
+        }
+      }
+      float x0 = (acc[0][0] + acc[1][0]) * cs0, x1 = (acc[0][1] + acc[1][1]) * cs1;   // token r, heads 2j, 2j + 1
+      float x2 = (acc[0][2] + acc[1][2]) * cs0, x3 = (acc[0][3] + acc[1][3]) * cs1;   // token r + 8
+      if (vis != 0xFFFFu) {                    // hidden tokens: no weight, and scales of zero
+        if (!((vis >> r) & 1)) x0 = x1 = -INFINITY;
+        if (!((vis >> (r + 8)) & 1)) x2 = x3 = -INFINITY;
+        const uint32_t lo = (vis >> (2 * j)) & 3u, hi = (vis >> (2 * j + 8)) & 3u;
+        const uint32_t keep = (lo & 1 ? 0xFFu : 0u) | (lo & 2 ? 0xFF00u : 0u) | (hi & 1 ? 0xFF0000u : 0u) |
+                              (hi & 2 ? 0xFF000000u : 0u);
+        ga.x &= keep, ga.y &= keep, ga.z &= keep, ga.w &= keep;
+        gb.x &= keep, gb.y &= keep, gb.z &= keep, gb.w &= keep;
+      }
+      // as differences: where M is large, M + 7 is rounded by as much as that
+      float d0 = x0 - M0, d1 = x1 - M1, d2 = x2 - M0, d3 = x3 - M1;
+      if (__any_sync(0xffffffffu, fmaxf(fmaxf(d0, d2), fmaxf(d1, d3)) > kRaise)) {
+        const float t0 = warp_max_xor(fmaxf(x0, x2), 4), t1 = warp_max_xor(fmaxf(x1, x3), 4);
+        const float n0 = t0 - M0 > kRaise ? t0 - kHead : M0, n1 = t1 - M1 > kRaise ? t1 - kHead : M1;
+        const float f0 = exp2_neg(M0 - n0), f1 = exp2_neg(M1 - n1);
+        M0 = n0;
+        M1 = n1;
+        l0 *= f0;
+        l1 *= f1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          o[i][0] *= f0;
+          o[i][1] *= f1;
+          o[i][2] *= f0;
+          o[i][3] *= f1;
+        }
+        d0 = x0 - M0, d1 = x1 - M1, d2 = x2 - M0, d3 = x3 - M1;
+      }
+      const float w0 = exp2_neg(d0), w1 = exp2_neg(d1), w2 = exp2_neg(d2), w3 = exp2_neg(d3);
+      l0 += w0 + w2;
+      l1 += w1 + w3;
+      const uint32_t p0 = movmatrix_t(pack_f16(w0, w1)), p1 = movmatrix_t(pack_f16(w2, w3));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {            // block i of channels: 16 i + 2 r, 16 i + 2 r + 1
+        uint32_t v0, v1, v2, v3;
+        codes4(i < 4 ? (&va.x)[i] : (&vb.x)[i - 4], v0, v1, v2, v3);
+        const uint32_t g = i < 4 ? (&ga.x)[i] : (&gb.x)[i - 4];
+        mma_f16(o[i], v0, v1, v2, v3, mul2(p0, cvt_lo(g)), mul2(p1, cvt_hi(g)));
+      }
+    }
+    __syncwarp();
+    const int kn = k + kStages;
+    if (kn < mine) {
+      const long long t = __shfl_sync(0xffffffffu, (kn >> 5) == (k >> 5) ? cur : next, kn & 31);
+      if (lane == 0) issue(stage, t);
+    }
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+  if (!ok) {
+    // A copy did not arrive in time.  Those in flight, this one among them, would land on
+    // what is written over the ring: they are waited for, by the full limit (but not for
+    // one that the test hook never started).
+    if (lane == 0) flag_error(a.err, KV_DEVERR_TIMEOUT);
+    for (int kk = k; kk < min(mine, k + kStages); ++kk) {
+      if (!(a.stall && kk == 0 && blockIdx.x == 0 && warp == 0)) mbar_wait(bar + stage, phase, kPolls);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    __syncwarp();
+    M0 = M1 = kNoRef;
+    l0 = l1 = 0.f;
+  }
+
+  // ---- the warps' results -> the CTA's, the pair's ----
+  __syncthreads();                             // every warp is done with its ring
+  float* wo = reinterpret_cast<float*>(smem);
+  float* wm = wo + kWarps * G * kHeadStride;   // [warp][head] M, then l
+  float* wl = wm + kWarps * G;
+  l0 = warp_sum_xor(l0, 4);
+  l1 = warp_sum_xor(l1, 4);
+  const float ve = pow2i(a.L.v_exp);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int g = 2 * j + u;
+    if (g < G) {
+      float* d = wo + (warp * G + g) * kHeadStride + 2 * r;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) *reinterpret_cast<float2*>(d + 16 * i) = make_float2(o[i][u] * ve, o[i][2 + u] * ve);
+      if (r == 0) {
+        wm[warp * G + g] = u ? M1 : M0;
+        wl[warp * G + g] = u ? l1 : l0;
+      }
+    }
+  }
+  __syncthreads();
+  join_parts<G, kWarps, kHeadStride>(a.c, a.Hq, a.n_split, a.cluster, a.tickets, smem, split, pair, b, h,
+                                     [](int c) { return c; });
+}
+
+// Splits per (sequence, KV head), from the host's bound on visible tiles: none up to two
+// tiles per warp; else a tile per warp at least, at most one wave of one CTA per SM where
+// pairs are few, two per SM where that would leave SMs idle, and about six waves for more
+// pairs, so that sequences of different lengths even out.  Where a cluster's worth of
+// splits has up to two tiles per warp: no more than those.
+int splits(const Pool& p, int B, long long max_len, int window, int n_sink) {
+  long long tokens = max_len;
+  if (window) tokens = std::min(tokens, (long long)window + n_sink + 2 * kTile);
+  const long long tiles = (tokens + kTile - 1) / kTile, pairs = (long long)B * p.cfg.num_kv_heads, sms = p.sm_count;
+  const long long want = sms >= 4 * pairs ? sms / pairs : (pairs <= sms ? 2 * sms / pairs : (12 * sms + pairs - 1) / pairs);
+  if (tiles <= 2 * kWarps) return 1;
+  const long long most = std::min<long long>((tiles + kWarps - 1) / kWarps, kMaxSplits);
+  const long long n = std::max(1ll, std::min(want, most));
+  return (int)(tiles <= 2 * kMaxCluster * kWarps ? std::min<long long>(n, kMaxCluster) : n);
+}
+
+template <int G>
+cudaError_t launch_t(const DecodeFp4Args& a, int device, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(decode_fp4_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return e;
+  const long long pairs = (long long)a.B * a.L.Hkv;
+  if (pairs * a.n_split > INT32_MAX) return cudaErrorInvalidValue;
+  DecodeFp4Args b = a;
+  b.cluster = a.n_split > 1 && a.n_split <= kMaxCluster &&
+              pairs <= resident_clusters<decode_fp4_kernel<G>>(device, a.n_split, kThreads, kSmem);
+  return launch_dependent(decode_fp4_kernel<G>, dim3((unsigned)(pairs * a.n_split)), kThreads, kSmem, s,
+                          b.cluster ? a.n_split : 1, b);
+}
+
+}  // namespace
+
+size_t decode_fp4_workspace(const Pool& p, int B, int max_len) {
+  const int n = splits(p, B, max_len, 0, 0);
+  return n == 1 ? 16 : (size_t)B * p.cfg.num_q_heads * n * kPart * sizeof(float);
+}
+
+// Fewer sequences are split further: the most that any batch up to B needs.
+size_t decode_fp4_workspace_up_to(const Pool& p, int B, int max_len) {
+  size_t most = 0;
+  for (int b = 1; b <= B; ++b) most = std::max(most, decode_fp4_workspace(p, b, max_len));
+  return most;
+}
+
+cudaError_t launch_decode_fp4(const Pool& p, const Fp4Layer& L, int layer, int B, const AttnCall& c, cudaStream_t s) {
+  DecodeFp4Args a{L, c, B, p.cfg.num_q_heads, splits(p, B, c.max_len, c.window, c.n_sink),
+                  p.tickets + (size_t)layer * p.cfg.max_seqs * p.cfg.num_kv_heads, p.err,
+                  p.test_wait_polls > 0 ? p.test_wait_polls : kPolls, p.test_stall_first_copy};
+  switch (p.G) {
+    case 1: return launch_t<1>(a, p.device, s);
+    case 2: return launch_t<2>(a, p.device, s);
+    case 4: return launch_t<4>(a, p.device, s);
+    default: return launch_t<8>(a, p.device, s);
+  }
+}
+
+}  // namespace kvint2

@@ -34,7 +34,7 @@
 #include <cmath>
 
 #include "kv_device.cuh"
-#include "kv_fp8.h"
+#include "kv_fp4.h"
 
 namespace kvint2 {
 
@@ -304,6 +304,48 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(RopeArgs a, const __g
   }
 }
 
+// The same with a position for each axis: a pair turns by that of its own.  Only the
+// table differs.
+template <bool kPairs>
+__global__ void __launch_bounds__(kThreads, 4)
+    rope_axes_kernel(RopeArgs a, int64_t pos_stride, const __grid_constant__ RopeAxes axes,
+                     const __grid_constant__ RopeParams rp) {
+  __shared__ __align__(16) float tab[kTile * kTokStride];
+  __shared__ int pos[kTile], at[4][kTile];
+  release_successor();
+  after_predecessor();
+  const int t0 = blockIdx.x * kTile;
+  if (threadIdx.x < kTile) {
+    const int t = threadIdx.x;
+    int low = t0 + t < a.n_tokens ? 0 : -1;    // below 0: a token without work
+    for (int x = 0; x < axes.n; ++x) {
+      at[x][t] = low < 0 ? -1 : a.positions[x * pos_stride + t0 + t];
+      low = min(low, at[x][t]);
+    }
+    pos[t] = low;
+  }
+  __syncthreads();
+  const int n = rp.rd >> 1;
+  for (int i = threadIdx.x; i < kTile * 64; i += kThreads) {
+    const int t = i >> 6, f = i & 63;
+    if (f < n && pos[t] >= 0) {
+      const float2 cs = turn_cos_sin((unsigned long long)at[axes.axis[f]][t] * rp.turn[f], rp.att);
+      float* d = tab + t * kTokStride + 4 * (f >> 3) + (f & 3) + 32 * ((f >> 2) & 1);
+      d[0] = cs.x;
+      d[64] = cs.y;
+    }
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 31, units = a.heads[0] + a.heads[1];
+  for (int u = blockIdx.y * kWarps + (threadIdx.x >> 5); u < units; u += gridDim.y * kWarps) {
+    const bool k = u >= a.heads[0];
+    const int h = u - (k ? a.heads[0] : 0);
+    const int64_t is = k ? a.in_stride[1] : a.in_stride[0], os = k ? a.out_stride[1] : a.out_stride[0];
+    rows_unit<kPairs>(rp, tab, pos, (k ? a.in[1] : a.in[0]) + t0 * is + h * 128, is,
+                      (k ? a.out[1] : a.out[0]) + t0 * os + h * 128, os, lane);
+  }
+}
+
 struct AppendFp8Args {
   const uint16_t *q, *k, *v;
   int64_t q_stride, k_stride, v_stride, qo_stride;
@@ -536,9 +578,8 @@ kv_status_t rope_params(const kv_rope_config_t& c, RopeParams* out) {
   return KV_OK;
 }
 
-cudaError_t launch_rope(const Pool& p, const RopeParams& r, int n_tokens, const int32_t* positions, const RopeRows& q,
-                        const RopeRows& k, cudaStream_t s) {
-  if (n_tokens == 0) return cudaSuccess;
+namespace {
+RopeArgs rope_args(const Pool& p, int n_tokens, const int32_t* positions, const RopeRows& q, const RopeRows& k) {
   RopeArgs a{};
   const RopeRows* rows[2] = {&q, &k};
   for (int w = 0; w < 2; ++w) {
@@ -550,9 +591,28 @@ cudaError_t launch_rope(const Pool& p, const RopeParams& r, int n_tokens, const 
   }
   a.positions = positions;
   a.n_tokens = n_tokens;
-  const long long tiles = ((long long)n_tokens + kTile - 1) / kTile;
-  const dim3 grid((unsigned)tiles, slices(p, tiles, a.heads[0] + a.heads[1], kRopePerSm));
-  return launch_dependent(r.interleaved ? rope_kernel<true> : rope_kernel<false>, grid, kThreads, 0, s, 1, a, r);
+  return a;
+}
+dim3 rope_grid(const Pool& p, const RopeArgs& a) {
+  const long long tiles = ((long long)a.n_tokens + kTile - 1) / kTile;
+  return dim3((unsigned)tiles, slices(p, tiles, a.heads[0] + a.heads[1], kRopePerSm));
+}
+}  // namespace
+
+cudaError_t launch_rope(const Pool& p, const RopeParams& r, int n_tokens, const int32_t* positions, const RopeRows& q,
+                        const RopeRows& k, cudaStream_t s) {
+  if (n_tokens == 0) return cudaSuccess;
+  const RopeArgs a = rope_args(p, n_tokens, positions, q, k);
+  return launch_dependent(r.interleaved ? rope_kernel<true> : rope_kernel<false>, rope_grid(p, a), kThreads, 0, s, 1, a, r);
+}
+
+cudaError_t launch_rope_axes(const Pool& p, const RopeParams& r, const RopeAxes& x, int n_tokens,
+                             const int32_t* positions, int64_t pos_stride, const RopeRows& q, const RopeRows& k,
+                             cudaStream_t s) {
+  if (n_tokens == 0) return cudaSuccess;
+  const RopeArgs a = rope_args(p, n_tokens, positions, q, k);
+  return launch_dependent(r.interleaved ? rope_axes_kernel<true> : rope_axes_kernel<false>, rope_grid(p, a), kThreads, 0,
+                          s, 1, a, pos_stride, x, r);
 }
 
 cudaError_t launch_append_fp8(const Pool& p, const Fp8Store& f, const RopeParams& r, int layer, int n_seqs,

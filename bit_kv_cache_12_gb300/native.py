@@ -30,6 +30,7 @@ KV_NOALLOC_SCRATCH_BYTES = 16 << 20
 KV_POOL_INT2_3TIER = 0
 KV_POOL_BF16 = 1
 KV_POOL_FP8 = 2
+KV_POOL_FP4 = 4
 KV_ROPE_STYLES = {"half": 0, "interleaved": 1}
 KV_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
@@ -59,6 +60,12 @@ class KvFp8Layout(ctypes.Structure):
                 ("codes_head_stride", ctypes.c_size_t), ("tile_bytes", ctypes.c_size_t),
                 ("exps_layer_stride", ctypes.c_size_t), ("exps_page_stride", ctypes.c_size_t),
                 ("exps_head_stride", ctypes.c_size_t)]
+
+
+class KvFp4Layout(ctypes.Structure):
+    _fields_ = [("tiles", ctypes.c_void_p), ("layer_stride", ctypes.c_size_t),
+                ("page_stride", ctypes.c_size_t), ("head_stride", ctypes.c_size_t),
+                ("tile_bytes", ctypes.c_size_t)]
 
 
 class KvRopeConfig(ctypes.Structure):
@@ -103,6 +110,17 @@ _SIG = {
     "kv_prefill_workspace_bytes": (ctypes.c_size_t, [_P, _I32, _I32, _I32]),
     "kv_prefill_attention_fp8": (_I32, [_P, _I32, _I32, _P, _P, _P, _P, _I32, _I32, _I32, ctypes.c_float,
                                         _I32, _I32, _P, _P, _P, ctypes.c_size_t, _P]),
+    "kv_pool_get_fp4_layout": (_I32, [_P, _I32, ctypes.POINTER(KvFp4Layout)]),
+    "kv_pool_set_fp4_range": (_I32, [_P, _I32, _I32, _I32]),
+    "kv_pool_set_rope_axes": (_I32, [_P, _I32, _I32, ctypes.POINTER(_I32), _I32]),
+    "kv_rope_apply_axes": (_I32, [_P, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P]),
+    "kv_append_fp4": (_I32, [_P, _I32, _I32, _P, _I64, _P, _I64, _P, _P, _P, _I32, _I32, _P]),
+    "kv_read_fp4": (_I32, [_P, _I32, _I32, _P, _P, _P, _I32, _I32, _P, _I64, _P, _I64, _P]),
+    "kv_decode_attention_fp4": (_I32, [_P, _I32, _I32, _P, _P, _P, _I32, _I32, ctypes.c_float, _I32, _I32,
+                                       _P, _P, _P, ctypes.c_size_t, _P]),
+    "kv_prompt_workspace_bytes": (ctypes.c_size_t, [_P, _I32, _I32, _I32]),
+    "kv_prompt_attention": (_I32, [_P, _I32, _P, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _I32, _I32,
+                                   ctypes.c_float, _I32, _I32, _P, _P, _P, ctypes.c_size_t, _P]),
 }
 
 _lib = None
@@ -342,6 +360,65 @@ def kv_prefill_attention_fp8(pool, layer, n_seqs, q, cu_q, seq_len, page_table, 
         _ptr(out), _ptr(lse), _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
+def kv_pool_get_fp4_layout(pool, layer):
+    out = KvFp4Layout()
+    _check("kv_pool_get_fp4_layout", lib().kv_pool_get_fp4_layout(pool, layer, ctypes.byref(out)))
+    return out
+
+
+def kv_pool_set_fp4_range(pool, layer, k_exp, v_exp):
+    _check("kv_pool_set_fp4_range", lib().kv_pool_set_fp4_range(pool, layer, k_exp, v_exp))
+
+
+def kv_pool_set_rope_axes(pool, layer, n_axes, axis):
+    """axis: a sequence with the axis of each of the layer's rotary_dim / 2 pairs."""
+    _check("kv_pool_set_rope_axes", lib().kv_pool_set_rope_axes(
+        pool, layer, n_axes, (_I32 * len(axis))(*[int(x) for x in axis]), len(axis)))
+
+
+def kv_rope_apply_axes(pool, layer, n_tokens, positions, pos_stride, q, q_stride, k, k_stride, q_out,
+                       q_out_stride, k_out, k_out_stride, stream=None):
+    _check("kv_rope_apply_axes", lib().kv_rope_apply_axes(
+        pool, layer, n_tokens, _ptr(positions), pos_stride, _ptr(q), q_stride, _ptr(k), k_stride,
+        _ptr(q_out), q_out_stride, _ptr(k_out), k_out_stride, _stream(stream)))
+
+
+def kv_append_fp4(pool, layer, n_seqs, k, k_stride, v, v_stride, cu_tokens, start_pos, page_table,
+                  max_pages_per_seq, max_tokens_per_seq, stream=None):
+    _check("kv_append_fp4", lib().kv_append_fp4(
+        pool, layer, n_seqs, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(cu_tokens), _ptr(start_pos),
+        _ptr(page_table), max_pages_per_seq, max_tokens_per_seq, _stream(stream)))
+
+
+def kv_read_fp4(pool, layer, n_seqs, cu_tokens, start_pos, page_table, max_pages_per_seq,
+                max_tokens_per_seq, k_out, k_out_stride, v_out, v_out_stride, stream=None):
+    _check("kv_read_fp4", lib().kv_read_fp4(
+        pool, layer, n_seqs, _ptr(cu_tokens), _ptr(start_pos), _ptr(page_table), max_pages_per_seq,
+        max_tokens_per_seq, _ptr(k_out), k_out_stride, _ptr(v_out), v_out_stride, _stream(stream)))
+
+
+def kv_decode_attention_fp4(pool, layer, B, q, seq_len, page_table, max_pages_per_seq, max_seq_len,
+                            softmax_scale, window, n_sink, out, lse, workspace, workspace_bytes,
+                            stream=None):
+    _check("kv_decode_attention_fp4", lib().kv_decode_attention_fp4(
+        pool, layer, B, _ptr(q), _ptr(seq_len), _ptr(page_table), max_pages_per_seq, max_seq_len,
+        float(softmax_scale), window, n_sink, _ptr(out), _ptr(lse), _ptr(workspace),
+        workspace_bytes, _stream(stream)))
+
+
+def kv_prompt_workspace_bytes(pool, n_seqs, max_q_per_seq, max_k_per_seq):
+    return lib().kv_prompt_workspace_bytes(pool, n_seqs, max_q_per_seq, max_k_per_seq)
+
+
+def kv_prompt_attention(pool, n_seqs, q, q_stride, q_rows, k, k_stride, v, v_stride, kv_rows, cu_q,
+                        cu_k, max_q_per_seq, max_k_per_seq, softmax_scale, window, n_sink, out, lse,
+                        workspace, workspace_bytes, stream=None):
+    _check("kv_prompt_attention", lib().kv_prompt_attention(
+        pool, n_seqs, _ptr(q), q_stride, q_rows, _ptr(k), k_stride, _ptr(v), v_stride, kv_rows,
+        _ptr(cu_q), _ptr(cu_k), max_q_per_seq, max_k_per_seq, float(softmax_scale), window, n_sink,
+        _ptr(out), _ptr(lse), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
 # ---- device-memory views (zero copy) ---------------------------------------
 
 class _CudaArray:
@@ -421,6 +498,14 @@ class KVPool:
         shp = (c.num_pages, c.num_kv_heads, c.page_size // 16, 2)
         return (device_view(lay.codes, (*shp, 2048), torch.uint8, self),
                 device_view(lay.exps, shp, torch.int8, self))
+
+    def fp4_view(self, layer=0):
+        """FP4 pool: tiles uint8 [num_pages, Hkv, page_size/16, 2304]."""
+        import torch
+        lay = kv_pool_get_fp4_layout(self.handle, layer)
+        c = self.cfg
+        return device_view(lay.tiles, (c.num_pages, c.num_kv_heads, c.page_size // 16, lay.tile_bytes),
+                           torch.uint8, self)
 
     def error(self):
         return kv_pool_get_error(self.handle)

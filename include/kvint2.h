@@ -84,7 +84,12 @@ enum {
                                  after this code except to tear it down. */
 };
 
-typedef enum { KV_POOL_INT2_3TIER = 0, KV_POOL_BF16 = 1, KV_POOL_FP8 = 2 } kv_pool_kind_t;
+typedef enum {
+  KV_POOL_INT2_3TIER = 0,
+  KV_POOL_BF16 = 1,
+  KV_POOL_FP8 = 2,
+  KV_POOL_FP4 = 4         /* 3 is no kind                                    */
+} kv_pool_kind_t;
 
 typedef struct {
   int32_t kind;           /* kv_pool_kind_t                                  */
@@ -117,8 +122,8 @@ typedef struct {
  *   sink_k / sink_v:   bf16 [max_seqs][Hkv][sink_tokens][128]
  *   recent_k/recent_v: bf16 [max_seqs][Hkv][recent_tokens][128] (ring)
  *   BF16 pool: bf16_k / bf16_v bf16 [num_pages][Hkv][page_size][128]
- * Pointers that do not apply to the pool kind are NULL (an FP8 pool: all of
- * them; see kv_pool_get_fp8_layout). */
+ * Pointers that do not apply to the pool kind are NULL (an FP8 or FP4 pool: all
+ * of them; see kv_pool_get_fp8_layout and kv_pool_get_fp4_layout). */
 typedef struct {
   void* hist;
   size_t hist_layer_stride, hist_page_stride, hist_head_stride, tile_bytes;
@@ -269,10 +274,10 @@ kv_status_t kv_append_step(kv_pool_t* pool, int32_t layer, int32_t B, const void
                            const int32_t* page_table, int32_t max_pages_per_seq, void* stream);
 
 /* Bytes of device workspace kv_decode_attention / kv_decode_attention_bf16
- * / kv_decode_attention_fp8 need for a batch of B sequences whose history (INT2
- * pool) or total length (BF16 and FP8 pools) is at most max_len tokens.  0 on
- * invalid arguments.  Of an FP8 pool the size covers smaller batches too, which
- * are split further: a workspace for the largest B and max_len serves every
+ * / kv_decode_attention_fp8 / kv_decode_attention_fp4 need for a batch of B
+ * sequences whose history (INT2 pool) or total length (other pools) is at most
+ * max_len tokens.  0 on invalid arguments.  Of an FP8 or FP4 pool the size covers
+ * smaller batches too, which are split further: a workspace for the largest B and max_len serves every
  * call up to them.  Every decode call takes max_hist_len / max_seq_len <=
  * KV_MAX_DECODE_LEN (else KV_ERR_INVALID_ARG). */
 #define KV_MAX_DECODE_LEN 6553600
@@ -372,7 +377,9 @@ kv_status_t kv_decode_attention_noalloc(kv_pool_t* pool, int32_t layer, int32_t 
  * kv_decode_attention_fp8's first CTA waits for a copy that is never started,
  * and kv_prefill_attention_fp8's first CTA for keys that are never handed over;
  * both end the same way (the decode skips that warp's share of the tokens, the
- * prompt rows that CTA had taken on and not finished become NaN).  max_polls > 0
+ * prompt rows that CTA had taken on and not finished become NaN).  On an FP4 pool
+ * the first warp of kv_decode_attention_fp4's first CTA waits like that, and on a
+ * pool of any kind kv_prompt_attention's first CTA.  max_polls > 0
  * replaces the default poll limit of those waits (one to four seconds; a poll
  * takes up to 3.7 us) for the pool's decode, prompt and bulk append calls; 0
  * restores it.  INT2 and BF16 pools, whose decodes wait for copies in flight with
@@ -558,6 +565,154 @@ kv_status_t kv_prefill_attention_fp8(kv_pool_t* pool, int32_t layer, int32_t n_s
                                      float softmax_scale, int32_t window, int32_t n_sink, void* out,
                                      float* lse, void* workspace, size_t workspace_bytes,
                                      void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The 4-bit cache (pool kind KV_POOL_FP4) and what goes with it: rotary positions
+ * with several axes, writing and reading back, single-token attention over the
+ * cache, and attention over packed prompts of bf16 rows.  A prompt:
+ * kv_rope_apply_axes, kv_prompt_attention over its own rows, kv_append_fp4.  A
+ * token: kv_rope_apply_axes, kv_append_fp4, kv_decode_attention_fp4.  A chunk
+ * behind cached tokens: kv_read_fp4 of those in front of the chunk's own k and v
+ * rows, kv_prompt_attention.  Every call below requires the pool's device to be the
+ * current one (KV_ERR_INVALID_ARG otherwise) and reads the caller's buffers from
+ * device memory only.
+ *
+ * Format.  A token's 128 channels of one KV head and tensor (K or V) are 8 blocks of
+ * 16; a block has one e4m3 scale s and 16 e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives), and the layer one exponent e per tensor (kv_pool_set_fp4_range):
+ * the value is code * s * 2^e.  72 bytes instead of 256.
+ *   tiles uint8 [num_layers][num_pages][Hkv][page_size/16][2304], 16 tokens each;
+ *   of token t and channel c of a tile
+ *     K code  at 64 t + c/2, bits 4 (c%2) ..
+ *     V code  at 1024 + 512 (c/64) + 64 ((c%16)/2) + 16 ((t%8)/2) + 4 ((c/16)%4)
+ *                + 2 (t/8) + c%2, bits 4 (t%2) ..
+ *     K scale at 2048 + 8 t + c/16
+ *     V scale at 2176 + 32 ((t%8)/2) + 4 (c/16) + 2 (t/8) + t%2
+ * ------------------------------------------------------------------------- */
+
+typedef struct {
+  void* tiles;
+  size_t layer_stride, page_stride, head_stride, tile_bytes;
+} kv_fp4_layout_t;
+
+/* Where an FP4 pool keeps `layer` (device pointer, strides in bytes; tile_bytes =
+ * 2304). */
+kv_status_t kv_pool_get_fp4_layout(const kv_pool_t* pool, int32_t layer, kv_fp4_layout_t* out);
+
+/* The exponents of one layer's K and V, -32 to 32 each (0 until set).  A block's
+ * scale is its largest magnitude / 6 / 2^e as an e4m3 number: exact to 4 bits for
+ * magnitudes from 2^(e-3) to 2688 * 2^e, coarser down to 2^(e-7), zero below that,
+ * saturated above.  A host call: it holds for the calls made after it, a
+ * captured graph keeps what was set when it was captured, and tokens that are
+ * cached already change by the same power of two. */
+kv_status_t kv_pool_set_fp4_range(kv_pool_t* pool, int32_t layer, int32_t k_exp, int32_t v_exp);
+
+/* Which axis turns each rotated pair of one layer (any pool kind): pair i of a
+ * token is rotated by the token's position on axis[i], for images and video (time,
+ * row, column).
+ *   n_axes  1 to 4
+ *   axis    host int32 [n_pairs], each 0 to n_axes - 1; n_pairs = rotary_dim / 2
+ * The layer's rotary positions are set first (kv_pool_set_rope, with a rotary_dim
+ * above 0; it takes the axes back to one).  A host call, like kv_pool_set_rope.
+ * Calls that take one position per token (kv_rope_apply, kv_append_fp8) use it on
+ * every axis. */
+kv_status_t kv_pool_set_rope_axes(kv_pool_t* pool, int32_t layer, int32_t n_axes, const int32_t* axis,
+                                  int32_t n_pairs);
+
+/* kv_rope_apply with a position for each of the layer's axes.
+ *   positions  device int32 [n_axes][pos_stride], pos_stride >= n_tokens: token i's
+ *              position on axis a at positions[a * pos_stride + i]; the rows of a
+ *              token with a negative position on any axis are neither read nor
+ *              written
+ * The other arguments, and the result for the same angles, as in kv_rope_apply. */
+kv_status_t kv_rope_apply_axes(const kv_pool_t* pool, int32_t layer, int32_t n_tokens,
+                               const int32_t* positions, int64_t pos_stride, const void* q,
+                               int64_t q_stride, const void* k, int64_t k_stride, void* q_out,
+                               int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                               void* stream);
+
+/* Write tokens to an FP4 pool: token i of sequence s goes to cache position
+ * start_pos[s] + i, in page page_table[s][position / page_size].  k is stored as it
+ * is given: rotated already.
+ *   k, v       device bf16, token i at k + i*k_stride, its Hkv heads of 128 channels
+ *              contiguous; 16-byte aligned, strides (in elements) multiples of 8 and
+ *              at least a token's channels
+ *   cu_tokens  device int32 [n_seqs+1] prefix sums; rows from cu_tokens[n_seqs] on
+ *              are not read
+ *   start_pos  device int32 [n_seqs]: tokens the sequence already caches
+ *   max_tokens_per_seq  host bound (sizes the grid; longer sequences are flagged
+ *              KV_DEVERR_SEQ_RANGE and truncated)
+ * Of each block of 16 channels x (as multiples of 2^e):
+ *   s = max |x| / 6 rounded to e4m3 (nearest even, at most 448),
+ *   code = x / s rounded to e2m1 (nearest even, at most 6); 0 where s is 0.
+ * The quotients are IEEE fp32 ones, so codes can be reproduced bit by bit.  A block
+ * with a NaN or an infinity is stored as NaN (its scale is).  Other tokens keep
+ * their bytes, also where a tile is shared with them.  Sequences must not share a
+ * page that is written.  A sequence that would leave the page table's span, or pass
+ * position 2^31 - 2, is skipped (KV_DEVERR_SEQ_RANGE); a tile with a bad page id is
+ * not stored (KV_DEVERR_PAGE_ID). */
+kv_status_t kv_append_fp4(kv_pool_t* pool, int32_t layer, int32_t n_seqs, const void* k,
+                          int64_t k_stride, const void* v, int64_t v_stride,
+                          const int32_t* cu_tokens, const int32_t* start_pos,
+                          const int32_t* page_table, int32_t max_pages_per_seq,
+                          int32_t max_tokens_per_seq, void* stream);
+
+/* Read tokens of an FP4 pool back: row cu_tokens[s] + i of k_out and v_out becomes
+ * the token at cache position start_pos[s] + i of sequence s, its values rounded to
+ * bf16 (exact within bf16's range).  Arguments as in kv_append_fp4; either output
+ * may be NULL.  Rows from cu_tokens[n_seqs] on, those behind max_tokens_per_seq
+ * tokens of a sequence, those of a sequence out of range and those of a bad page
+ * are not written; errors as there. */
+kv_status_t kv_read_fp4(const kv_pool_t* pool, int32_t layer, int32_t n_seqs,
+                        const int32_t* cu_tokens, const int32_t* start_pos,
+                        const int32_t* page_table, int32_t max_pages_per_seq,
+                        int32_t max_tokens_per_seq, void* k_out, int64_t k_out_stride, void* v_out,
+                        int64_t v_out_stride, void* stream);
+
+/* One decode step over an FP4 pool.  Arguments, visible tokens, errors and limits as
+ * in kv_decode_attention_fp8. */
+kv_status_t kv_decode_attention_fp4(kv_pool_t* pool, int32_t layer, int32_t B, const void* q,
+                                    const int32_t* seq_len, const int32_t* page_table,
+                                    int32_t max_pages_per_seq, int32_t max_seq_len,
+                                    float softmax_scale, int32_t window, int32_t n_sink, void* out,
+                                    float* lse, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/* Causal attention over packed bf16 rows: sequence s has n_s = cu_q[s+1] - cu_q[s]
+ * queries and m_s = cu_k[s+1] - cu_k[s] keys and values, the queries being the last
+ * n_s of the m_s positions.  Query i is at position p = m_s - n_s + i and attends to
+ * the positions j <= p with j > p - window or j < n_sink (window 0: all j <= p); a
+ * query at a negative position sees nothing and gets zeros and lse = -inf.  The pool
+ * (of any kind) gives the head counts and the error word; its cache is not used.
+ *   q          device bf16, row i at q + i*q_stride, its Hq heads contiguous; k, v
+ *              the same with their Hkv heads.  16-byte aligned, strides in elements,
+ *              multiples of 8 and at least a token's channels, below 2^31
+ *   q_rows, kv_rows  host: rows that q, and k and v, hold (no row behind is touched)
+ *   cu_q, cu_k device int32 [n_seqs+1] prefix sums, from 0; rows from cu_q[n_seqs]
+ *              on are neither read nor written, rows of k and v from cu_k[n_seqs] on
+ *              never reach an output
+ *   max_q_per_seq, max_k_per_seq  host bounds, each at most KV_MAX_DECODE_LEN (blocks
+ *              of 256 rows of all sequences and KV heads at most 2^31 - 1)
+ *   out, lse   [q_rows][Hq][128] bf16, 16-byte aligned, and [q_rows][Hq] fp32 or NULL
+ *              (ln sum_j exp(softmax_scale * q.k_j), to join it with attention over
+ *              other tokens)
+ *   workspace  16-byte aligned, >= kv_prompt_workspace_bytes(pool, n_seqs,
+ *              max_q_per_seq, max_k_per_seq); one for the largest bounds serves every
+ *              call up to them
+ * A sequence with more queries or keys than its bound, a negative count, or rows
+ * outside [0, q_rows) or [0, kv_rows) sets KV_DEVERR_SEQ_RANGE and gets none of its
+ * rows written.  Logits are fp32.  What hidden keys and values hold never reaches the
+ * output, NaN and infinities included; a visible value that is not finite makes that
+ * output channel not finite.  n_seqs at most the pool's max_seqs.  Calls may overlap if their
+ * workspaces and outputs differ. */
+size_t kv_prompt_workspace_bytes(const kv_pool_t* pool, int32_t n_seqs, int32_t max_q_per_seq,
+                                 int32_t max_k_per_seq);
+kv_status_t kv_prompt_attention(kv_pool_t* pool, int32_t n_seqs, const void* q, int64_t q_stride,
+                                int64_t q_rows, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, int64_t kv_rows, const int32_t* cu_q,
+                                const int32_t* cu_k, int32_t max_q_per_seq, int32_t max_k_per_seq,
+                                float softmax_scale, int32_t window, int32_t n_sink, void* out,
+                                float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

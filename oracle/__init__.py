@@ -15,6 +15,8 @@ It is a plain, slow restatement of the method, step by step, in numpy:
   or (when the ring is full) eviction of the oldest recent token into history.
 * ``oracle.fp8cache``  the 8-bit cache: e4m3 codes with a power-of-two scale per
   tile, rotary positions, the append, attention under a window with first tokens.
+* ``oracle.fp4cache``  the 4-bit cache: e2m1 codes with an e4m3 scale per 16 channels,
+  rotary positions with several axes, attention over packed rows.
 
 Sources: "OSCAR: Offline Spectral Covariance-Aware Rotation for 2-bit KV Cache
 Quantization" (gist.science explainer), section 2.2 B "Online-Betriebsphase";
@@ -26,4 +28,4 @@ come from the oracle itself (closed forms, brute force, hand-worked fixtures
 under ``tests/golden/``).
 """
 
-from . import kvquant, attention, tiers, fp8cache  # noqa: F401
+from . import kvquant, attention, tiers, fp8cache, fp4cache  # noqa: F401
