@@ -12,11 +12,14 @@
 // One CTA per SM: two tiles of 128 rows take turns, one in the tensor cores while the other
 // is in the softmax.
 //   warps 0-3, 4-7   softmax of a tile: a thread owns a row; S is read from tensor memory,
-//                    the weights go back over it as bf16; then this item's rows
-//   warps 8-11       look through the values of tiles that some row sees only in part
+//                    the weights go back over it as bf16
+//   warps 8-11       write an item's rows, while the softmax is at the next one
 //   warp 12          issues the products: S = Q K^T from shared memory, O += P V with P from
 //                    tensor memory and V token-major as it is stored
-//   warp 13          walks the items; warp 14 loads q, K and V tiles (TMA); warp 15 idles
+//   warp 13          walks the items
+//   warp 14          loads q, K and V tiles (TMA)
+//   warp 15          hands loaded tiles on to the issuer, after a look through the values of
+//                    those that some row sees only in part
 // Tensor memory: S0, S1 (P over them), O0, O1, 128 columns each.
 // Hidden keys: a tile that some row sees only in part is masked by select after the product
 // (a NaN in a hidden K row never enters).  Its values that are not finite are zeroed in
@@ -42,27 +45,33 @@ constexpr int kKeys = 128;                     // keys of a tile
 constexpr int kThreads = 16 * 32;              // four warpgroups
 // registers per thread of the softmax warpgroups and of the two others: they share the
 // launch's 128 each
-constexpr int kSoftRegs = 200, kOtherRegs = 56;
+constexpr int kSoftRegs = 184, kOtherRegs = 72;
 static_assert(2 * kSoftRegs + 2 * kOtherRegs <= 4 * 128, "setmaxnreg.inc draws on the launch's registers");
 constexpr int kPolls = 1 << 18;                // bound of a wait: a poll suspends for up to 3.7 us, so about a second
 constexpr int kMaxSplits = 32;
 constexpr int kPart = 132;                     // floats of a row's part: lse, 3 unused, 128 channels
 constexpr float kNoRef = -3e38f;
 constexpr float kRaise = 20.f;
-constexpr int kStages = 2;                     // of K and of V
+constexpr int kStages = 2;                     // of K and of V (the issuer takes them in turns)
 
 constexpr uint32_t kOffQ = 0;                  // two tiles
 constexpr uint32_t kOffK = 2 * kOperand;
 constexpr uint32_t kOffV = kOffK + kStages * kOperand;
-constexpr uint32_t kOffOut = kOffV + kStages * kOperand;   // 2 KB for each softmax warp
-constexpr uint32_t kOffInfo = kOffOut + 8 * 2048;
+constexpr uint32_t kOffOut = kOffV + kStages * kOperand;   // 4 KB for each writing warp
+constexpr uint32_t kOffInfo = kOffOut + 4 * 4096;
 
 constexpr int kItems = 4;                      // ring of items
 constexpr int kLists = 8;                      // ring of passes
 
-enum { kKFull = 0, kKEmpty = kKFull + kStages, kVLand = kKEmpty + kStages, kVFull = kVLand + kStages,
-       kVEmpty = kVFull + kStages, kQFull = kVEmpty + kStages, kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kPFull = kSFull + 2,
-       kOFull = kPFull + 2, kDrain = kOFull + 2, kCancel, kItem, kFree = kItem + kItems, kBars = kFree + kItems };
+constexpr int kRing = 4;                       // of barriers that may run ahead of those who wait for them
+
+// Barriers.  kData: V of a pass and K of the next (an item's first K comes with q).  kGo:
+// all that the products of a pass wait for, a ring for each tile: P, and for tile 0 that the
+// data are there.  kEmpty: the products of a pass and the next scores are complete; kFirst:
+// an item's first scores are.
+enum { kData = 0, kEmpty = kData + kStages, kGo = kEmpty + kStages, kLooked = kGo + 2 * kRing, kQFull = kLooked + kRing,
+       kQEmpty = kQFull + 2, kFirst = kQEmpty + 2, kSFull = kFirst + 1, kOFull = kSFull + 2, kORead = kOFull + 2, kLast = kORead + 2, kDrain = kLast + 4,
+       kCancel, kItem, kFree = kItem + kItems, kBars = kFree + kItems };
 
 // An item: a block of rows and the key tiles they see.
 enum { kKeyed = 0, kNoKeys = 1, kStop = 2 };   // rows with keys, rows that see none, no item
@@ -80,12 +89,15 @@ struct Shared {
   uint4 cancel;                                // what the scheduler answered
   uint64_t bars[kBars];
   uint32_t list[kLists][4];                    // of a pass that is seen in part: tokens with values that are not finite
+  float2 ml[2][2][kRows];                      // of an item with keys (odd, even) and tile: each row's M and l,
+  uint32_t poison[2][2][4];                    // and whether it sees a token listed before the last pass;
+  int2 end[2];                                 // the last pass, and of those seen in part
   uint32_t tmem;
   int abort;
   int steps;                                   // items looked at so far
   int given;                                   // items published so far
   int taken;                                   // an item taken on but not published yet, else -1
-  int next[8];                                 // softmax warps, at their end: the item whose rows would have come next
+  int next[4];                                 // writing warps, at their end: the item whose rows would have come next
 };
 constexpr uint32_t kSmem = kOffInfo + sizeof(Shared) + 1024;
 
@@ -121,6 +133,11 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, i
           dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(h), "r"(row), "r"(smem_u32(bar))
       : "memory");
+}
+__device__ __forceinline__ void prefetch_box(const CUtensorMap* map, int c, int h, int row) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(c), "r"(h), "r"(row)
+               : "memory");
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 y = __floats2bfloat162_rn(a, b);
@@ -175,37 +192,37 @@ struct Maps {
   const CUtensorMap *q, *k, *v;
 };
 
-// The loads of an item: false where a wait ran out.  g, keyed: passes (of K and of V) and
-// items with keys loaded so far.
+// The loads of an item: false where a wait ran out.  Pass g brings V of its own and K of the
+// next pass, into stages g and g + 1 modulo two: free when the products of pass g - 2 and
+// the scores of pass g - 1 are complete.  q, g: items and passes loaded so far.
 __device__ __forceinline__ bool load_item(const PromptArgs& a, const Maps& maps, const Work& w, bool withhold, uint8_t* sm,
-                                          Shared* sh, const Waiter& wait, int (&g)[2], int (&keyed)[2]) {
+                                          Shared* sh, const Waiter& wait, int (&q)[2], int& g) {
   const int lane = threadIdx.x & 31, tokens = kRows / a.G, h = w.h, k0 = w.k0, q0 = w.c0 + w.row0 / a.G;
   const uint32_t base = smem_u32(sm);
   auto ready = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(sh->bars + bar, parity)) != 0; };
+  auto load = [&](uint32_t to, const CUtensorMap* map, int head, int row, int bar) {
+    load_box(base + to, map, 0, head, row, sh->bars + bar);
+    load_box(base + to + kOperand / 2, map, 64, head, row, sh->bars + bar);
+  };
   for (int tile = 0; tile < 2; ++tile) {
-    if (keyed[tile] && !ready(kQEmpty + tile, (keyed[tile] - 1) & 1)) return false;
+    if (q[tile] && !ready(kQEmpty + tile, (q[tile] - 1) & 1)) return false;
     if (lane == 0) {
-      uint64_t* bar = sh->bars + kQFull + tile;
-      mbar_expect_tx(bar, kOperand);
-      for (int half = 0; half < 2; ++half)
-        load_box(base + kOffQ + tile * kOperand + half * (kOperand / 2), maps.q, 64 * half, h * a.G, q0 + tile * tokens, bar);
+      mbar_expect_tx(sh->bars + kQFull + tile, tile ? 2 * kOperand : kOperand);
+      load(kOffQ + tile * kOperand, maps.q, h * a.G, q0 + tile * tokens, kQFull + tile);
+      // after the last scores of the item before: every K stage is free
+      if (tile) load(kOffK + g % kStages * kOperand, maps.k, h, k0 + w.tile(w.i0) * kKeys, kQFull + 1);
     }
-    ++keyed[tile];
+    ++q[tile];
   }
-  for (int i = w.i0; i < w.i1; ++i) {
-    const int row = k0 + w.tile(i) * kKeys;
-    for (int kv = 0; kv < 2; ++kv) {
-      const int stage = g[kv] % kStages, use = g[kv] / kStages;
-      if (use && !ready((kv ? kVEmpty : kKEmpty) + stage, (use - 1) & 1)) return false;
-      if (kv && withhold && i + 1 == w.i1) return false;
-      if (lane == 0) {
-        uint64_t* bar = sh->bars + (kv ? kVLand : kKFull) + stage;
-        mbar_expect_tx(bar, kOperand);
-        for (int half = 0; half < 2; ++half)
-          load_box(base + (kv ? kOffV : kOffK) + stage * kOperand + half * (kOperand / 2), kv ? maps.v : maps.k, 64 * half, h,
-                   row, bar);
-      }
-      ++g[kv];
+  for (int i = w.i0; i < w.i1; ++i, ++g) {
+    const int stage = g % kStages, last = i + 1 == w.i1;
+    if (g >= kStages && !ready(kEmpty + stage, (g / kStages - 1) & 1)) return false;
+    if (i == w.i0 + 1 && !ready(kFirst, (q[1] - 1) & 1)) return false;
+    if (withhold && last) return false;
+    if (lane == 0) {
+      mbar_expect_tx(sh->bars + kData + stage, last ? kOperand : 2 * kOperand);
+      if (!last) load(kOffK + (g + 1) % kStages * kOperand, maps.k, h, k0 + w.tile(i + 1) * kKeys, kData + stage);
+      load(kOffV + stage * kOperand, maps.v, h, k0 + w.tile(i) * kKeys, kData + stage);
     }
   }
   __syncwarp();
@@ -214,31 +231,29 @@ __device__ __forceinline__ bool load_item(const PromptArgs& a, const Maps& maps,
 
 __device__ __forceinline__ void load_tiles(const PromptArgs& a, const Maps& maps, uint8_t* sm, Shared* sh, const Waiter& wait) {
   const int lane = threadIdx.x & 31;
-  int g[2] = {0, 0}, keyed[2] = {0, 0};
+  int q[2] = {0, 0}, g = 0;
   for (int item = 0;; ++item) {
     const int slot = item & (kItems - 1);
     if (!__all_sync(0xffffffffu, wait.handed(sh->bars + kItem + slot, (item / kItems) & 1))) break;
     const Work& w = sh->work[slot];
     if (w.state == kStop) break;
-    if (w.state == kKeyed &&
-        !load_item(a, maps, w, a.stall && blockIdx.x == 0 && item == 0, sm, sh, wait, g, keyed))
-      break;
+    if (w.state == kKeyed && !load_item(a, maps, w, a.stall && blockIdx.x == 0 && item == 0, sm, sh, wait, q, g)) break;
     if (lane == 0) arrive(sh->bars + kFree + slot);
     __syncwarp();
   }
   // whatever happened to those who wait for them: no load may land after the CTA has ended
+#pragma unroll 1
+  for (int i = max(g - kStages, 0); i < g; ++i) mbar_wait(sh->bars + kData + i % kStages, (i / kStages) & 1, kPolls);
+#pragma unroll 1
   for (int i = 0; i < 2; ++i)
-    if (keyed[i]) mbar_wait(sh->bars + kQFull + i, (keyed[i] - 1) & 1, kPolls);
-  for (int kv = 0; kv < 2; ++kv)
-    for (int n = max(g[kv] - kStages, 0); n < g[kv]; ++n)
-      mbar_wait(sh->bars + (kv ? kVLand : kKFull) + n % kStages, (n / kStages) & 1, kPolls);
+    if (q[i]) mbar_wait(sh->bars + kQFull + i, (q[i] - 1) & 1, kPolls);
 }
 
-// ---- values of tiles seen in part (four warps, a thread to a token) ----------------
+// ---- loaded tiles, and the values of those seen in part (one warp) --------------------
 
 __device__ __forceinline__ void look_through(const PromptArgs& a, uint8_t* sm, Shared* sh, const Waiter& wait) {
-  const int tid = threadIdx.x & 127, lane = threadIdx.x & 31;
-  int g = 0;
+  const int lane = threadIdx.x & 31;
+  int g = 0, part = 0;                         // passes, and those that are seen in part
   for (int item = 0;; ++item) {
     const int slot = item & (kItems - 1);
     if (!__all_sync(0xffffffffu, wait.handed(sh->bars + kItem + slot, (item / kItems) & 1))) return;
@@ -246,20 +261,38 @@ __device__ __forceinline__ void look_through(const PromptArgs& a, uint8_t* sm, S
     if (w.state == kStop) return;
     if (w.state == kKeyed) {
       for (int i = w.i0; i < w.i1; ++i, ++g) {
-        const int stage = g % kStages;
-        if (!__all_sync(0xffffffffu, wait(sh->bars + kVLand + stage, (g / kStages) & 1))) return;
-        if (in_part(a, w, w.tile(i) * kKeys)) {
-          uint8_t* row = sm + kOffV + stage * kOperand + tid * 128;
-          uint32_t m = 0;
+        const int stage = g % kStages, t0 = w.tile(i) * kKeys;
+        if (!__all_sync(0xffffffffu, wait(sh->bars + kData + stage, (g / kStages) & 1))) return;
+        if (!in_part(a, w, t0)) {
+          if (lane == 0) arrive(sh->bars + kGo + g % kRing);
+          continue;
+        }
+        uint8_t* tile = sm + kOffV + stage * kOperand + lane * 128;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {          // a lane to a token
+          uint8_t* row = tile + 32 * 128 * q;
+          bool bad = false;
+          // where some row may not see all 32 tokens
+          if (t0 + 32 * q + 31 > w.first || (a.c.window && t0 + 32 * q < w.keys - a.c.window && t0 + 32 * q + 31 >= w.sinks)) {
+            // sums of products with zero: NaN if one of the values is not finite
+            __nv_bfloat162 n[4];
+            const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {       // the swizzle: eight lanes read eight different banks
-            const uint4 x = *reinterpret_cast<const uint4*>(row + (c >> 3) * (kOperand / 2) + (((c ^ tid) & 7) << 4));
-            m = __vmaxu2(__vmaxu2(__vmaxu2(m, x.x & 0x7FFF7FFFu), __vmaxu2(x.y & 0x7FFF7FFFu, x.z & 0x7FFF7FFFu)),
-                         x.w & 0x7FFF7FFFu);
+            for (int i = 0; i < 4; ++i) n[i] = zero;
+            auto add = [&](__nv_bfloat162& s, uint32_t x) { s = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&x), zero, s); };
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {     // the swizzle: eight lanes read eight different banks
+              const uint4 x = *reinterpret_cast<const uint4*>(row + (c >> 3) * (kOperand / 2) + (((c ^ lane) & 7) << 4));
+              add(n[0], x.x);
+              add(n[1], x.y);
+              add(n[2], x.z);
+              add(n[3], x.w);
+            }
+            const __nv_bfloat162 sum = __hadd2(__hadd2(n[0], n[1]), __hadd2(n[2], n[3]));
+            bad = __hisnan(sum.x) || __hisnan(sum.y);
           }
-          const bool bad = (m & 0xFFFFu) >= 0x7F80u || (m >> 16) >= 0x7F80u;
           const uint32_t listed = __ballot_sync(0xffffffffu, bad);
-          if (lane == 0) sh->list[g & (kLists - 1)][tid >> 5] = listed;
+          if (lane == 0) sh->list[g & (kLists - 1)][q] = listed;
           if (bad) {
 #pragma unroll 1
             for (int c = 0; c < 64; ++c) {
@@ -270,10 +303,15 @@ __device__ __forceinline__ void look_through(const PromptArgs& a, uint8_t* sm, S
               *p = x;
             }
           }
-          fence_async();
+          __syncwarp();
         }
+        fence_async();
         __syncwarp();
-        if (lane == 0) arrive(sh->bars + kVFull + stage);
+        if (lane == 0) {
+          arrive(sh->bars + kLooked + part % kRing);
+          arrive(sh->bars + kGo + g % kRing);
+        }
+        ++part;
       }
     }
     if (lane == 0) arrive(sh->bars + kFree + slot);
@@ -285,11 +323,13 @@ __device__ __forceinline__ void look_through(const PromptArgs& a, uint8_t* sm, S
 
 // The items: this CTA's own, then those of CTAs that have not been launched yet, asked of
 // the hardware's scheduler one ahead.
-__device__ __forceinline__ void walk(const PromptArgs& a, Shared* sh, const Waiter& wait) {
+__device__ __forceinline__ void walk(const PromptArgs& a, const CUtensorMap* q, Shared* sh, const Waiter& wait) {
   const int lane = threadIdx.x & 31;
   auto ready = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(sh->bars + bar, parity)) != 0; };
   auto publish = [&](const Work& w, int item) -> bool {
     const int slot = item & (kItems - 1);
+    if (w.state == kKeyed && lane < 4)         // its q comes to the L2 cache while the items before are worked on
+      prefetch_box(q, 64 * (lane & 1), w.h * a.G, w.c0 + w.row0 / a.G + (lane >> 1) * (kRows / a.G));
     if (item >= kItems && !ready(kFree + slot, (item / kItems - 1) & 1)) return false;
     if (lane == 0) {
       sh->work[slot] = w;
@@ -342,28 +382,26 @@ __device__ __forceinline__ void walk(const PromptArgs& a, Shared* sh, const Wait
 
 // The whole warp runs this, in step, and one lane of it issues: addresses stay in uniform
 // registers.  The loops are not unrolled: the code of the other warps passes through the
-// same instruction cache, and a short loop stays in it.
-__device__ __forceinline__ void issue_products(uint32_t tmem, uint8_t* sm, Shared* sh, const Waiter& wait) {
+// same instruction cache, and a short loop stays in it.  The tensor cores take four products
+// ahead (256 clocks), and a wait that the whole warp votes on takes some 150 of them: so
+// there is one wait and one commit between two groups of products, both by the lane that
+// issues.  After a wait that ran out it issues nothing more (`dead`); the others notice by
+// the abort flag.
+__device__ __forceinline__ void issue_products(const PromptArgs& a, uint32_t tmem, uint8_t* sm, Shared* sh, const Waiter& wait) {
   const uint32_t base = smem_u32(sm);
   const uint64_t q0 = desc(base + kOffQ, 16), k0 = desc(base + kOffK, 16), v0 = desc(base + kOffV, kOperand / 2);
-  auto ready = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(sh->bars + bar, parity)) != 0; };
-  auto scores = [&](int tile, int stage, bool last) {
-    if (elect_one()) {
-      uint64_t q = q0 + ((tile * kOperand) >> 4), k = k0 + ((stage * kOperand) >> 4);
-      const uint32_t d = tmem + 128 * tile;
+  bool dead = false;
+  auto scores = [&](int tile, int stage) {     // the issuing lane
+    uint64_t q = q0 + ((tile * kOperand) >> 4), k = k0 + ((stage * kOperand) >> 4);
+    const uint32_t d = tmem + 128 * tile;
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
+    for (int half = 0; half < 2; ++half) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma_ss(d, q + 2 * ks, k + 2 * ks, half | ks);
-        q += (kOperand / 2) >> 4;
-        k += (kOperand / 2) >> 4;
-      }
-      commit(sh->bars + kSFull + tile);
-      arrive(sh->bars + kSFull + tile);        // a release after this warp saw the lists so far
-      if (tile == 1) commit(sh->bars + kKEmpty + stage);
-      if (last) commit(sh->bars + kQEmpty + tile);
+      for (int ks = 0; ks < 4; ++ks) mma_ss(d, q + 2 * ks, k + 2 * ks, half | ks);
+      q += (kOperand / 2) >> 4;
+      k += (kOperand / 2) >> 4;
     }
-    __syncwarp();
+    commit(sh->bars + kSFull + tile);
   };
   int g = 0, keyed = 0;                        // passes and items with keys so far
   for (int item = 0;; ++item) {
@@ -372,43 +410,52 @@ __device__ __forceinline__ void issue_products(uint32_t tmem, uint8_t* sm, Share
     const int state = sh->work[slot].state, passes = sh->work[slot].i1 - sh->work[slot].i0;
     if (state == kStop) return;
     if (state == kKeyed) {
-      if (!ready(kKFull + g % kStages, (g / kStages) & 1)) return;
-#pragma unroll 1
-      for (int tile = 0; tile < 2; ++tile) {
-        if (!ready(kQFull + tile, keyed & 1)) return;
+      if (elect_one()) {
+        dead = dead || !wait(sh->bars + kQFull, keyed & 1) || !wait(sh->bars + kQFull + 1, keyed & 1);
         fence_after();
-        scores(tile, g % kStages, passes == 1);
+        if (!dead) {
+#pragma unroll 1
+          for (int tile = 0; tile < 2; ++tile) {
+            scores(tile, g % kStages);
+            if (passes == 1) commit(sh->bars + kQEmpty + tile);
+          }
+          commit(sh->bars + kFirst);
+        }
       }
+      __syncwarp();
+#pragma unroll 1
       for (int it = 0; it < passes; ++it, ++g) {
-        const int stage = g % kStages, next = (g + 1) % kStages;
+        const int stage = g % kStages;
+        const uint32_t ph = (g / kRing) & 1;
         const bool last = it + 1 == passes;
-        // V, and the K of the next scores, long since there: looked at before P is due
-        if (!ready(kVFull + stage, (g / kStages) & 1)) return;
-        if (!last && !ready(kKFull + next, ((g + 1) / kStages) & 1)) return;
 #pragma unroll 1
         for (int tile = 0; tile < 2; ++tile) {
-          if (!ready(kPFull + tile, g & 1)) return;
-          fence_after();
           if (elect_one()) {
-            uint64_t v = v0 + ((stage * kOperand) >> 4);
-            uint32_t p = tmem + 128 * tile;
-            const uint32_t d = tmem + 256 + 128 * tile;
+            dead = dead || !wait(sh->bars + kGo + tile * kRing + g % kRing, ph);
+            if (it == 0 && keyed) dead = dead || !wait(sh->bars + kORead + tile, (keyed - 1) & 1);
+            fence_after();
+            if (!dead) {
+              uint64_t v = v0 + ((stage * kOperand) >> 4);
+              uint32_t p = tmem + 128 * tile;
+              const uint32_t d = tmem + 256 + 128 * tile;
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
+              for (int half = 0; half < 2; ++half) {
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks)   // 16 tokens: 8 columns of P, 16 rows of V
-                mma_ts(d, p + 8 * ks, v + ((ks * 2048) >> 4), it | half | ks);
-              p += 32;
-              v += (4 * 2048) >> 4;
-            }
-            if (tile == 1) commit(sh->bars + kVEmpty + stage);
-            if (last) {
-              arrive(sh->bars + kOFull + tile);   // a release after this warp saw the last list
-              commit(sh->bars + kOFull + tile);
+                for (int ks = 0; ks < 4; ++ks)   // 16 tokens: 8 columns of P, 16 rows of V
+                  mma_ts(d, p + 8 * ks, v + ((ks * 2048) >> 4), it | half | ks);
+                p += 32;
+                v += (4 * 2048) >> 4;
+              }
+              if (last) {
+                commit(sh->bars + kOFull + tile);
+              } else {
+                scores(tile, stage ^ 1);
+                if (it + 2 == passes) commit(sh->bars + kQEmpty + tile);
+              }
+              if (tile == 1) commit(sh->bars + kEmpty + stage);
             }
           }
           __syncwarp();
-          if (!last) scores(tile, next, it + 2 == passes);
         }
       }
       ++keyed;
@@ -436,31 +483,53 @@ struct Row {
 
 struct RowOut {
   float M = kNoRef, l = 0.f;
-  bool poison = false;                         // sees a listed token
+  bool poison = false;                         // sees a token that is listed (before the last pass)
 };
 
-// The keys from t0 on that row i of the block sees.
-__device__ __forceinline__ void sees(const PromptArgs& a, const Work& w, int i, int t0, uint32_t (&see)[4]) {
-  const int pos = w.pos0 + Row(a, w, i).token;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t m = below(pos + 1 - t0, 32 * q);
-    if (a.c.window) m &= ~below(pos + 1 - a.c.window - t0, 32 * q) | below(w.sinks - t0, 32 * q);
-    see[q] = m;
-  }
+// The 32 keys from t0 on that the row at position pos sees.
+__device__ __forceinline__ uint32_t sees(const PromptArgs& a, const Work& w, int pos, int t0) {
+  uint32_t m = below(pos + 1 - t0, 0);
+  if (a.c.window) m &= ~below(pos + 1 - a.c.window - t0, 0) | below(w.sinks - t0, 0);
+  return m;
 }
-// Whether it sees a listed token of pass g (known once V is there).
-__device__ __forceinline__ bool poisoned(const PromptArgs& a, const Work& w, const Shared* sh, int i, int t0, int g) {
-  uint32_t see[4];
-  sees(a, w, i, t0, see);
-  const uint32_t* list = sh->list[g & (kLists - 1)];
-  return ((list[0] & see[0]) | (list[1] & see[1]) | (list[2] & see[2]) | (list[3] & see[3])) != 0;
+// Whether it sees a listed token of pass g, the part-th one of those seen in part, whose
+// products are complete (so that the wait only orders this after the look).
+__device__ __forceinline__ bool poisoned(const PromptArgs& a, const Work& w, Shared* sh, int i, int t0, int g, int part) {
+  mbar_wait(sh->bars + kLooked + part % kRing, (part / kRing) & 1, kPolls);
+  const int pos = w.pos0 + Row(a, w, i).token;
+  uint32_t hit = 0;
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) hit |= sh->list[g & (kLists - 1)][q] & sees(a, w, pos, t0 + 32 * q);
+  return hit != 0;
+}
+
+// Scores of keys that this thread's row does not see: -inf (before the sign that scale may
+// bring), in tensor memory.  A short loop beside the usual path: unrolled into it, it cost
+// 1,500 clocks where it ran, cold as it is.
+__device__ __forceinline__ void hide(const PromptArgs& a, const Work& w, uint32_t ts, int pos, int t0, bool minus) {
+  const float none = minus ? INFINITY : -INFINITY;
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t see = sees(a, w, pos, t0 + 32 * q);
+    if (__all_sync(0xffffffffu, see == 0xFFFFFFFFu)) continue;
+    float v[32];
+    ld32(ts + 32 * q, v);
+    settle(v);
+    uint32_t u[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) u[i] = __float_as_uint((see >> i) & 1 ? v[i] : none);
+    st16(ts + 32 * q, u);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) u[i] = __float_as_uint((see >> (16 + i)) & 1 ? v[16 + i] : none);
+    st16(ts + 32 * q + 16, u);
+  }
+  wait_st();
 }
 
 // The passes of an item, up to its last weights.  g: the pass, counted over the CTA's
-// items; left at the last one.
+// items; left at the last one.  parts: those of them that are seen in part.
 __device__ __forceinline__ bool softmax_rows(const PromptArgs& a, const Work& w, uint32_t trow, int tile, Shared* sh,
-                                             const Waiter& wait, int& g, RowOut& ro) {
+                                             const Waiter& wait, int& g, int& parts, RowOut& ro) {
   const uint32_t ts = trow + 128 * tile, to = trow + 256 + 128 * tile;
   const int i0 = tile * kRows + (threadIdx.x & 127), passes = w.i1 - w.i0;
   const bool minus = a.c.scale < 0.f;
@@ -472,10 +541,12 @@ __device__ __forceinline__ bool softmax_rows(const PromptArgs& a, const Work& w,
     const int t0 = w.tile(w.i0 + it) * kKeys;
     if (!__all_sync(0xffffffffu, wait(sh->bars + kSFull + tile, g & 1))) return false;
     fence_after();
-    if (check >= 0) ro.poison |= poisoned(a, w, sh, i0, check, g - 1);
+    if (check >= 0) ro.poison |= poisoned(a, w, sh, i0, check, g - 1, parts - 1);
     const bool part = in_part(a, w, t0);
     check = part ? t0 : -1;
+    parts += part;
     float c = cs;
+    if (part) hide(a, w, ts, w.pos0 + Row(a, w, i0).token, t0, minus);
     float v[kKeys];
 #pragma unroll
     for (int q = 0; q < 4; ++q) ld32(ts + 32 * q, v + 32 * q);
@@ -484,13 +555,6 @@ __device__ __forceinline__ bool softmax_rows(const PromptArgs& a, const Work& w,
     if (minus) {
 #pragma unroll
       for (int i = 0; i < kKeys; ++i) v[i] = -v[i];
-    }
-    if (part) {
-      uint32_t see[4];
-      sees(a, w, i0, t0, see);
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i)
-        if (!((see[i >> 5] >> (i & 31)) & 1)) v[i] = -INFINITY;
     }
     float top[4];
 #pragma unroll
@@ -556,9 +620,14 @@ __device__ __forceinline__ bool softmax_rows(const PromptArgs& a, const Work& w,
     wait_st();
     fence_before();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) arrive(sh->bars + kPFull + tile);
+    if ((threadIdx.x & 31) == 0) arrive(sh->bars + kGo + tile * kRing + g % kRing);
     if (it + 1 == passes) return true;
   }
+}
+
+// A row's part of a split.
+__device__ __forceinline__ float* part_of(const PromptArgs& a, const Work& w, const Row& r) {
+  return static_cast<float*>(a.c.ws) + ((((size_t)w.s * a.c.max_q + r.token) * a.Hq + r.hq) * a.n_split + w.split) * kPart;
 }
 
 // Channels 32 q .. of a row that sees listed tokens: a bit for each that some visible value
@@ -591,82 +660,134 @@ __device__ __forceinline__ uint32_t spoiled(const PromptArgs& a, const Work& w, 
   return bits;
 }
 
-// A row's result: normalised to the output, or as a part of a split.  `stage`: 2 KB of
-// shared memory for 32 channels of the warp's 32 rows, from which they are written 64 bytes
-// at a time.
-__device__ __forceinline__ void write_row(const PromptArgs& a, const Work& w, uint32_t to, uint8_t* stage, int row0, bool any,
-                                          bool ok, const RowOut& ro) {
-  const int lane = threadIdx.x & 31;
-  const Row row(a, w, row0 + lane);
-  const float nan = __uint_as_float(0x7FC00000u);
-  const bool empty = ok && ro.l == 0.f;
-  const float f = !ok ? nan : (empty ? 0.f : 1.f / ro.l);
-  const float lse = !ok ? nan : lse_of(ro.M, ro.l);
-  float* part = static_cast<float*>(a.c.ws) + ((((size_t)w.s * a.c.max_q + row.token) * a.Hq + row.hq) * a.n_split + w.split) * kPart;
-  // where this lane's 16 bytes of the warp's rows 8 i + lane / 4 go
-  uint4* dst[4];
+// Rows of a tile, a thread to a row: its products times f to the output, or as a part of a
+// split.  `stage`: 4 KB of shared memory for 64 channels of the warp's 32 rows, from which
+// they are written 128 bytes at a time.  have: there are products (else f stands for all);
+// read: their barrier, arrived on once they are out of tensor memory.  Short loops: the code
+// is cold whenever it runs (unrolled, a tile took 11,000 clocks).
+__device__ __forceinline__ void write_rows(const PromptArgs& a, const Work& w, uint32_t to, uint8_t* stage, int row0, bool have,
+                                           float f, uint64_t* read) {
+  const int lane = threadIdx.x & 31, shift = __ffs(a.G) - 1;
+  // to shared memory: this lane's row, 16-byte chunk c of row r at c ^ r % 8 (no bank
+  // conflicts either way); from there: lane 8 u + c takes chunk c of rows 8 u + i
+  uint8_t* put = stage + lane * 128;
+  const uint8_t* get = stage + (lane >> 3) * 1024;
+  const int token = (w.row0 + row0 + 8 * (lane >> 3)) >> shift, m = w.m;
+  uint4* out = static_cast<uint4*>(a.c.out) + (((size_t)w.c0 + token) * a.Hq + w.h * a.G) * 16 + (lane & 7);
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      float o[16];
+      if (have) {
+        ld16(to + 64 * half + 16 * q, o);
+        settle16(o);
+      }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const Row r(a, w, row0 + 8 * i + (lane >> 2));
-    dst[i] = r.live ? static_cast<uint4*>(a.c.out) + r.qrow * 16 + (lane & 3) : nullptr;
+      for (int i = 0; i < 16; ++i) o[i] = have && f != 0.f ? o[i] * f : f;
+      if (a.n_split > 1) {
+        const Row row(a, w, row0 + lane);
+        if (row.live) {
+          float* part = part_of(a, w, row) + 4 + 64 * half + 16 * q;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4*>(part + 4 * i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          *reinterpret_cast<uint4*>(put + (((2 * q + c) ^ (lane & 7)) << 4)) =
+              make_uint4(pack_bf16(o[8 * c], o[8 * c + 1]), pack_bf16(o[8 * c + 2], o[8 * c + 3]),
+                         pack_bf16(o[8 * c + 4], o[8 * c + 5]), pack_bf16(o[8 * c + 6], o[8 * c + 7]));
+      }
+    }
+    if (have && half) {
+      fence_before();
+      __syncwarp();
+      if (lane == 0) arrive(read);
+    }
+    __syncwarp();
+    if (a.n_split == 1) {
+#pragma unroll 4
+      for (int i = 0; i < 8; ++i)
+        if (token + (i >> shift) < m)
+          out[(size_t)((i >> shift) * a.Hq + (i & (a.G - 1))) * 16 + 8 * half] =
+              *reinterpret_cast<const uint4*>(get + i * 128 + (((lane & 7) ^ i) << 4));
+      __syncwarp();
+    }
   }
-  const bool read = any && ok;                 // the same for the whole warp
-#pragma unroll
+}
+
+// The channels of a row that some visible value makes not finite, over what was just written.
+__device__ __forceinline__ void spoil_row(const PromptArgs& a, const Work& w, int i) {
+  const Row row(a, w, i);
+  if (!row.live) return;
+#pragma unroll 1
   for (int q = 0; q < 4; ++q) {
-    float o[32];
-    if (read) {
-      ld32(to + 32 * q, o);
-      settle(o);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] = empty ? 0.f : o[i] * f;
-    if (ro.poison && row.live && ok) {
-      const uint32_t bits = spoiled(a, w, row0 + lane, q);
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if ((bits >> i) & 1) o[i] = nan;
-    }
-    if (a.n_split > 1) {
-      if (row.live) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<float4*>(part + 4 + 32 * q + 4 * i) =
-              make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-      }
-    } else {
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t u[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) u[e] = pack_bf16(o[8 * i + 2 * e], o[8 * i + 2 * e + 1]);
-        // 16-byte chunk i of row r at i ^ (r / 2 % 4): no bank conflicts either way
-        *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
-      }
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {            // eight rows per step, four lanes each
-        const int r = 8 * i + (lane >> 2);
-        if (dst[i]) dst[i][4 * q] = *reinterpret_cast<const uint4*>(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
-      }
+#pragma unroll 1
+    for (uint32_t bits = spoiled(a, w, i, q); bits; bits &= bits - 1) {
+      const int c = 32 * q + __ffs(bits) - 1;
+      if (a.n_split > 1)
+        part_of(a, w, row)[4 + c] = __uint_as_float(0x7FC00000u);
+      else
+        static_cast<uint16_t*>(a.c.out)[row.qrow * 128 + c] = 0x7FC0;
     }
   }
-  if (row.live) {
-    if (a.n_split > 1)
-      part[0] = lse;
-    else if (a.c.lse)
-      a.c.lse[row.qrow] = lse;
+}
+
+// The rows of every item (four warps).  Returns the first item whose rows were not written.
+__device__ __forceinline__ int write_items(const PromptArgs& a, uint32_t tmem, uint8_t* sm, Shared* sh, const Waiter& wait) {
+  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, m = 32 * warp + lane;
+  int keyed = 0, item = 0;
+  for (;; ++item) {
+    const int slot = item & (kItems - 1);
+    if (!__all_sync(0xffffffffu, wait.handed(sh->bars + kItem + slot, (item / kItems) & 1))) break;
+    const Work& w = sh->work[slot];
+    if (w.state == kStop) break;
+    const bool any = w.state == kKeyed;
+#pragma unroll 1
+    for (int tile = 0; tile < 2; ++tile) {
+      const int i = tile * kRows + m;          // this thread's row of the block
+      float f = 0.f;
+      {                                        // before the last products are complete
+        float2 ml = make_float2(kNoRef, 0.f);
+        if (any) {
+          if (!__all_sync(0xffffffffu, wait(sh->bars + kLast + 2 * (keyed & 1) + tile, (keyed >> 1) & 1))) return item;
+          ml = sh->ml[keyed & 1][tile][m];
+        }
+        if (ml.y != 0.f) f = 1.f / ml.y;
+        const Row row(a, w, i);
+        if (row.live) {
+          const float lse = lse_of(ml.x, ml.y);
+          if (a.n_split > 1)
+            *part_of(a, w, row) = lse;
+          else if (a.c.lse)
+            a.c.lse[row.qrow] = lse;
+        }
+      }
+      if (any && !__all_sync(0xffffffffu, wait(sh->bars + kOFull + tile, keyed & 1))) return item;
+      fence_after();
+      write_rows(a, w, tmem + ((uint32_t)(32 * warp) << 16) + 256 + 128 * tile, sm + kOffOut + warp * 4096,
+                 tile * kRows + 32 * warp, any, f, sh->bars + kORead + tile);
+      if (any) {
+        bool poison = (sh->poison[keyed & 1][tile][warp] >> lane) & 1;
+        const int t0 = w.tile(w.i1 - 1) * kKeys;
+        if (in_part(a, w, t0)) poison |= poisoned(a, w, sh, i, t0, sh->end[keyed & 1].x, sh->end[keyed & 1].y);
+        if (poison) spoil_row(a, w, i);
+      }
+    }
+    if (any) ++keyed;
+    __syncwarp();
+    if (lane == 0) arrive(sh->bars + kFree + slot);
   }
+  return item;
 }
 
 // Rows of items that a CTA took on and did not get to before it gave up: not a number (in a
 // split, the row's part: the join would read what the workspace held before).  first: the
 // first item whose rows this warp has not written.
 __device__ __forceinline__ void abandon(const PromptArgs& a, const Shared* sh, int first) {
-  const int i = threadIdx.x, given = sh->given;   // this thread's row of a block
+  const int given = sh->given;
   const float nan = __uint_as_float(0x7FC00000u);
 #pragma unroll 1
   for (int item = first; item <= given; ++item) {
@@ -676,15 +797,18 @@ __device__ __forceinline__ void abandon(const PromptArgs& a, const Shared* sh, i
     else if (sh->taken < 0 || !find_work(a, sh->taken, w))
       return;
     if (w.state == kStop) return;
-    const Row row(a, w, i);
-    if (!row.live) continue;
-    if (a.n_split > 1) {
-      static_cast<float*>(a.c.ws)[((((size_t)w.s * a.c.max_q + row.token) * a.Hq + row.hq) * a.n_split + w.split) * kPart] = nan;
-    } else {
-      uint4* out = static_cast<uint4*>(a.c.out) + row.qrow * 16;
 #pragma unroll 1
-      for (int c = 0; c < 16; ++c) out[c] = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
-      if (a.c.lse) a.c.lse[row.qrow] = nan;
+    for (int tile = 0; tile < 2; ++tile) {     // this thread's rows
+      const Row row(a, w, tile * kRows + (threadIdx.x & 127));
+      if (!row.live) continue;
+      if (a.n_split > 1) {
+        *part_of(a, w, row) = nan;
+      } else {
+        uint4* out = static_cast<uint4*>(a.c.out) + row.qrow * 16;
+#pragma unroll 1
+        for (int c = 0; c < 16; ++c) out[c] = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+        if (a.c.lse) a.c.lse[row.qrow] = nan;
+      }
     }
   }
 }
@@ -699,24 +823,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   release_successor();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(sh->bars + kKFull + i, 1);
-      mbar_init(sh->bars + kKEmpty + i, 1);
-      mbar_init(sh->bars + kVLand + i, 1);
-      mbar_init(sh->bars + kVFull + i, 4);
-      mbar_init(sh->bars + kVEmpty + i, 1);
+      mbar_init(sh->bars + kData + i, 1);
+      mbar_init(sh->bars + kEmpty + i, 1);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(sh->bars + kGo + i, 4 + 1);    // softmax warps, looking warp
+      mbar_init(sh->bars + kGo + kRing + i, 4);
+      mbar_init(sh->bars + kLooked + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sh->bars + kQFull + i, 1);
       mbar_init(sh->bars + kQEmpty + i, 1);
-      mbar_init(sh->bars + kSFull + i, 2);
-      mbar_init(sh->bars + kPFull + i, 4);
-      mbar_init(sh->bars + kOFull + i, 2);
+      mbar_init(sh->bars + kSFull + i, 1);
+      mbar_init(sh->bars + kOFull + i, 1);
+      mbar_init(sh->bars + kORead + i, 4);
+      mbar_init(sh->bars + kLast + i, 4);      // of odd and even items: the softmax may be one ahead of the rows
+      mbar_init(sh->bars + kLast + 2 + i, 4);
     }
+    mbar_init(sh->bars + kFirst, 1);
     mbar_init(sh->bars + kDrain, 1);
     mbar_init(sh->bars + kCancel, 1);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(sh->bars + kItem + i, 1);
-      mbar_init(sh->bars + kFree + i, 2 * kRows + 6);   // softmax threads, four looking warps, loader, issuer
+      mbar_init(sh->bars + kFree + i, 8 + 4 + 3);       // softmax, writing warps, loader, issuer, looking warp
     }
     mbar_fence_init();
     sh->abort = 0;
@@ -738,46 +867,47 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Waiter wait{&sh->abort, a.polls, &sh->steps};
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    const int tile = warp >> 2;
+    const int tile = warp >> 2, lane = threadIdx.x & 31;
     const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const int m0 = 32 * (warp & 3);            // this warp's rows of the tile
-    int g = 0, keyed = 0, item = 0;
-    for (;; ++item) {
+    int g = 0, parts = 0, keyed = 0;
+    for (int item = 0;; ++item) {
       const int slot = item & (kItems - 1);
       if (!__all_sync(0xffffffffu, wait.handed(sh->bars + kItem + slot, (item / kItems) & 1))) break;
       const Work& w = sh->work[slot];
       if (w.state == kStop) break;
-      RowOut ro;
-      bool ok = true;
       if (w.state == kKeyed) {
-        ok = softmax_rows(a, w, trow, tile, sh, wait, g, ro);
-        if (ok) ok = __all_sync(0xffffffffu, wait(sh->bars + kOFull + tile, keyed & 1)) != 0;
-        fence_after();
-        const int t0 = w.tile(w.i1 - 1) * kKeys;
-        if (ok && in_part(a, w, t0)) ro.poison |= poisoned(a, w, sh, tile * kRows + (threadIdx.x & 127), t0, g);
+        RowOut ro;
+        if (!softmax_rows(a, w, trow, tile, sh, wait, g, parts, ro)) break;
+        sh->ml[keyed & 1][tile][threadIdx.x & 127] = make_float2(ro.M, ro.l);
+        const uint32_t poison = __ballot_sync(0xffffffffu, ro.poison);
+        if (lane == 0) {
+          sh->poison[keyed & 1][tile][warp & 3] = poison;
+          if (warp == 0) sh->end[keyed & 1] = make_int2(g, parts - 1);
+        }
+        __syncwarp();
+        if (lane == 0) arrive(sh->bars + kLast + 2 * (keyed & 1) + tile);
         ++g;
         ++keyed;
       }
-      write_row(a, w, trow + 256 + 128 * tile, sm + kOffOut + warp * 2048, tile * kRows + m0, w.state == kKeyed, ok, ro);
-      arrive(sh->bars + kFree + slot);
-      if (!ok) {
-        ++item;
-        break;
-      }
+      if (lane == 0) arrive(sh->bars + kFree + slot);
+      __syncwarp();
     }
-    if ((threadIdx.x & 31) == 0) sh->next[warp] = item;   // kept there: held in a register to the end it costs spills
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp < 12) look_through(a, sm, sh, wait);
-    if (warp == 12) issue_products(__shfl_sync(0xffffffffu, tmem, 0), sm, sh, wait);
-    if (warp == 13) walk(a, sh, wait);
+    if (warp < 12) {
+      const int next = write_items(a, tmem, sm, sh, wait);
+      if ((threadIdx.x & 31) == 0) sh->next[warp - 8] = next;
+    }
+    if (warp == 12) issue_products(a, __shfl_sync(0xffffffffu, tmem, 0), sm, sh, wait);
+    if (warp == 13) walk(a, &mq, sh, wait);
     if (warp == 14) load_tiles(a, {&mq, &mk, &mv}, sm, sh, wait);
+    if (warp == 15) look_through(a, sm, sh, wait);
   }
   __syncwarp();
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp < 8 && sh->abort) abandon(a, sh, sh->next[warp]);
+  if (warp >= 8 && warp < 12 && sh->abort) abandon(a, sh, sh->next[warp - 8]);
   if (warp == 12) {
     if (sh->abort) {                           // products may be in flight: wait (bounded) before giving back the memory
       if (elect_one()) {                       // the lane that issued them

@@ -47,6 +47,18 @@ __device__ __forceinline__ void ld32(uint32_t t, float* v) {
       : "r"(t)
       : "memory");
 }
+// 16 columns
+__device__ __forceinline__ void ld16(uint32_t t, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(t)
+      : "memory");
+}
+__device__ __forceinline__ void settle16(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : KV_TIE8(v, 0), KV_TIE8(v, 8) : : "memory");
+}
 // no use of the values moves above the wait
 __device__ __forceinline__ void settle(float* v) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
