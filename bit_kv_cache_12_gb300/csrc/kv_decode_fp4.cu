@@ -26,10 +26,12 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 4;                     // 2304-byte tiles in flight per warp
+constexpr int kUnit = 2 * kTile;               // tokens of a step: two tiles
+constexpr uint32_t kUnitBytes = 2 * kFp4TileBytes;
+constexpr int kStages = 3;                     // units in flight per warp
 constexpr int kPolls = 1 << 18;                // bound of a copy's wait: a poll suspends for up to 3.7 us, so about a second
 constexpr float kRaise = 7.f, kHead = 3.f;     // M moves when x > M + 7, to the largest x - 3
-constexpr uint32_t kRing = kWarps * kStages * kFp4TileBytes;
+constexpr uint32_t kRing = kWarps * kStages * kUnitBytes;
 constexpr uint32_t kSmem = kRing + kWarps * kStages * 8;
 // Results of the warps in shared memory (over the ring): heads 136 floats apart, so that a
 // half warp's pairs of channels fall into different banks.
@@ -48,6 +50,26 @@ struct DecodeFp4Args {
   int cluster;                                 // the splits of a pair are a cluster
 };
 
+// The units a query at position n - 1 sees: the first `ns`, then those from w0 on.
+struct Units {
+  int n, low, sinks, ns, w0, total;
+  __device__ __forceinline__ Units(int len, int window, int n_sink) {
+    n = len;
+    low = window ? max(len - window, 0) : 0;
+    sinks = window ? min(n_sink, len) : 0;
+    w0 = low / kUnit;
+    ns = min((sinks + kUnit - 1) / kUnit, w0);
+    total = ns + (len + kUnit - 1) / kUnit - w0;
+  }
+  __device__ __forceinline__ int unit(int i) const { return i < ns ? i : i - ns + w0; }
+  // bit t: token t of the unit is visible
+  __device__ __forceinline__ uint32_t mask(int unit) const {
+    const int t0 = unit * kUnit;
+    auto below = [&](int j) { return j <= t0 ? 0u : (j - t0 >= kUnit ? 0xFFFFFFFFu : (1u << (j - t0)) - 1u); };
+    return below(n) & (~below(low) | below(sinks));
+  }
+};
+
 // The four code pairs of a word as fp16 pairs.
 __device__ __forceinline__ void codes4(uint32_t w, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
   asm("{ .reg .b8 p, q, r, s; mov.b32 {p, q, r, s}, %4; cvt.rn.f16x2.e2m1x2 %0, p; cvt.rn.f16x2.e2m1x2 %1, q; "
@@ -61,7 +83,7 @@ template <int G>
 __global__ void __launch_bounds__(kThreads, 2) decode_fp4_kernel(DecodeFp4Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
-  uint8_t* ring = smem + warp * kStages * kFp4TileBytes;
+  uint8_t* ring = smem + warp * kStages * kUnitBytes;
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + kRing) + warp * kStages;
   if (lane < kStages) mbar_init(bar + lane, 1);
   mbar_fence_init();
@@ -87,47 +109,61 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp4_kernel(DecodeFp4Args a
     if (split == 0 && threadIdx.x == 0) flag_error(a.err, KV_DEVERR_LENGTH);
     n = min(max(n, 0), a.c.max_len);
   }
-  const Span sp(n, a.c.window, a.c.n_sink);
-  const int per = (sp.total + a.n_split - 1) / a.n_split;
-  const int i0 = split * per, count = max(min(per, sp.total - i0), 0);
-  const int mine = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;   // tiles i0 + warp, + kWarps, ..
-  const int tpp = a.L.P / kTile, tpp_shift = tpp >> 1;
+  const Units un(n, a.c.window, a.c.n_sink);
+  const int per = (un.total + a.n_split - 1) / a.n_split;
+  const int i0 = split * per, count = max(min(per, un.total - i0), 0);
+  const int mine = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;   // units i0 + warp, + kWarps, ..
   const int32_t* pt = a.c.pt + (size_t)b * a.c.max_pages;
+  const bool wide = a.L.P == kUnit;            // a unit is a page, not two
 
-  // The warp's k-th tile: its page id is read a batch of 32 tiles ahead and not looked at
-  // before its turn (no load below waits for another where it is issued).
-  auto page_of = [&](int k) -> int {
-    return pt[k < mine ? sp.tile(i0 + warp + k * kWarps) >> tpp_shift : 0];
+  // The warp's k-th unit: what is visible of it, and the stored index of its tiles (below
+  // 2^31: 2304 bytes each; -1: not visible, or behind a bad page id).  Page ids are read a
+  // batch of 32 units ahead and not looked at before their turn (no load below waits for
+  // another where it is issued); those of hidden tiles are not looked at at all.
+  struct Batch {
+    uint32_t vis;
+    int pid0, pid1;
   };
-  auto stored = [&](int k, int pid) -> long long {   // -1: no such tile, or behind a bad page id
-    if (k >= mine) return -1;
+  auto batch_of = [&](int k) -> Batch {
+    Batch x;
+    const int u = un.unit(i0 + warp + k * kWarps);
+    x.vis = k < mine ? un.mask(u) : 0u;
+    x.pid0 = pt[x.vis & 0xFFFFu ? (wide ? u : 2 * u) : 0];
+    x.pid1 = pt[x.vis >> 16 ? (wide ? u : 2 * u + 1) : 0];
+    return x;
+  };
+  auto tile_of = [&](uint32_t vis, int pid, int second) -> int {
+    if (!vis) return -1;
     if (pid < 0 || pid >= a.L.num_pages) {
       flag_error(a.err, KV_DEVERR_PAGE_ID);
       return -1;
     }
-    return ((long long)pid * a.L.Hkv + h) * tpp + (sp.tile(i0 + warp + k * kWarps) & (tpp - 1));
+    const int t = pid * a.L.Hkv + h;
+    return wide ? 2 * t + second : t;
   };
   const uint64_t policy = l2_evict_first_policy();
-  auto issue = [&](int stage, long long t) {     // lane 0
-    if (t < 0) {
-      mbar_expect_tx(bar + stage, 0);
-    } else {
-      mbar_expect_tx(bar + stage, kFp4TileBytes);
-      bulk_g2s_hint(ring + stage * kFp4TileBytes, a.L.tiles + t * kFp4TileBytes, kFp4TileBytes, bar + stage, policy);
-    }
+  auto issue = [&](int stage, int t0, int t1) {  // lane 0
+    uint8_t* to = ring + stage * kUnitBytes;
+    mbar_expect_tx(bar + stage, (t0 >= 0 ? kFp4TileBytes : 0) + (t1 >= 0 ? kFp4TileBytes : 0));
+    if (t0 >= 0) bulk_g2s_hint(to, a.L.tiles + (size_t)t0 * kFp4TileBytes, kFp4TileBytes, bar + stage, policy);
+    if (t1 >= 0)
+      bulk_g2s_hint(to + kFp4TileBytes, a.L.tiles + (size_t)t1 * kFp4TileBytes, kFp4TileBytes, bar + stage, policy);
   };
-  // lane l knows the l-th tile of the current 32 and the page id of the next
-  const int pid0 = page_of(lane);
-  int next_pid = page_of(32 + lane);
-  long long cur = stored(lane, pid0), next = -1;
+  // lane l knows the l-th unit of the current 32 and the page ids of the next
+  Batch ahead = batch_of(lane);
+  int cur0 = tile_of(ahead.vis & 0xFFFFu, ahead.pid0, 0), cur1 = tile_of(ahead.vis >> 16, ahead.pid1, 1);
+  uint32_t vis_now = ahead.vis & ((cur0 >= 0 ? 0xFFFFu : 0u) | (cur1 >= 0 ? 0xFFFF0000u : 0u)), whole = 0;
+  int next0 = -1, next1 = -1;
+  uint32_t vis_next = 0;
+  ahead = batch_of(32 + lane);
 #pragma unroll
   for (int k = 0; k < kStages; ++k) {
-    const long long t = __shfl_sync(0xffffffffu, cur, k);
+    const int t0 = __shfl_sync(0xffffffffu, cur0, k), t1 = __shfl_sync(0xffffffffu, cur1, k);
     if (lane != 0 || k >= mine) continue;
     if (a.stall && k == 0 && blockIdx.x == 0 && warp == 0)
       mbar_expect_tx(bar, kFp4TileBytes);
     else
-      issue(k, t);
+      issue(k, t0, t1);
   }
 
   // q as the B operand: scaled per head by a power of two, fp16
@@ -161,32 +197,35 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp4_kernel(DecodeFp4Args a
   int k = 0, stage = 0, phase = 0;
   for (; k < mine; ++k) {
     if ((k & 31) == 0) {                       // the next 32: their page ids have been on the way since the last batch
-      if (k) cur = next;
-      next = stored(k + 32 + lane, next_pid);
-      next_pid = page_of(k + 64 + lane);
+      if (k) {
+        cur0 = next0;
+        cur1 = next1;
+        vis_now = vis_next;
+      }
+      next0 = tile_of(ahead.vis & 0xFFFFu, ahead.pid0, 0);
+      next1 = tile_of(ahead.vis >> 16, ahead.pid1, 1);
+      vis_next = ahead.vis & ((next0 >= 0 ? 0xFFFFu : 0u) | (next1 >= 0 ? 0xFFFF0000u : 0u));
+      ahead = batch_of(k + 64 + lane);
+      whole = __ballot_sync(0xffffffffu, vis_now == 0xFFFFFFFFu);
     }
     // the lanes vote: a copy that lands just as the limit runs out must not part them
     if (!__all_sync(0xffffffffu, mbar_wait(bar + stage, phase, a.polls))) {
       ok = false;
       break;
     }
-    const bool have = __shfl_sync(0xffffffffu, (int)(cur >= 0), k & 31);
-    if (have) {
-      const int tile = sp.tile(i0 + warp + k * kWarps);
-      const uint32_t vis = sp.mask(tile);
-      const uint8_t* st = ring + stage * kFp4TileBytes;
-      const uint4 ka = *reinterpret_cast<const uint4*>(st + r * 64 + j * 16);
-      const uint4 kb = *reinterpret_cast<const uint4*>(st + (r + 8) * 64 + j * 16);
-      const uint32_t sa2 = cvt_lo(*reinterpret_cast<const uint16_t*>(st + kFp4KScale + r * 8 + j * 2));
-      const uint32_t sb2 = cvt_lo(*reinterpret_cast<const uint16_t*>(st + kFp4KScale + (r + 8) * 8 + j * 2));
-      const uint4 va = *reinterpret_cast<const uint4*>(st + kFp4V + lane * 16);
-      const uint4 vb = *reinterpret_cast<const uint4*>(st + kFp4V + 512 + lane * 16);
-      uint4 ga = *reinterpret_cast<const uint4*>(st + kFp4VScale + j * 32);
-      uint4 gb = *reinterpret_cast<const uint4*>(st + kFp4VScale + j * 32 + 16);
+    const uint8_t* st = ring + stage * kUnitBytes;
+    float x[2][4];                             // per tile: token r heads 2j, 2j + 1, then token r + 8
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint8_t* tile = st + t * kFp4TileBytes;
+      const uint4 ka = *reinterpret_cast<const uint4*>(tile + r * 64 + j * 16);
+      const uint4 kb = *reinterpret_cast<const uint4*>(tile + (r + 8) * 64 + j * 16);
+      const uint32_t sa = cvt_lo(*reinterpret_cast<const uint16_t*>(tile + kFp4KScale + r * 8 + j * 2));
+      const uint32_t sb = cvt_lo(*reinterpret_cast<const uint16_t*>(tile + kFp4KScale + (r + 8) * 8 + j * 2));
       float acc[2][4] = {};
 #pragma unroll
       for (int half = 0; half < 2; ++half) {   // channels 32 j + 16 half ..: one scale for each token
-        const uint32_t ma = __byte_perm(sa2, sa2, half ? 0x3232 : 0x1010), mb = __byte_perm(sb2, sb2, half ? 0x3232 : 0x1010);
+        const uint32_t ma = __byte_perm(sa, sa, half ? 0x3232 : 0x1010), mb = __byte_perm(sb, sb, half ? 0x3232 : 0x1010);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           uint32_t a0, a2, a4, a6, a1, a3, a5, a7;
@@ -197,53 +236,75 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp4_kernel(DecodeFp4Args a
           mma_f16(acc[half], mul2(a4, ma), mul2(a5, mb), mul2(a6, ma), mul2(a7, mb), qf[2 * s + 2], qf[2 * s + 3]);
         }
       }
-      float x0 = (acc[0][0] + acc[1][0]) * cs0, x1 = (acc[0][1] + acc[1][1]) * cs1;   // token r, heads 2j, 2j + 1
-      float x2 = (acc[0][2] + acc[1][2]) * cs0, x3 = (acc[0][3] + acc[1][3]) * cs1;   // token r + 8
-      if (vis != 0xFFFFu) {                    // hidden tokens: no weight, and scales of zero
-        if (!((vis >> r) & 1)) x0 = x1 = -INFINITY;
-        if (!((vis >> (r + 8)) & 1)) x2 = x3 = -INFINITY;
-        const uint32_t lo = (vis >> (2 * j)) & 3u, hi = (vis >> (2 * j + 8)) & 3u;
-        const uint32_t keep = (lo & 1 ? 0xFFu : 0u) | (lo & 2 ? 0xFF00u : 0u) | (hi & 1 ? 0xFF0000u : 0u) |
-                              (hi & 2 ? 0xFF000000u : 0u);
-        ga.x &= keep, ga.y &= keep, ga.z &= keep, ga.w &= keep;
-        gb.x &= keep, gb.y &= keep, gb.z &= keep, gb.w &= keep;
-      }
-      // as differences: where M is large, M + 7 is rounded by as much as that
-      float d0 = x0 - M0, d1 = x1 - M1, d2 = x2 - M0, d3 = x3 - M1;
-      if (__any_sync(0xffffffffu, fmaxf(fmaxf(d0, d2), fmaxf(d1, d3)) > kRaise)) {
-        const float t0 = warp_max_xor(fmaxf(x0, x2), 4), t1 = warp_max_xor(fmaxf(x1, x3), 4);
-        const float n0 = t0 - M0 > kRaise ? t0 - kHead : M0, n1 = t1 - M1 > kRaise ? t1 - kHead : M1;
-        const float f0 = exp2_neg(M0 - n0), f1 = exp2_neg(M1 - n1);
-        M0 = n0;
-        M1 = n1;
-        l0 *= f0;
-        l1 *= f1;
+      x[t][0] = (acc[0][0] + acc[1][0]) * cs0;
+      x[t][1] = (acc[0][1] + acc[1][1]) * cs1;
+      x[t][2] = (acc[0][2] + acc[1][2]) * cs0;
+      x[t][3] = (acc[0][3] + acc[1][3]) * cs1;
+    }
+    uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+    if (!((whole >> (k & 31)) & 1)) {          // hidden tokens: no weight, and scales of zero
+      const uint32_t vis = __shfl_sync(0xffffffffu, vis_now, k & 31);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          o[i][0] *= f0;
-          o[i][1] *= f1;
-          o[i][2] *= f0;
-          o[i][3] *= f1;
-        }
-        d0 = x0 - M0, d1 = x1 - M1, d2 = x2 - M0, d3 = x3 - M1;
+      for (int t = 0; t < 2; ++t) {
+        const uint32_t v = vis >> (16 * t);
+        if (!((v >> r) & 1)) x[t][0] = x[t][1] = -INFINITY;
+        if (!((v >> (r + 8)) & 1)) x[t][2] = x[t][3] = -INFINITY;
+        const uint32_t lo = (v >> (2 * j)) & 3u, hi = (v >> (2 * j + 8)) & 3u;
+        keep[t] = (lo & 1 ? 0xFFu : 0u) | (lo & 2 ? 0xFF00u : 0u) | (hi & 1 ? 0xFF0000u : 0u) | (hi & 2 ? 0xFF000000u : 0u);
       }
-      const float w0 = exp2_neg(d0), w1 = exp2_neg(d1), w2 = exp2_neg(d2), w3 = exp2_neg(d3);
+    }
+    // as differences: where M is large, M + 7 is rounded by as much as that
+    const float t0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
+    const float t1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
+    if (__any_sync(0xffffffffu, fmaxf(t0 - M0, t1 - M1) > kRaise)) {
+      const float u0 = warp_max_xor(t0, 4), u1 = warp_max_xor(t1, 4);
+      const float n0 = u0 - M0 > kRaise ? u0 - kHead : M0, n1 = u1 - M1 > kRaise ? u1 - kHead : M1;
+      const float f0 = exp2_neg(M0 - n0), f1 = exp2_neg(M1 - n1);
+      M0 = n0;
+      M1 = n1;
+      l0 *= f0;
+      l1 *= f1;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        o[i][0] *= f0;
+        o[i][1] *= f1;
+        o[i][2] *= f0;
+        o[i][3] *= f1;
+      }
+    }
+    uint32_t p[2][2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const float w0 = exp2_neg(x[t][0] - M0), w1 = exp2_neg(x[t][1] - M1);
+      const float w2 = exp2_neg(x[t][2] - M0), w3 = exp2_neg(x[t][3] - M1);
       l0 += w0 + w2;
       l1 += w1 + w3;
-      const uint32_t p0 = movmatrix_t(pack_f16(w0, w1)), p1 = movmatrix_t(pack_f16(w2, w3));
+      p[t][0] = movmatrix_t(pack_f16(w0, w1));
+      p[t][1] = movmatrix_t(pack_f16(w2, w3));
+    }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {            // block i of channels: 16 i + 2 r, 16 i + 2 r + 1
-        uint32_t v0, v1, v2, v3;
-        codes4(i < 4 ? (&va.x)[i] : (&vb.x)[i - 4], v0, v1, v2, v3);
-        const uint32_t g = i < 4 ? (&ga.x)[i] : (&gb.x)[i - 4];
-        mma_f16(o[i], v0, v1, v2, v3, mul2(p0, cvt_lo(g)), mul2(p1, cvt_hi(g)));
+    for (int t = 0; t < 2; ++t) {
+      const uint8_t* tile = st + t * kFp4TileBytes;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {            // blocks 4 q ..: channels 16 i + 2 r, 16 i + 2 r + 1 of block i
+        const uint4 v = *reinterpret_cast<const uint4*>(tile + kFp4V + 512 * q + lane * 16);
+        const uint4 g = *reinterpret_cast<const uint4*>(tile + kFp4VScale + j * 32 + 16 * q);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t v0, v1, v2, v3;
+          codes4((&v.x)[w], v0, v1, v2, v3);
+          const uint32_t s = (&g.x)[w] & keep[t];
+          mma_f16(o[4 * q + w], v0, v1, v2, v3, mul2(p[t][0], cvt_lo(s)), mul2(p[t][1], cvt_hi(s)));
+        }
       }
     }
     __syncwarp();
     const int kn = k + kStages;
     if (kn < mine) {
-      const long long t = __shfl_sync(0xffffffffu, (kn >> 5) == (k >> 5) ? cur : next, kn & 31);
-      if (lane == 0) issue(stage, t);
+      const bool same = (kn >> 5) == (k >> 5);
+      const int u0 = __shfl_sync(0xffffffffu, same ? cur0 : next0, kn & 31);
+      const int u1 = __shfl_sync(0xffffffffu, same ? cur1 : next1, kn & 31);
+      if (lane == 0) issue(stage, u0, u1);
     }
     if (++stage == kStages) {
       stage = 0;
