@@ -703,12 +703,14 @@ kv_status_t kv_decode_attention_fp4(kv_pool_t* pool, int32_t layer, int32_t B, c
       st != KV_OK)
     return st;
   const Pool& p = pool->p;
-  if (workspace_bytes < kvint2::decode_fp4_workspace(p, B, max_seq_len)) return KV_ERR_INVALID_ARG;
+  const int seen = kvint2::effective_window(window, max_seq_len);
+  const int splits = kvint2::decode_fp4_splits(p, B, max_seq_len, seen, n_sink);
+  if (workspace_bytes < kvint2::decode_fp4_workspace(p, B, splits)) return KV_ERR_INVALID_ARG;
   if (kv_status_t st = on_pool_device(p); st != KV_OK) return st;
   return cuda_status(kvint2::launch_decode_fp4(p, kvint2::fp4_layer(p, pool->fp4, pool->range[layer], layer), layer, B,
+                                               splits,
                                                {q, seq_len, page_table, max_pages_per_seq, max_seq_len, softmax_scale,
-                                                kvint2::effective_window(window, max_seq_len), n_sink, out, lse,
-                                                workspace},
+                                                seen, n_sink, out, lse, workspace},
                                                static_cast<cudaStream_t>(stream)));
 }
 

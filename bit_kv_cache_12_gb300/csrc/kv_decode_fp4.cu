@@ -354,20 +354,28 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp4_kernel(DecodeFp4Args a
                                      [](int c) { return c; });
 }
 
-// Splits per (sequence, KV head), from the host's bound on visible tiles: none up to two
-// tiles per warp; else a tile per warp at least, at most one wave of one CTA per SM where
-// pairs are few, two per SM where that would leave SMs idle, and about six waves for more
-// pairs, so that sequences of different lengths even out.  Where a cluster's worth of
-// splits has up to two tiles per warp: no more than those.
-int splits(const Pool& p, int B, long long max_len, int window, int n_sink) {
-  long long tokens = max_len;
-  if (window) tokens = std::min(tokens, (long long)window + n_sink + 2 * kTile);
-  const long long tiles = (tokens + kTile - 1) / kTile, pairs = (long long)B * p.cfg.num_kv_heads, sms = p.sm_count;
-  const long long want = sms >= 4 * pairs ? sms / pairs : (pairs <= sms ? 2 * sms / pairs : (12 * sms + pairs - 1) / pairs);
-  if (tiles <= 2 * kWarps) return 1;
-  const long long most = std::min<long long>((tiles + kWarps - 1) / kWarps, kMaxSplits);
-  const long long n = std::max(1ll, std::min(want, most));
-  return (int)(tiles <= 2 * kMaxCluster * kWarps ? std::min<long long>(n, kMaxCluster) : n);
+// Microseconds that a call takes with each (sequence, KV head) pair in n splits of `units`
+// units, as far as they depend on n.  A warp takes 0.62 us for a unit where an SM has one
+// CTA and 0.88 where it has two (measured by graph replay: 8 pairs of 100,000 tokens in 19
+// splits, one CTA per SM, 28.2 us; in 38, two, 27.6).  Up to two CTAs per SM all run at
+// once; more come in waves, with 2.1 us for the start and end of each and an uneven last
+// one (512 pairs of 20,480 tokens: 263 us in one split, 247 in two, 255 in three; of 8,192:
+// 110, 115 and 120).  A join inside a cluster (up to 8 splits) costs 1 us, through memory
+// 0.1 and 0.13 for each split (1024 tokens of 2 pairs: 5.0 us in 8 splits, 6.9 in 9, 7.1 in
+// one).  What the largest length of a batch costs, so that shorter ones are even with it.
+double cost_of(const Pool& p, long long pairs, long long units, int n) {
+  const long long ctas = pairs * n, sms = p.sm_count;
+  const double steps = (double)(((units + n - 1) / n + kWarps - 1) / kWarps);
+  const double join = n == 1 ? 0. : (n <= kMaxCluster ? 1. : 0.1 + 0.13 * n);
+  if (ctas <= sms) return join + 0.62 * steps;
+  if (ctas <= 2 * sms) return join + 0.88 * steps;
+  return join + (double)ctas / (2 * sms) * (0.88 * steps + 2.1) + 0.21 * steps;
+}
+
+// More than one split only up to so many CTAs: what the workspace is sized by.
+long long most_ctas(const Pool& p) { return 16ll * p.sm_count; }
+int most_splits(const Pool& p, long long pairs, long long units) {
+  return (int)std::max(1ll, std::min<long long>({kMaxSplits, units, most_ctas(p) / pairs}));
 }
 
 template <int G>
@@ -385,20 +393,37 @@ cudaError_t launch_t(const DecodeFp4Args& a, int device, cudaStream_t s) {
 
 }  // namespace
 
-size_t decode_fp4_workspace(const Pool& p, int B, int max_len) {
-  const int n = splits(p, B, max_len, 0, 0);
-  return n == 1 ? 16 : (size_t)B * p.cfg.num_q_heads * n * kPart * sizeof(float);
+// From the host's bound on visible tokens.
+int decode_fp4_splits(const Pool& p, int B, int max_len, int window, int n_sink) {
+  long long tokens = max_len;
+  if (window) tokens = std::min(tokens, (long long)window + n_sink + 2 * kUnit);
+  const long long units = (tokens + kUnit - 1) / kUnit, pairs = (long long)B * p.cfg.num_kv_heads;
+  int best = 1;
+  double least = cost_of(p, pairs, units, 1);
+  for (int n = 2, most = most_splits(p, pairs, units); n <= most; ++n) {
+    const double c = cost_of(p, pairs, units, n);
+    if (c < least) {
+      least = c;
+      best = n;
+    }
+  }
+  return best;
 }
 
-// Fewer sequences are split further: the most that any batch up to B needs.
+size_t decode_fp4_workspace(const Pool& p, int B, int n_split) {
+  return n_split == 1 ? 16 : (size_t)B * p.cfg.num_q_heads * n_split * kPart * sizeof(float);
+}
+
+// What any call needs of up to B sequences of up to max_len tokens, whatever its window.
 size_t decode_fp4_workspace_up_to(const Pool& p, int B, int max_len) {
-  size_t most = 0;
-  for (int b = 1; b <= B; ++b) most = std::max(most, decode_fp4_workspace(p, b, max_len));
-  return most;
+  const long long units = ((long long)max_len + kUnit - 1) / kUnit, pairs = (long long)B * p.cfg.num_kv_heads;
+  const long long parts = std::min(most_ctas(p), pairs * std::min<long long>(kMaxSplits, units));
+  return std::max<size_t>(16, (size_t)parts * p.G * kPart * sizeof(float));
 }
 
-cudaError_t launch_decode_fp4(const Pool& p, const Fp4Layer& L, int layer, int B, const AttnCall& c, cudaStream_t s) {
-  DecodeFp4Args a{L, c, B, p.cfg.num_q_heads, splits(p, B, c.max_len, c.window, c.n_sink),
+cudaError_t launch_decode_fp4(const Pool& p, const Fp4Layer& L, int layer, int B, int n_split, const AttnCall& c,
+                              cudaStream_t s) {
+  DecodeFp4Args a{L, c, B, p.cfg.num_q_heads, n_split,
                   p.tickets + (size_t)layer * p.cfg.max_seqs * p.cfg.num_kv_heads, p.err,
                   p.test_wait_polls > 0 ? p.test_wait_polls : kPolls, p.test_stall_first_copy};
   switch (p.G) {

@@ -54,9 +54,13 @@ struct Fp4Rows {                      // k and v rows, strides in elements
 cudaError_t launch_append_fp4(const Pool& p, const Fp4Layer& L, const Fp4Tokens& t, const Fp4Rows& in, cudaStream_t s);
 cudaError_t launch_read_fp4(const Pool& p, const Fp4Layer& L, const Fp4Tokens& t, const Fp4Rows& out, cudaStream_t s);
 
-size_t decode_fp4_workspace(const Pool& p, int B, int max_len);
+// Splits of each (sequence, KV head), the workspace they need, and what any call up to these
+// bounds needs.
+int decode_fp4_splits(const Pool& p, int B, int max_len, int window, int n_sink);
+size_t decode_fp4_workspace(const Pool& p, int B, int n_split);
 size_t decode_fp4_workspace_up_to(const Pool& p, int B, int max_len);
-cudaError_t launch_decode_fp4(const Pool& p, const Fp4Layer& L, int layer, int B, const AttnCall& c, cudaStream_t s);
+cudaError_t launch_decode_fp4(const Pool& p, const Fp4Layer& L, int layer, int B, int n_split, const AttnCall& c,
+                              cudaStream_t s);
 
 // Attention of packed rows.
 struct PromptCall {
