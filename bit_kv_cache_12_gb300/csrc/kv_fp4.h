@@ -35,7 +35,7 @@ inline Fp4Layer fp4_layer(const Pool& p, const Fp4Store& f, const Fp4Range& r, i
 // Which axis turns each rotated pair of a layer (a kernel parameter).
 struct RopeAxes {
   int n = 1;
-  uint8_t axis[64] = {};
+  alignas(4) uint8_t axis[64] = {};
 };
 cudaError_t launch_rope_axes(const Pool& p, const RopeParams& r, const RopeAxes& x, int n_tokens,
                              const int32_t* positions, int64_t pos_stride, const RopeRows& q, const RopeRows& k,

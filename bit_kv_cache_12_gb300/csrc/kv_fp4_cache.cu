@@ -2,18 +2,20 @@
 //
 // Of a block of 16 channels x of a token (as multiples of 2^e, e the layer's exponent):
 //   s = e4m3(max |x| / 6),  code = e2m1(x / s),  value = code * s * 2^e.
-// Quotients are IEEE ones: the largest magnitude's by division, once per block; x / s by
-// the reciprocal r = fl(1 / s) and one correction,  q = q0 + (x - q0 s) r,  q0 = fl(x r),
-// in paired fp32 instructions.  What counts is that a quotient halfway between two codes
-// comes out exactly, or it would round to the wrong side: q0 misses some of those by a
-// last place (s = 15/8 of a power of two times 1.25), q none.  (x of 8 bits over s of 4 is
-// otherwise at least 2^-9 away from a halfway point.)
+// The codes are those of exact quotients.  max |x| has 8 bits and its product with
+// fl(1 / 6) comes out exactly where the quotient lies halfway between two e4m3 numbers (the
+// constant is off by 2^-25.4, less than half a last place of any such number), and on the
+// right side of it elsewhere.  x / s: with r near 1 / s (to a last place or two),
+//   q0 = fl(x r),  q = q0 + (x - q0 s) r,
+// in paired fp32 instructions; the remainder is exact, so a quotient halfway between two
+// codes comes out exactly, which q0 alone does not give (s = 15/8 of a power of two times
+// 1.25); x of 8 bits over s of 4 is otherwise at least 2^-9 away from a halfway point.
 //
 // Bound: memory traffic (512 B of rows and 144 B stored per token and KV head) for long
 // prompts, latency for single tokens.  A warp owns a (tile, head, tensor): one writer for
-// the bytes that two tokens share, no atomics.  A lane quantizes whole blocks (32 bytes
-// of a row), so no value crosses lanes: four tokens' blocks each, for V the four tokens
-// whose codes share its bytes.
+// the bytes that two tokens share, no atomics.  16 lanes take a token's row, 16 bytes each,
+// so every load and store of rows is of whole lines; two lanes share a block and exchange
+// its maximum.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -58,14 +60,6 @@ __device__ __forceinline__ uint32_t e2m1x8(float a0, float a1, float b0, float b
   return r;
 }
 
-// A block of a row as it comes from memory, and its scale.
-struct Block {
-  uint32_t w[8];                               // 16 bf16 values
-  uint32_t scale;                              // e4m3 byte
-  float s, r;                                  // scale * 2^e and its reciprocal
-  uint64_t ns2, r2;                            // -s, r as pairs
-};
-
 // Read once by this kernel, written perhaps by the one in front, which may have been
 // running when this one came up: not the read-only path.
 __device__ __forceinline__ uint4 ld_once(const void* p) {
@@ -75,46 +69,47 @@ __device__ __forceinline__ uint4 ld_once(const void* p) {
                : "l"(p));
   return v;
 }
-
-__device__ __forceinline__ void load_block(Block& b, const uint16_t* p, bool live) {
-  uint4 x = make_uint4(0, 0, 0, 0), y = x;
-  if (live) {
-    x = ld_once(p);
-    y = ld_once(p + 8);
-  }
-  b.w[0] = x.x; b.w[1] = x.y; b.w[2] = x.z; b.w[3] = x.w;
-  b.w[4] = y.x; b.w[5] = y.y; b.w[6] = y.z; b.w[7] = y.w;
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {   // of bf16 pairs; NaN wins
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
-__device__ __forceinline__ void scale_block(Block& b, int e) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, b.w[i] & 0x7FFF7FFFu);
-  m = max(m & 0xFFFFu, m >> 16);               // the largest magnitude's bits
+// Half a block, eight channels of a token; this lane's neighbour (lane ^ 1) has the other.
+struct Half {
+  uint32_t w[4];                               // bf16 pairs
+  uint32_t scale;                              // the block's, e4m3
+  uint64_t ns2, r2;                            // pairs of -s * 2^e and its reciprocal
+};
+
+// The block's scale, from what both lanes hold.
+__device__ __forceinline__ void scale_block(Half& b, int e) {
+  uint32_t m = larger(larger(b.w[0] & 0x7FFF7FFFu, b.w[1] & 0x7FFF7FFFu), larger(b.w[2] & 0x7FFF7FFFu, b.w[3] & 0x7FFF7FFFu));
+  m = larger(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = larger(m, (m >> 16) | (m << 16)) & 0xFFFFu;   // the largest magnitude's bits
   const float top = bf16lo(m) * pow2i(-e);
-  b.scale = m >= 0x7F80u ? 0x7Fu : __nv_cvt_float_to_fp8(__fdiv_rn(top, 6.f), __NV_SATFINITE, __NV_E4M3);
+  b.scale = m >= 0x7F80u ? 0x7Fu : __nv_cvt_float_to_fp8(top * 0x1.555556p-3f, __NV_SATFINITE, __NV_E4M3);
   const __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b.scale, __NV_E4M3);
-  const float s = __half2float(__half(hr)) * pow2i(e);
-  const bool live = m < 0x7F80u && s > 0.f;
-  b.s = live ? s : 1.f;
-  b.r = live ? __frcp_rn(s) : 0.f;
-  if (!live) {                                 // codes of zero
+  float s = __half2float(__half(hr)) * pow2i(e), r;
+  if (m >= 0x7F80u || b.scale == 0) {          // codes of zero
+    s = 1.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b.w[i] = 0;
-  } else if (top > 6.f * 448.f) {                     // beyond the format's range: cut where the code is the largest anyway
-    const float cut = 7.f * b.s;               // (s = 448 * 2^e: finite)
+    for (int i = 0; i < 4; ++i) b.w[i] = 0;
+  } else if (top > 6.f * 448.f) {              // beyond the format's range: cut where the code is the largest anyway
+    const float cut = 7.f * s;                 // (s = 448 * 2^e: finite)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
       const float x = fminf(fmaxf(bf16lo(b.w[i]), -cut), cut), y = fminf(fmaxf(bf16hi(b.w[i]), -cut), cut);
       b.w[i] = (__float_as_uint(x) >> 16) | (__float_as_uint(y) & 0xFFFF0000u);   // 7 * 448 * 2^e is a bf16 value
     }
   }
-  b.ns2 = f2(-b.s, -b.s);
-  b.r2 = f2(b.r, b.r);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  b.ns2 = f2(-s, -s);
+  b.r2 = f2(r, r);
 }
 
 // The quotients of values 2 i and 2 i + 1.
-__device__ __forceinline__ void quotients(const Block& b, int i, float& q0, float& q1) {
+__device__ __forceinline__ void quotients(const Half& b, int i, float& q0, float& q1) {
   const uint64_t x = f2(bf16lo(b.w[i]), bf16hi(b.w[i])), q = f2_mul(x, b.r2);
   f2_split(f2_fma(f2_fma(q, b.ns2, x), b.r2, q), q0, q1);
 }
@@ -128,17 +123,16 @@ struct Fp4CacheArgs {
 };
 
 // The i-th tile that sequence s's tokens touch: slots [t0, t1) of it, the row of slot 0
-// (rows t0 .. t1 - 1 exist), its stored index without the head.  False where there is
-// nothing to do.
+// (rows t0 .. t1 - 1 exist), its page, as the table has it, and its place there.  False where
+// there is nothing to do.
 struct Place {
-  int t0, t1, sub;
-  long long pid;
+  int t0, t1, pid, sub;
   int64_t row0;
 };
 __device__ __forceinline__ bool find_place(const Fp4CacheArgs& a, int x, Place& p) {
   const int s = x / a.tiles, i = x - s * a.tiles;
-  const int c0 = a.t.cu[s], start = a.t.start[s];
-  int n = a.t.cu[s + 1] - c0;
+  const int c0 = a.t.cu[s], c1 = a.t.cu[s + 1], start = a.t.start[s];
+  int n = c1 - c0;
   const bool first = i == 0 && blockIdx.y == 0 && threadIdx.x == 0;
   if (n < 0 || n > a.t.max_tokens) {
     if (first) flag_error(a.err, KV_DEVERR_SEQ_RANGE);
@@ -149,102 +143,114 @@ __device__ __forceinline__ bool find_place(const Fp4CacheArgs& a, int x, Place& 
     if (first) flag_error(a.err, KV_DEVERR_SEQ_RANGE);
     return false;
   }
-  const long long base = ((long long)(start / kTile) + i) * kTile;   // position of slot 0
-  const long long lo = max(base, (long long)start), hi = min(base + kTile, (long long)start + n);
-  if (lo >= hi) return false;
-  p.t0 = (int)(lo - base);
-  p.t1 = (int)(hi - base);
-  p.row0 = (int64_t)c0 + (base - start);
+  // a position is below 2^31: so is that of slot 0 of its tile, and tiles behind the last are not touched
+  const int tile = start / kTile + i;
+  if (tile > (start + n - 1) / kTile) return false;
+  const int base = tile * kTile;
+  p.t0 = max(start - base, 0);
+  p.t1 = min(start + n - base, kTile);
+  p.row0 = (int64_t)c0 + base - start;
   p.pid = a.t.pt[(size_t)s * a.t.max_pages + base / a.L.P];
-  p.sub = (int)(base / kTile % (a.L.P / kTile));
-  if (p.pid < 0 || p.pid >= a.L.num_pages) {
-    if (blockIdx.y == 0 && threadIdx.x == 0) flag_error(a.err, KV_DEVERR_PAGE_ID);
-    return false;
-  }
+  p.sub = tile & (a.L.P / kTile - 1);
   return true;
 }
+__device__ __forceinline__ bool good_page(const Fp4CacheArgs& a, const Place& p) {
+  if (p.pid >= 0 && p.pid < a.L.num_pages) return true;
+  if (blockIdx.y == 0 && threadIdx.x == 0) flag_error(a.err, KV_DEVERR_PAGE_ID);
+  return false;
+}
 __device__ __forceinline__ uint8_t* tile_of(const Fp4CacheArgs& a, const Place& p, int h) {
-  return a.L.tiles + ((p.pid * a.L.Hkv + h) * (a.L.P / kTile) + p.sub) * kFp4TileBytes;
+  return a.L.tiles + (((size_t)p.pid * a.L.Hkv + h) * (a.L.P / kTile) + p.sub) * kFp4TileBytes;
 }
 
-// K of a tile: lane (t % 4, g) takes block g of tokens t, t + 4, ..
-__device__ __forceinline__ void store_k(const uint16_t* in, int64_t stride, int t0, int t1, int e, uint8_t* tile, int lane) {
-  const int g = lane & 7, t = lane >> 3;
-  Block b[4];
-#pragma unroll
-  for (int u = 0; u < 4; ++u) load_block(b[u], in + (t + 4 * u) * stride + 16 * g, t + 4 * u >= t0 && t + 4 * u < t1);
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    if (t + 4 * u < t0 || t + 4 * u >= t1) continue;
-    scale_block(b[u], e);
-    uint32_t w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float q[8];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) quotients(b[u], 4 * i + k, q[2 * k], q[2 * k + 1]);
-      w[i] = e2m1x8(q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7]);
-    }
-    *reinterpret_cast<uint2*>(tile + 64 * (t + 4 * u) + 8 * g) = make_uint2(w[0], w[1]);
-    tile[kFp4KScale + 8 * (t + 4 * u) + g] = (uint8_t)b[u].scale;
-  }
-}
+// The slot of a tile whose row a lane's u-th load or store of K, of V is of.
+__device__ __forceinline__ int k_slot(int u, int lane) { return 2 * u + (lane >> 4); }
+__device__ __forceinline__ int v_slot(int u, int lane) { return 4 * (u >> 2) + 2 * (lane >> 4) + (u & 1) + 8 * ((u >> 1) & 1); }
 
-// V of a tile: lane (j, g) takes block g of tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9, whose
-// codes share its eight words and whose scales its ninth.
-__device__ __forceinline__ void store_v(const uint16_t* in, int64_t stride, int t0, int t1, int e, uint8_t* tile, int lane) {
-  const int g = lane & 7, j = lane >> 3;
-  Block b[4];
-  uint32_t mine = 0;                           // bytes of the scale word, halves of the code bytes
+// K of a tile; x: this lane's eight pieces of rows.
+__device__ __forceinline__ void store_k(const uint4 (&x)[8], int t0, int t1, int e, uint8_t* tile, int lane) {
+  const int c = lane & 15;
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int t = 2 * j + (u & 1) + 8 * (u >> 1);
-    const bool live = t >= t0 && t < t1;
-    if (live) mine |= 1u << u;
-    load_block(b[u], in + t * stride + 16 * g, live);
-  }
-  if (mine == 0) return;
-  uint32_t scales = 0, byte_mask = 0, code_mask = 0;
+  for (int u = 0; u < 8; ++u) {
+    const int t = k_slot(u, lane);
+    Half b{{x[u].x, x[u].y, x[u].z, x[u].w}};
+    scale_block(b, e);
+    float q[8];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    scale_block(b[u], e);
-    scales |= b[u].scale << (8 * u);
-    if ((mine >> u) & 1) {
-      byte_mask |= 0xFFu << (8 * u);
-      code_mask |= (u & 1 ? 0xF0F0u : 0x0F0Fu) << (16 * (u >> 1));
+    for (int i = 0; i < 4; ++i) quotients(b, i, q[2 * i], q[2 * i + 1]);
+    const uint32_t w = e2m1x8(q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7]);
+    if (t >= t0 && t < t1) {
+      *reinterpret_cast<uint32_t*>(tile + 64 * t + 4 * c) = w;
+      if ((c & 1) == 0) tile[kFp4KScale + 8 * t + (c >> 1)] = (uint8_t)b.scale;
     }
   }
-  uint32_t* sw = reinterpret_cast<uint32_t*>(tile + kFp4VScale + 32 * j + 4 * g);
-  *sw = mine == 15u ? scales : (*sw & ~byte_mask) | (scales & byte_mask);
-  uint32_t* cw = reinterpret_cast<uint32_t*>(tile + kFp4V + 512 * (g >> 2) + 16 * j + 4 * (g & 3));   // 16 words apart
-  uint32_t old[8];
+}
+
+// V of a tile.  Four loads are of the tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9, whose codes share
+// the lane's four words and whose scales share one.
+__device__ __forceinline__ void store_v(const uint4 (&x)[8], int t0, int t1, int e, uint8_t* tile, int lane) {
+  const int c = lane & 15, g = c >> 1;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) old[i] = mine == 15u ? 0u : cw[16 * i];
+  for (int v = 0; v < 2; ++v) {
+    const int j = 2 * v + (lane >> 4);
+    Half b[4];
+    uint32_t scales = 0, byte_mask = 0, code_mask = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {                // channels 2 i, 2 i + 1
-    float q[4][2];
+    for (int u = 0; u < 4; ++u) {
+      const uint4& y = x[4 * v + u];
+      b[u].w[0] = y.x, b[u].w[1] = y.y, b[u].w[2] = y.z, b[u].w[3] = y.w;
+      scale_block(b[u], e);
+      scales |= b[u].scale << (8 * u);
+      const int t = v_slot(4 * v + u, lane);
+      if (t >= t0 && t < t1) {
+        byte_mask |= 0xFFu << (8 * u);
+        code_mask |= (u & 1 ? 0xF0F0u : 0x0F0Fu) << (16 * (u >> 1));
+      }
+    }
+    uint32_t* sw = reinterpret_cast<uint32_t*>(tile + kFp4VScale + 32 * j + 4 * g);
+    uint32_t* cw = reinterpret_cast<uint32_t*>(tile + kFp4V + 512 * (g >> 2) + 256 * (c & 1) + 16 * j + 4 * (g & 3));
+    uint32_t old[4] = {}, os = 0;              // cw: 16 words apart
+    if (byte_mask != 0 && byte_mask != 0xFFFFFFFFu) {
+      os = *sw;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) quotients(b[u], i, q[u][0], q[u][1]);
-    const uint32_t w = e2m1x8(q[0][0], q[1][0], q[0][1], q[1][1], q[2][0], q[3][0], q[2][1], q[3][1]);
-    cw[16 * i] = (old[i] & ~code_mask) | (w & code_mask);
+      for (int i = 0; i < 4; ++i) old[i] = cw[16 * i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float q[4][2];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) quotients(b[u], i, q[u][0], q[u][1]);
+      const uint32_t w = e2m1x8(q[0][0], q[1][0], q[0][1], q[1][1], q[2][0], q[3][0], q[2][1], q[3][1]);
+      if (byte_mask) cw[16 * i] = (old[i] & ~code_mask) | (w & code_mask);
+    }
+    if (byte_mask && (c & 1) == 0) *sw = (os & ~byte_mask) | (scales & byte_mask);
   }
 }
 
-__global__ void __launch_bounds__(kThreads) append_fp4_kernel(Fp4CacheArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) append_fp4_kernel(Fp4CacheArgs a) {
   release_successor();
   after_predecessor();
   Place p;
   if (!find_place(a, blockIdx.x, p)) return;
   const int lane = threadIdx.x & 31;
   for (int u = blockIdx.y * kWarps + (threadIdx.x >> 5); u < 2 * a.L.Hkv; u += gridDim.y * kWarps) {
-    const int v = u >= a.L.Hkv, h = u - (v ? a.L.Hkv : 0);
+    const bool v = u >= a.L.Hkv;
+    const int h = u - (v ? a.L.Hkv : 0);
+    const int64_t stride = v ? a.rows.v_stride : a.rows.k_stride;
+    const uint16_t* in = static_cast<const uint16_t*>(v ? a.rows.v : a.rows.k) + p.row0 * stride + h * 128 + 8 * (lane & 15);
+    uint4 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int t = v ? v_slot(i, lane) : k_slot(i, lane);
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (t >= p.t0 && t < p.t1) x[i] = ld_once(in + t * stride);
+    }
+    if (!good_page(a, p)) return;              // (its id came with the rows)
     uint8_t* tile = tile_of(a, p, h);
     if (v)
-      store_v(static_cast<const uint16_t*>(a.rows.v) + p.row0 * a.rows.v_stride + h * 128, a.rows.v_stride, p.t0, p.t1,
-              a.L.v_exp, tile, lane);
+      store_v(x, p.t0, p.t1, a.L.v_exp, tile, lane);
     else
-      store_k(static_cast<const uint16_t*>(a.rows.k) + p.row0 * a.rows.k_stride + h * 128, a.rows.k_stride, p.t0, p.t1,
-              a.L.k_exp, tile, lane);
+      store_k(x, p.t0, p.t1, a.L.k_exp, tile, lane);
   }
 }
 
@@ -264,72 +270,74 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b, float s) {
   const __nv_bfloat162 y = __floats2bfloat162_rn(a * s, b * s);
   return *reinterpret_cast<const uint32_t*>(&y);
 }
-__device__ __forceinline__ void store_block(uint16_t* p, const uint32_t (&w)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  *reinterpret_cast<uint4*>(p + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-}
 
 __device__ __forceinline__ void load_k(uint16_t* out, int64_t stride, int t0, int t1, int e, const uint8_t* tile, int lane) {
-  const int g = lane & 7, t = lane >> 3;
-  uint2 w[4];
-  uint32_t sc[4];
+  const int c = lane & 15;
+  uint32_t w[8], sc[8];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    w[u] = *reinterpret_cast<const uint2*>(tile + 64 * (t + 4 * u) + 8 * g);
-    sc[u] = tile[kFp4KScale + 8 * (t + 4 * u) + g];
+  for (int u = 0; u < 8; ++u) {
+    const int t = k_slot(u, lane);
+    w[u] = *reinterpret_cast<const uint32_t*>(tile + 64 * t + 4 * c);
+    sc[u] = tile[kFp4KScale + 8 * t + (c >> 1)];
   }
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    if (t + 4 * u < t0 || t + 4 * u >= t1) continue;
+  for (int u = 0; u < 8; ++u) {
+    const int t = k_slot(u, lane);
+    if (t < t0 || t >= t1) continue;
     const float s = scale_of(sc[u], e);
-    uint32_t y[8];
+    uint32_t f[4];
+    codes4(w[u], f);
+    uint32_t y[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t f[4];
-      codes4(i ? w[u].y : w[u].x, f);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 x = __half22float2(u32_as_h2(f[k]));
-        y[4 * i + k] = bf16_pair(x.x, x.y, s);
-      }
+    for (int k = 0; k < 4; ++k) {
+      const float2 x = __half22float2(u32_as_h2(f[k]));
+      y[k] = bf16_pair(x.x, x.y, s);
     }
-    store_block(out + (t + 4 * u) * stride + 16 * g, y);
+    *reinterpret_cast<uint4*>(out + t * stride + 8 * c) = make_uint4(y[0], y[1], y[2], y[3]);
   }
 }
 
 __device__ __forceinline__ void load_v(uint16_t* out, int64_t stride, int t0, int t1, int e, const uint8_t* tile, int lane) {
-  const int g = lane & 7, j = lane >> 3;
-  const uint32_t* cw = reinterpret_cast<const uint32_t*>(tile + kFp4V + 512 * (g >> 2) + 16 * j + 4 * (g & 3));
-  uint32_t w[8];
+  const int c = lane & 15, g = c >> 1;
+  uint32_t w[2][4], sw[2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = cw[16 * i];
-  const uint32_t sw = *reinterpret_cast<const uint32_t*>(tile + kFp4VScale + 32 * j + 4 * g);
+  for (int v = 0; v < 2; ++v) {
+    const int j = 2 * v + (lane >> 4);
+    const uint32_t* cw = reinterpret_cast<const uint32_t*>(tile + kFp4V + 512 * (g >> 2) + 256 * (c & 1) + 16 * j + 4 * (g & 3));
 #pragma unroll
-  for (int hi = 0; hi < 2; ++hi) {             // tokens 2 j + 8 hi, + 1
-    const float s0 = scale_of(sw >> (16 * hi), e), s1 = scale_of(sw >> (16 * hi + 8), e);
-    uint32_t y0[8], y1[8];
+    for (int i = 0; i < 4; ++i) w[v][i] = cw[16 * i];
+    sw[v] = *reinterpret_cast<const uint32_t*>(tile + kFp4VScale + 32 * j + 4 * g);
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {              // channels 2 i, 2 i + 1
-      uint32_t f[4];
-      codes4(w[i], f);
-      const float2 a = __half22float2(u32_as_h2(f[2 * hi])), b = __half22float2(u32_as_h2(f[2 * hi + 1]));
-      y0[i] = bf16_pair(a.x, b.x, s0);
-      y1[i] = bf16_pair(a.y, b.y, s1);
+  for (int v = 0; v < 2; ++v) {
+    uint32_t f[4][4];                          // [channels 2 i, 2 i + 1 of two][two tokens of four]
+#pragma unroll
+    for (int i = 0; i < 4; ++i) codes4(w[v][i], f[i]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int t = v_slot(4 * v + u, lane);
+      if (t < t0 || t >= t1) continue;
+      const float s = scale_of(sw[v] >> (8 * u), e);
+      uint32_t y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 a = __half22float2(u32_as_h2(f[i][2 * (u >> 1)])), b = __half22float2(u32_as_h2(f[i][2 * (u >> 1) + 1]));
+        y[i] = u & 1 ? bf16_pair(a.y, b.y, s) : bf16_pair(a.x, b.x, s);
+      }
+      *reinterpret_cast<uint4*>(out + t * stride + 8 * c) = make_uint4(y[0], y[1], y[2], y[3]);
     }
-    const int t = 2 * j + 8 * hi;
-    if (t >= t0 && t < t1) store_block(out + t * stride + 16 * g, y0);
-    if (t + 1 >= t0 && t + 1 < t1) store_block(out + (t + 1) * stride + 16 * g, y1);
   }
 }
 
-__global__ void __launch_bounds__(kThreads) read_fp4_kernel(Fp4CacheArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) read_fp4_kernel(Fp4CacheArgs a) {
   release_successor();
   after_predecessor();
   Place p;
-  if (!find_place(a, blockIdx.x, p)) return;
+  if (!find_place(a, blockIdx.x, p) || !good_page(a, p)) return;
   const int lane = threadIdx.x & 31;
   for (int u = blockIdx.y * kWarps + (threadIdx.x >> 5); u < 2 * a.L.Hkv; u += gridDim.y * kWarps) {
-    const int v = u >= a.L.Hkv, h = u - (v ? a.L.Hkv : 0);
+    const bool v = u >= a.L.Hkv;
+    const int h = u - (v ? a.L.Hkv : 0);
     const uint8_t* tile = tile_of(a, p, h);
     if (v ? a.rows.v == nullptr : a.rows.k == nullptr) continue;
     if (v)

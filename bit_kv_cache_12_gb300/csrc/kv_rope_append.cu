@@ -312,9 +312,12 @@ __global__ void __launch_bounds__(kThreads, 4)
                      const __grid_constant__ RopeParams rp) {
   __shared__ __align__(16) float tab[kTile * kTokStride];
   __shared__ int pos[kTile], at[4][kTile];
+  __shared__ __align__(4) uint8_t axis[64];                 // (lanes look at different pairs: not from the parameter)
   release_successor();
   after_predecessor();
   const int t0 = blockIdx.x * kTile;
+  if (threadIdx.x >= kTile && threadIdx.x < kTile + 16)
+    reinterpret_cast<uint32_t*>(axis)[threadIdx.x - kTile] = reinterpret_cast<const uint32_t*>(axes.axis)[threadIdx.x - kTile];
   if (threadIdx.x < kTile) {
     const int t = threadIdx.x;
     int low = t0 + t < a.n_tokens ? 0 : -1;    // below 0: a token without work
@@ -329,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   for (int i = threadIdx.x; i < kTile * 64; i += kThreads) {
     const int t = i >> 6, f = i & 63;
     if (f < n && pos[t] >= 0) {
-      const float2 cs = turn_cos_sin((unsigned long long)at[axes.axis[f]][t] * rp.turn[f], rp.att);
+      const float2 cs = turn_cos_sin((unsigned long long)at[axis[f]][t] * rp.turn[f], rp.att);
       float* d = tab + t * kTokStride + 4 * (f >> 3) + (f & 3) + 32 * ((f >> 2) & 1);
       d[0] = cs.x;
       d[64] = cs.y;
