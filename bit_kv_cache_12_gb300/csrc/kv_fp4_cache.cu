@@ -5,11 +5,10 @@
 // The codes are those of exact quotients.  max |x| has 8 bits and its product with
 // fl(1 / 6) comes out exactly where the quotient lies halfway between two e4m3 numbers (the
 // constant is off by 2^-25.4, less than half a last place of any such number), and on the
-// right side of it elsewhere.  x / s: with r near 1 / s (to a last place or two),
-//   q0 = fl(x r),  q = q0 + (x - q0 s) r,
-// in paired fp32 instructions; the remainder is exact, so a quotient halfway between two
-// codes comes out exactly, which q0 alone does not give (s = 15/8 of a power of two times
-// 1.25); x of 8 bits over s of 4 is otherwise at least 2^-9 away from a halfway point.
+// right side of it elsewhere.  x / s is the product with a reciprocal that is off by a last
+// place or two of fp32, rounded to fp16 on the way to e2m1: a quotient halfway between two
+// codes (3 bits) comes out exactly, and as x of 8 bits over s of 4 is otherwise at least 2^-9
+// away from a halfway point, no other quotient (2^-11 off) reaches one.
 //
 // Bound: memory traffic (512 B of rows and 144 B stored per token and KV head) for long
 // prompts, latency for single tokens.  A warp owns a (tile, head, tensor): one writer for
@@ -27,7 +26,7 @@ namespace kvint2 {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 
 __device__ __forceinline__ uint64_t f2(float a, float b) {
@@ -43,22 +42,18 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
-// Four bytes of codes; in each the first value's in the low four bits.
-__device__ __forceinline__ uint32_t e2m1x8(float a0, float a1, float b0, float b1, float c0, float c1, float d0, float d1) {
+// Four bytes of codes from four fp16 pairs; in each the first value's in the low four bits.
+__device__ __forceinline__ uint32_t e2m1x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   uint32_t r;
-  asm("{ .reg .b8 p, q, r, s; cvt.rn.satfinite.e2m1x2.f32 p, %2, %1; cvt.rn.satfinite.e2m1x2.f32 q, %4, %3; "
-      "cvt.rn.satfinite.e2m1x2.f32 r, %6, %5; cvt.rn.satfinite.e2m1x2.f32 s, %8, %7; mov.b32 %0, {p, q, r, s}; }"
+  asm("{ .reg .b8 p, q, r, s; cvt.rn.satfinite.e2m1x2.f16x2 p, %1; cvt.rn.satfinite.e2m1x2.f16x2 q, %2; "
+      "cvt.rn.satfinite.e2m1x2.f16x2 r, %3; cvt.rn.satfinite.e2m1x2.f16x2 s, %4; mov.b32 %0, {p, q, r, s}; }"
       : "=r"(r)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1), "f"(d0), "f"(d1));
+      : "r"(a), "r"(b), "r"(c), "r"(d));
   return r;
 }
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) { return h2_as_u32(__floats2half2_rn(a, b)); }
 
 // Read once by this kernel, written perhaps by the one in front, which may have been
 // running when this one came up: not the read-only path.
@@ -79,39 +74,60 @@ __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {   // of bf1
 struct Half {
   uint32_t w[4];                               // bf16 pairs
   uint32_t scale;                              // the block's, e4m3
-  uint64_t ns2, r2;                            // pairs of -s * 2^e and its reciprocal
+  uint64_t r2;                                 // 1 / (s * 2^e), twice
 };
 
-// The block's scale, from what both lanes hold.
-__device__ __forceinline__ void scale_block(Half& b, int e) {
+// Of a block the largest magnitude's bits, from what both lanes hold (above 0x7F7F: not all
+// are finite).
+__device__ __forceinline__ uint32_t magnitude(const Half& b) {
   uint32_t m = larger(larger(b.w[0] & 0x7FFF7FFFu, b.w[1] & 0x7FFF7FFFu), larger(b.w[2] & 0x7FFF7FFFu, b.w[3] & 0x7FFF7FFFu));
   m = larger(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = larger(m, (m >> 16) | (m << 16)) & 0xFFFFu;   // the largest magnitude's bits
-  const float top = bf16lo(m) * pow2i(-e);
-  b.scale = m >= 0x7F80u ? 0x7Fu : __nv_cvt_float_to_fp8(top * 0x1.555556p-3f, __NV_SATFINITE, __NV_E4M3);
-  const __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b.scale, __NV_E4M3);
-  float s = __half2float(__half(hr)) * pow2i(e), r;
-  if (m >= 0x7F80u || b.scale == 0) {          // codes of zero
+  return larger(m, m >> 16) & 0xFFFFu;
+}
+
+// A block whose codes do not come by the usual way: zeros, or cut where they are the largest anyway.
+__device__ __forceinline__ void unusual(Half& b, uint32_t m, float& s) {
+  if (m >= 0x7F80u || s == 0.f) {
+    if (m >= 0x7F80u) b.scale = 0x7Fu;
     s = 1.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) b.w[i] = 0;
-  } else if (top > 6.f * 448.f) {              // beyond the format's range: cut where the code is the largest anyway
-    const float cut = 7.f * s;                 // (s = 448 * 2^e: finite)
+  } else {
+    const float cut = 7.f * s;                 // (finite, and a bf16 value)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float x = fminf(fmaxf(bf16lo(b.w[i]), -cut), cut), y = fminf(fmaxf(bf16hi(b.w[i]), -cut), cut);
-      b.w[i] = (__float_as_uint(x) >> 16) | (__float_as_uint(y) & 0xFFFF0000u);   // 7 * 448 * 2^e is a bf16 value
+      b.w[i] = (__float_as_uint(x) >> 16) | (__float_as_uint(y) & 0xFFFF0000u);
     }
   }
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-  b.ns2 = f2(-s, -s);
-  b.r2 = f2(r, r);
+}
+
+// The scales of two blocks.  sixth: fl(1 / 6) * 2^-e, unit: 2^e.
+__device__ __forceinline__ void scale_blocks(Half& a, Half& b, float sixth, float unit) {
+  const uint32_t ma = magnitude(a), mb = magnitude(b);
+  const float ta = bf16lo(ma) * sixth, tb = bf16lo(mb) * sixth;
+  uint32_t pair, half;
+  asm("{ .reg .b16 p; cvt.rn.satfinite.e4m3x2.f32 p, %2, %3; cvt.u32.u16 %0, p; cvt.rn.f16x2.e4m3x2 %1, p; }"
+      : "=r"(pair), "=r"(half)
+      : "f"(tb), "f"(ta));
+  const float2 s2 = __half22float2(u32_as_h2(half));
+  float sa = s2.x * unit, sb = s2.y * unit, ra, rb;
+  a.scale = pair & 0xFFu;
+  b.scale = pair >> 8;
+  // beyond the range (tops of 2688 and more, not finite ones among them), or all zeros
+  if (__any_sync(0xffffffffu, !(fmaxf(ta, tb) < 448.f) || fminf(sa, sb) == 0.f || max(ma, mb) >= 0x7F80u)) {
+    if (!(ta < 448.f) || sa == 0.f || ma >= 0x7F80u) unusual(a, ma, sa);
+    if (!(tb < 448.f) || sb == 0.f || mb >= 0x7F80u) unusual(b, mb, sb);
+  }
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ra) : "f"(sa));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rb) : "f"(sb));
+  a.r2 = f2(ra, ra);
+  b.r2 = f2(rb, rb);
 }
 
 // The quotients of values 2 i and 2 i + 1.
 __device__ __forceinline__ void quotients(const Half& b, int i, float& q0, float& q1) {
-  const uint64_t x = f2(bf16lo(b.w[i]), bf16hi(b.w[i])), q = f2_mul(x, b.r2);
-  f2_split(f2_fma(f2_fma(q, b.ns2, x), b.r2, q), q0, q1);
+  f2_split(f2_mul(f2(bf16lo(b.w[i]), bf16hi(b.w[i])), b.r2), q0, q1);
 }
 
 struct Fp4CacheArgs {
@@ -170,18 +186,26 @@ __device__ __forceinline__ int v_slot(int u, int lane) { return 4 * (u >> 2) + 2
 // K of a tile; x: this lane's eight pieces of rows.
 __device__ __forceinline__ void store_k(const uint4 (&x)[8], int t0, int t1, int e, uint8_t* tile, int lane) {
   const int c = lane & 15;
+  const float sixth = 0x1.555556p-3f * pow2i(-e), unit = pow2i(e);
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    const int t = k_slot(u, lane);
-    Half b{{x[u].x, x[u].y, x[u].z, x[u].w}};
-    scale_block(b, e);
-    float q[8];
+  for (int u = 0; u < 8; u += 2) {
+    Half b[2] = {{{x[u].x, x[u].y, x[u].z, x[u].w}}, {{x[u + 1].x, x[u + 1].y, x[u + 1].z, x[u + 1].w}}};
+    scale_blocks(b[0], b[1], sixth, unit);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) quotients(b, i, q[2 * i], q[2 * i + 1]);
-    const uint32_t w = e2m1x8(q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7]);
-    if (t >= t0 && t < t1) {
-      *reinterpret_cast<uint32_t*>(tile + 64 * t + 4 * c) = w;
-      if ((c & 1) == 0) tile[kFp4KScale + 8 * t + (c >> 1)] = (uint8_t)b.scale;
+    for (int v = 0; v < 2; ++v) {
+      uint32_t q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float q0, q1;
+        quotients(b[v], i, q0, q1);
+        q[i] = pack_f16(q0, q1);
+      }
+      const uint32_t w = e2m1x8(q[0], q[1], q[2], q[3]);
+      const int t = k_slot(u + v, lane);
+      if (t >= t0 && t < t1) {
+        *reinterpret_cast<uint32_t*>(tile + 64 * t + 4 * c) = w;
+        if ((c & 1) == 0) tile[kFp4KScale + 8 * t + (c >> 1)] = (uint8_t)b[v].scale;
+      }
     }
   }
 }
@@ -190,6 +214,7 @@ __device__ __forceinline__ void store_k(const uint4 (&x)[8], int t0, int t1, int
 // the lane's four words and whose scales share one.
 __device__ __forceinline__ void store_v(const uint4 (&x)[8], int t0, int t1, int e, uint8_t* tile, int lane) {
   const int c = lane & 15, g = c >> 1;
+  const float sixth = 0x1.555556p-3f * pow2i(-e), unit = pow2i(e);
 #pragma unroll
   for (int v = 0; v < 2; ++v) {
     const int j = 2 * v + (lane >> 4);
@@ -199,7 +224,10 @@ __device__ __forceinline__ void store_v(const uint4 (&x)[8], int t0, int t1, int
     for (int u = 0; u < 4; ++u) {
       const uint4& y = x[4 * v + u];
       b[u].w[0] = y.x, b[u].w[1] = y.y, b[u].w[2] = y.z, b[u].w[3] = y.w;
-      scale_block(b[u], e);
+      if (u & 1) scale_blocks(b[u - 1], b[u], sixth, unit);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
       scales |= b[u].scale << (8 * u);
       const int t = v_slot(4 * v + u, lane);
       if (t >= t0 && t < t1) {
@@ -220,14 +248,15 @@ __device__ __forceinline__ void store_v(const uint4 (&x)[8], int t0, int t1, int
       float q[4][2];
 #pragma unroll
       for (int u = 0; u < 4; ++u) quotients(b[u], i, q[u][0], q[u][1]);
-      const uint32_t w = e2m1x8(q[0][0], q[1][0], q[0][1], q[1][1], q[2][0], q[3][0], q[2][1], q[3][1]);
+      const uint32_t w = e2m1x8(pack_f16(q[0][0], q[1][0]), pack_f16(q[0][1], q[1][1]), pack_f16(q[2][0], q[3][0]),
+                                pack_f16(q[2][1], q[3][1]));
       if (byte_mask) cw[16 * i] = (old[i] & ~code_mask) | (w & code_mask);
     }
     if (byte_mask && (c & 1) == 0) *sw = (os & ~byte_mask) | (scales & byte_mask);
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 4) append_fp4_kernel(Fp4CacheArgs a) {
+__global__ void __launch_bounds__(kThreads, 8) append_fp4_kernel(Fp4CacheArgs a) {
   release_successor();
   after_predecessor();
   Place p;
@@ -329,7 +358,7 @@ __device__ __forceinline__ void load_v(uint16_t* out, int64_t stride, int t0, in
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 4) read_fp4_kernel(Fp4CacheArgs a) {
+__global__ void __launch_bounds__(kThreads, 8) read_fp4_kernel(Fp4CacheArgs a) {
   release_successor();
   after_predecessor();
   Place p;
