@@ -67,11 +67,11 @@ constexpr int kRing = 4;                       // of barriers that may run ahead
 
 // Barriers.  kData: V of a pass and K of the next (an item's first K comes with q).  kGo:
 // all that the products of a pass wait for, a ring for each tile: P, and for tile 0 that the
-// data are there.  kEmpty: the products of a pass and the next scores are complete; kFirst:
-// an item's first scores are.
-enum { kData = 0, kEmpty = kData + kStages, kGo = kEmpty + kStages, kLooked = kGo + 2 * kRing, kQFull = kLooked + kRing,
-       kQEmpty = kQFull + 2, kFirst = kQEmpty + 2, kSFull = kFirst + 1, kOFull = kSFull + 2, kORead = kOFull + 2, kLast = kORead + 2, kDrain = kLast + 4,
-       kCancel, kItem, kFree = kItem + kItems, kBars = kFree + kItems };
+// data are there.  kSFull: a tile's scores of a pass; those of tile 1 also say that what came
+// before them is done with, the products of the pass before and its values among it.
+enum { kData = 0, kGo = kData + kStages, kLooked = kGo + 2 * kRing, kQFull = kLooked + kRing, kSFull = kQFull + 2,
+       kOFull = kSFull + 2, kORead = kOFull + 2, kLast = kORead + 2, kDrain = kLast + 4, kCancel, kItem, kFree = kItem + kItems,
+       kBars = kFree + kItems };
 
 // An item: a block of rows and the key tiles they see.
 enum { kKeyed = 0, kNoKeys = 1, kStop = 2 };   // rows with keys, rows that see none, no item
@@ -193,31 +193,29 @@ struct Maps {
 };
 
 // The loads of an item: false where a wait ran out.  Pass g brings V of its own and K of the
-// next pass, into stages g and g + 1 modulo two: free when the products of pass g - 2 and
-// the scores of pass g - 1 are complete.  q, g: items and passes loaded so far.
+// next pass, into stages g and g + 1 modulo two: free when the scores of pass g - 1 are
+// complete, and the products of pass g - 2 with them.  q, g: items and passes loaded so far.
 __device__ __forceinline__ bool load_item(const PromptArgs& a, const Maps& maps, const Work& w, bool withhold, uint8_t* sm,
-                                          Shared* sh, const Waiter& wait, int (&q)[2], int& g) {
+                                          Shared* sh, const Waiter& wait, int& q, int& g) {
   const int lane = threadIdx.x & 31, tokens = kRows / a.G, h = w.h, k0 = w.k0, q0 = w.c0 + w.row0 / a.G;
   const uint32_t base = smem_u32(sm);
-  auto ready = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(sh->bars + bar, parity)) != 0; };
   auto load = [&](uint32_t to, const CUtensorMap* map, int head, int row, int bar) {
     load_box(base + to, map, 0, head, row, sh->bars + bar);
     load_box(base + to + kOperand / 2, map, 64, head, row, sh->bars + bar);
   };
-  for (int tile = 0; tile < 2; ++tile) {
-    if (q[tile] && !ready(kQEmpty + tile, (q[tile] - 1) & 1)) return false;
-    if (lane == 0) {
-      mbar_expect_tx(sh->bars + kQFull + tile, tile ? 2 * kOperand : kOperand);
-      load(kOffQ + tile * kOperand, maps.q, h * a.G, q0 + tile * tokens, kQFull + tile);
-      // after the last scores of the item before: every K stage is free
-      if (tile) load(kOffK + g % kStages * kOperand, maps.k, h, k0 + w.tile(w.i0) * kKeys, kQFull + 1);
-    }
-    ++q[tile];
-  }
   for (int i = w.i0; i < w.i1; ++i, ++g) {
     const int stage = g % kStages, last = i + 1 == w.i1;
-    if (g >= kStages && !ready(kEmpty + stage, (g / kStages - 1) & 1)) return false;
-    if (i == w.i0 + 1 && !ready(kFirst, (q[1] - 1) & 1)) return false;
+    if (g && !__all_sync(0xffffffffu, wait(sh->bars + kSFull + 1, (g - 1) & 1))) return false;
+    if (i == w.i0) {                           // q, in the place of the item's before, whose last scores these are
+      if (lane == 0) {
+        for (int tile = 0; tile < 2; ++tile) {
+          mbar_expect_tx(sh->bars + kQFull + tile, tile ? kOperand : 2 * kOperand);
+          load(kOffQ + tile * kOperand, maps.q, h * a.G, q0 + tile * tokens, kQFull + tile);
+          if (!tile) load(kOffK + stage * kOperand, maps.k, h, k0 + w.tile(i) * kKeys, kQFull);
+        }
+      }
+      ++q;
+    }
     if (withhold && last) return false;
     if (lane == 0) {
       mbar_expect_tx(sh->bars + kData + stage, last ? kOperand : 2 * kOperand);
@@ -231,7 +229,7 @@ __device__ __forceinline__ bool load_item(const PromptArgs& a, const Maps& maps,
 
 __device__ __forceinline__ void load_tiles(const PromptArgs& a, const Maps& maps, uint8_t* sm, Shared* sh, const Waiter& wait) {
   const int lane = threadIdx.x & 31;
-  int q[2] = {0, 0}, g = 0;
+  int q = 0, g = 0;
   for (int item = 0;; ++item) {
     const int slot = item & (kItems - 1);
     if (!__all_sync(0xffffffffu, wait.handed(sh->bars + kItem + slot, (item / kItems) & 1))) break;
@@ -246,7 +244,7 @@ __device__ __forceinline__ void load_tiles(const PromptArgs& a, const Maps& maps
   for (int i = max(g - kStages, 0); i < g; ++i) mbar_wait(sh->bars + kData + i % kStages, (i / kStages) & 1, kPolls);
 #pragma unroll 1
   for (int i = 0; i < 2; ++i)
-    if (q[i]) mbar_wait(sh->bars + kQFull + i, (q[i] - 1) & 1, kPolls);
+    if (q) mbar_wait(sh->bars + kQFull + i, (q - 1) & 1, kPolls);
 }
 
 // ---- loaded tiles, and the values of those seen in part (one warp) --------------------
@@ -403,6 +401,7 @@ __device__ __forceinline__ void issue_products(const PromptArgs& a, uint32_t tme
     }
     commit(sh->bars + kSFull + tile);
   };
+  static_assert(kStages == 2, "the other stage is stage ^ 1");
   int g = 0, keyed = 0;                        // passes and items with keys so far
   for (int item = 0;; ++item) {
     const int slot = item & (kItems - 1);
@@ -411,53 +410,50 @@ __device__ __forceinline__ void issue_products(const PromptArgs& a, uint32_t tme
     if (state == kStop) return;
     if (state == kKeyed) {
       if (elect_one()) {
-        dead = dead || !wait(sh->bars + kQFull, keyed & 1) || !wait(sh->bars + kQFull + 1, keyed & 1);
+        dead = dead || !wait(sh->bars + kQFull, keyed & 1);
         fence_after();
         if (!dead) {
 #pragma unroll 1
           for (int tile = 0; tile < 2; ++tile) {
-            scores(tile, g % kStages);
-            if (passes == 1) commit(sh->bars + kQEmpty + tile);
+            if (tile) dead = !wait(sh->bars + kQFull + 1, keyed & 1);
+            if (!dead) scores(tile, g % kStages);
           }
-          commit(sh->bars + kFirst);
         }
       }
       __syncwarp();
+      if (elect_one()) {
 #pragma unroll 1
-      for (int it = 0; it < passes; ++it, ++g) {
-        const int stage = g % kStages;
-        const uint32_t ph = (g / kRing) & 1;
-        const bool last = it + 1 == passes;
+        for (int it = 0; it < passes; ++it) {
+          const int stage = (g + it) % kStages;
+          const uint32_t parity = ((g + it) / kRing) & 1;
+          uint64_t* go = sh->bars + kGo + (g + it) % kRing;
+          const bool last = it + 1 == passes;
 #pragma unroll 1
-        for (int tile = 0; tile < 2; ++tile) {
-          if (elect_one()) {
-            dead = dead || !wait(sh->bars + kGo + tile * kRing + g % kRing, ph);
+          for (int tile = 0; tile < 2; ++tile) {
+            dead = dead || !wait(go + tile * kRing, parity);
             if (it == 0 && keyed) dead = dead || !wait(sh->bars + kORead + tile, (keyed - 1) & 1);
             fence_after();
-            if (!dead) {
-              uint64_t v = v0 + ((stage * kOperand) >> 4);
-              uint32_t p = tmem + 128 * tile;
-              const uint32_t d = tmem + 256 + 128 * tile;
+            if (dead) continue;
+            uint64_t v = v0 + ((stage * kOperand) >> 4);
+            uint32_t p = tmem + 128 * tile;
+            const uint32_t d = tmem + 256 + 128 * tile;
 #pragma unroll 1
-              for (int half = 0; half < 2; ++half) {
+            for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)   // 16 tokens: 8 columns of P, 16 rows of V
-                  mma_ts(d, p + 8 * ks, v + ((ks * 2048) >> 4), it | half | ks);
-                p += 32;
-                v += (4 * 2048) >> 4;
-              }
-              if (last) {
-                commit(sh->bars + kOFull + tile);
-              } else {
-                scores(tile, stage ^ 1);
-                if (it + 2 == passes) commit(sh->bars + kQEmpty + tile);
-              }
-              if (tile == 1) commit(sh->bars + kEmpty + stage);
+              for (int ks = 0; ks < 4; ++ks)   // 16 tokens: 8 columns of P, 16 rows of V
+                mma_ts(d, p + 8 * ks, v + ((ks * 2048) >> 4), it | half | ks);
+              p += 32;
+              v += (4 * 2048) >> 4;
             }
+            if (last)
+              commit(sh->bars + kOFull + tile);
+            else
+              scores(tile, stage ^ 1);
           }
-          __syncwarp();
         }
       }
+      __syncwarp();
+      g += passes;
       ++keyed;
     }
     if (elect_one()) arrive(sh->bars + kFree + slot);
@@ -824,7 +820,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(sh->bars + kData + i, 1);
-      mbar_init(sh->bars + kEmpty + i, 1);
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(sh->bars + kGo + i, 4 + 1);    // softmax warps, looking warp
@@ -833,14 +828,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sh->bars + kQFull + i, 1);
-      mbar_init(sh->bars + kQEmpty + i, 1);
       mbar_init(sh->bars + kSFull + i, 1);
       mbar_init(sh->bars + kOFull + i, 1);
       mbar_init(sh->bars + kORead + i, 4);
       mbar_init(sh->bars + kLast + i, 4);      // of odd and even items: the softmax may be one ahead of the rows
       mbar_init(sh->bars + kLast + 2 + i, 4);
     }
-    mbar_init(sh->bars + kFirst, 1);
     mbar_init(sh->bars + kDrain, 1);
     mbar_init(sh->bars + kCancel, 1);
     for (int i = 0; i < kItems; ++i) {
