@@ -88,7 +88,8 @@ struct Shared {
   Work work[kItems];
   uint4 cancel;                                // what the scheduler answered
   uint64_t bars[kBars];
-  uint32_t list[kLists][4];                    // of a pass that is seen in part: tokens with values that are not finite
+  uint32_t list[kLists][4];                    // of a pass that is seen in part: tokens with values that are not finite,
+  uint32_t any[kLists];                        // and whether there are some
   float2 ml[2][2][kRows];                      // of an item with keys (odd, even) and tile: each row's M and l,
   uint32_t poison[2][2][4];                    // and whether it sees a token listed before the last pass;
   int2 end[2];                                 // the last pass, and of those seen in part
@@ -266,6 +267,7 @@ __device__ __forceinline__ void look_through(const PromptArgs& a, uint8_t* sm, S
           continue;
         }
         uint8_t* tile = sm + kOffV + stage * kOperand + lane * 128;
+        uint32_t any = 0;
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {          // a lane to a token
           uint8_t* row = tile + 32 * 128 * q;
@@ -290,6 +292,7 @@ __device__ __forceinline__ void look_through(const PromptArgs& a, uint8_t* sm, S
             bad = __hisnan(sum.x) || __hisnan(sum.y);
           }
           const uint32_t listed = __ballot_sync(0xffffffffu, bad);
+          any |= listed;
           if (lane == 0) sh->list[g & (kLists - 1)][q] = listed;
           if (bad) {
 #pragma unroll 1
@@ -306,6 +309,7 @@ __device__ __forceinline__ void look_through(const PromptArgs& a, uint8_t* sm, S
         fence_async();
         __syncwarp();
         if (lane == 0) {
+          sh->any[g & (kLists - 1)] = any;
           arrive(sh->bars + kLooked + part % kRing);
           arrive(sh->bars + kGo + g % kRing);
         }
@@ -489,9 +493,10 @@ __device__ __forceinline__ uint32_t sees(const PromptArgs& a, const Work& w, int
   return m;
 }
 // Whether it sees a listed token of pass g, the part-th one of those seen in part, whose
-// products are complete (so that the wait only orders this after the look).
+// products have been issued (so that the wait only orders this after the look).
 __device__ __forceinline__ bool poisoned(const PromptArgs& a, const Work& w, Shared* sh, int i, int t0, int g, int part) {
   mbar_wait(sh->bars + kLooked + part % kRing, (part / kRing) & 1, kPolls);
+  if (!sh->any[g & (kLists - 1)]) return false;   // the usual case
   const int pos = w.pos0 + Row(a, w, i).token;
   uint32_t hit = 0;
 #pragma unroll 1
@@ -537,10 +542,7 @@ __device__ __forceinline__ bool softmax_rows(const PromptArgs& a, const Work& w,
     const int t0 = w.tile(w.i0 + it) * kKeys;
     if (!__all_sync(0xffffffffu, wait(sh->bars + kSFull + tile, g & 1))) return false;
     fence_after();
-    if (check >= 0) ro.poison |= poisoned(a, w, sh, i0, check, g - 1, parts - 1);
     const bool part = in_part(a, w, t0);
-    check = part ? t0 : -1;
-    parts += part;
     float c = cs;
     if (part) hide(a, w, ts, w.pos0 + Row(a, w, i0).token, t0, minus);
     float v[kKeys];
@@ -617,6 +619,9 @@ __device__ __forceinline__ bool softmax_rows(const PromptArgs& a, const Work& w,
     fence_before();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) arrive(sh->bars + kGo + tile * kRing + g % kRing);
+    if (check >= 0) ro.poison |= poisoned(a, w, sh, i0, check, g - 1, parts - 1);   // while the products run
+    check = part ? t0 : -1;
+    parts += part;
     if (it + 1 == passes) return true;
   }
 }
