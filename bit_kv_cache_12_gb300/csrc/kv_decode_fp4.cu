@@ -15,6 +15,14 @@
 // bits down to 2^-32 of it.  The weights are rounded to fp16, and again times sV; M lags
 // so that the largest is between 2^3 and 2^7 (2^7 * 448 is in fp16's range), and weights
 // below 2^-28 of the largest are dropped.
+//
+// Bound: the cache's bytes (144 per token and KV head) for batches, latency for one short
+// sequence, between them the instructions that turn codes into operands (issue slots 62% in
+// use, tensor pipe 31%).  A warp takes two tiles at a step, copied whole (TMA, 4608 bytes)
+// two steps ahead, so that one tile's conversions run beside the other's products: with one
+// tile 64 sequences of 20,480 tokens took 317 us, with two 255.  Measured: 1024 tokens of 2
+// KV heads 5.0 us (6.3 with the host's part), 100,000 tokens of 8 28.9 us (115 MB, 4.0 TB/s),
+// 64 ragged sequences of 8k to 32k 296 us (1745 MB, 5.9 TB/s, 0.88 of a plain copy).
 #include <algorithm>
 
 #include "kv_decode_split.cuh"

@@ -305,7 +305,8 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(RopeArgs a, const __g
 }
 
 // The same with a position for each axis: a pair turns by that of its own.  Only the
-// table differs.
+// table differs: 8192 tokens of 64 + 8 heads on three axes 57 us, 5.3 TB/s, 0.79 of a plain
+// copy (one position: 52).  64 tokens 4.7 us, 11 with the host's part.
 template <bool kPairs>
 __global__ void __launch_bounds__(kThreads, 4)
     rope_axes_kernel(RopeArgs a, int64_t pos_stride, const __grid_constant__ RopeAxes axes,
