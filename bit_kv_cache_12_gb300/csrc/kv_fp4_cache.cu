@@ -156,13 +156,17 @@ struct Place {
 __device__ __forceinline__ bool find_place(const Fp4CacheArgs& a, int x, Place& p) {
   const int s = x / a.tiles, i = x - s * a.tiles;
   const int c0 = a.t.cu[s], c1 = a.t.cu[s + 1], start = a.t.start[s];
-  int n = c1 - c0;
   const bool first = i == 0 && blockIdx.y == 0 && threadIdx.x == 0;
-  if (n < 0 || n > a.t.max_tokens) {
+  if (c0 < 0 || c1 < c0) {                     // (no difference of these is taken: it could pass 32 bits)
     if (first) flag_error(a.err, KV_DEVERR_SEQ_RANGE);
-    n = min(n, a.t.max_tokens);
+    return false;
   }
-  if (n <= 0) return false;
+  int n = c1 - c0;
+  if (n > a.t.max_tokens) {
+    if (first) flag_error(a.err, KV_DEVERR_SEQ_RANGE);
+    n = a.t.max_tokens;
+  }
+  if (n == 0) return false;
   if (start < 0 || (long long)start + n > min((long long)a.t.max_pages * a.L.P, (long long)INT32_MAX)) {
     if (first) flag_error(a.err, KV_DEVERR_SEQ_RANGE);
     return false;

@@ -638,7 +638,8 @@ kv_status_t kv_rope_apply_axes(const kv_pool_t* pool, int32_t layer, int32_t n_t
  *              contiguous; 16-byte aligned, strides (in elements) multiples of 8 and
  *              at least a token's channels
  *   cu_tokens  device int32 [n_seqs+1] prefix sums; rows from cu_tokens[n_seqs] on
- *              are not read
+ *              are not read; a sequence whose first row or count is negative is skipped
+ *              (KV_DEVERR_SEQ_RANGE)
  *   start_pos  device int32 [n_seqs]: tokens the sequence already caches
  *   max_tokens_per_seq  host bound (sizes the grid; longer sequences are flagged
  *              KV_DEVERR_SEQ_RANGE and truncated)
