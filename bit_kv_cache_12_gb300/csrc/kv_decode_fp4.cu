@@ -21,7 +21,7 @@
 // use, tensor pipe 31%).  A warp takes two tiles at a step, copied whole (TMA, 4608 bytes)
 // two steps ahead, so that one tile's conversions run beside the other's products: with one
 // tile 64 sequences of 20,480 tokens took 317 us, with two 255.  Measured: 1024 tokens of 2
-// KV heads 5.0 us (6.3 with the host's part), 100,000 tokens of 8 28.9 us (115 MB, 4.0 TB/s),
+// KV heads 5.0 us (6.3 with the host's part), 100,000 tokens of 8 27.0 us (115 MB, 4.3 TB/s),
 // 64 ragged sequences of 8k to 32k 296 us (1745 MB, 5.9 TB/s, 0.88 of a plain copy).
 #include <algorithm>
 
@@ -358,8 +358,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp4_kernel(DecodeFp4Args a
     }
   }
   __syncthreads();
-  join_parts<G, kWarps, kHeadStride>(a.c, a.Hq, a.n_split, a.cluster, a.tickets, smem, split, pair, b, h,
-                                     [](int c) { return c; });
+  join_parts<G, kWarps, kHeadStride, (int)kRing, true>(a.c, a.Hq, a.n_split, a.cluster, a.tickets, smem, split, pair, b,
+                                                       h, [](int c) { return c; });
 }
 
 // Microseconds that a call takes with each (sequence, KV head) pair in n splits of `units`

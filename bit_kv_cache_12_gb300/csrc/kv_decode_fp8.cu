@@ -313,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp8_kernel(DecodeFp8Args a
     }
   }
   __syncthreads();
-  join_parts<G, kWarps, kHeadStride>(a.c, a.Hq, a.n_split, a.cluster, a.tickets, smem, split, pair, b, h,
-                                     [](int c) { return chan(c); });
+  join_parts<G, kWarps, kHeadStride, (int)kRing, false>(a.c, a.Hq, a.n_split, a.cluster, a.tickets, smem, split, pair, b,
+                                                        h, [](int c) { return chan(c); });
 }
 
 // Splits per (sequence, KV head), from the host's bound on visible tiles (times by

@@ -72,14 +72,132 @@ __device__ __forceinline__ float4 ld_remote4(uint32_t p) {
   return v;
 }
 
+// The last CTA of a pair to arrive joins the pair's splits, in their order.
+template <int G, int kWarps, int kRoom>
+__device__ __forceinline__ void join_through_memory(const float* parts, int n_split, unsigned* ticket, uint8_t* smem,
+                                                    uint16_t* out, float* lse) {
+  constexpr int kThreads = kWarps * 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ int last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const unsigned t = atomicAdd(ticket, 1u);
+    last = t == (unsigned)n_split - 1u;
+    if (last) *ticket = 0;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  float* sw = reinterpret_cast<float*>(smem);  // weights [split][G]
+  float* sl = sw + kMaxSplits * G;             // [G] l
+  float4* red = reinterpret_cast<float4*>(sl + ((G + 3) & ~3));
+  float4* buf = red + kThreads;                // parts, as many as there is room for
+  // G * 32 columns of four channels; where threads are left, several share a
+  // column, each a run of splits.  The parts come to shared memory all at once
+  // and the loops are short: loaded to registers by unrolled code, cold as it
+  // is, 36 splits of four heads took 4.3 us instead of 2.5.
+  constexpr int kCols = G * 32, kShare = kThreads / kCols, kQuads = G * kPart / 4;   // (16 bytes of a split)
+  constexpr int kFit = (kRoom - kMaxSplits * G * 4 - 32 - kThreads * 16) / (kQuads * 16);
+  static_assert(kFit >= 1, "a part fits");
+  const int col = threadIdx.x % kCols, sh = threadIdx.x / kCols;
+  const int g = col >> 5, c4 = col & 31;
+  const int run = (n_split + kShare - 1) / kShare, s0 = sh * run, s1 = min(s0 + run, n_split);
+  auto fetch = [&](int from, int to, int thread, int threads) {
+    const float4* src = reinterpret_cast<const float4*>(parts) + (size_t)from * kQuads;
+#pragma unroll 1
+    for (int i = thread; i < (to - from) * kQuads; i += threads)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(buf + i)), "l"(src + i) : "memory");
+  };
+  constexpr int kForm = G < kWarps ? G : 0;    // warps that form the weights meanwhile
+  if (warp >= kForm) fetch(0, min(kFit, n_split), threadIdx.x - 32 * kForm, kThreads - 32 * kForm);
+  if (warp < G) {
+    const int g = warp;
+    float M = kNoRef, l = 0.f;
+    float m[kMaxSplits / 32], ll[kMaxSplits / 32];
+#pragma unroll
+    for (int u = 0; u < kMaxSplits / 32; ++u) {
+      const int s = lane + 32 * u;
+      m[u] = kNoRef;
+      ll[u] = 0.f;
+      if (s < n_split) {
+        const float2 t = __ldcg(reinterpret_cast<const float2*>(parts + ((size_t)s * G + g) * kPart));
+        m[u] = t.x;
+        ll[u] = t.y;
+      }
+      M = fmaxf(M, m[u]);
+    }
+    M = warp_max_xor(M, 1);
+#pragma unroll
+    for (int u = 0; u < kMaxSplits / 32; ++u) {
+      const float f = ll[u] == 0.f ? 0.f : exp2_neg(m[u] - M);
+      l = fmaf(f, ll[u], l);
+      sw[(lane + 32 * u) * G + g] = ll[u] == 0.f ? -1.f : f;   // below 0: a split that saw no token
+    }
+    l = warp_sum_xor(l, 1);
+    if (lane == 0) {
+      sl[g] = l;
+      if (lse) lse[g] = lse_of(M, l);
+    }
+  }
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int from = 0;;) {
+    const int to = min(from + kFit, n_split);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+#pragma unroll 2
+    for (int s = max(s0, from); s < min(s1, to); ++s) {
+      const float f = sw[s * G + g];
+      const float4 p = buf[(s - from) * kQuads + g * (kPart / 4) + 1 + c4];
+      if (f < 0.f) continue;
+      acc.x = fmaf(f, p.x, acc.x);
+      acc.y = fmaf(f, p.y, acc.y);
+      acc.z = fmaf(f, p.z, acc.z);
+      acc.w = fmaf(f, p.w, acc.w);
+    }
+    if (to == n_split) break;
+    __syncthreads();
+    from = to;
+    fetch(from, min(from + kFit, n_split), threadIdx.x, kThreads);
+  }
+  if (kShare > 1) {
+    red[threadIdx.x] = acc;
+    __syncthreads();
+  }
+  if (sh == 0) {
+#pragma unroll
+    for (int u = 1; u < kShare; ++u) {
+      const float4 t = red[u * kCols + col];
+      acc.x += t.x;
+      acc.y += t.y;
+      acc.z += t.z;
+      acc.w += t.w;
+    }
+    const float l = sl[g], f = l == 0.f ? 0.f : 1.f / l;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * f, acc.y * f), hi = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+    *reinterpret_cast<uint2*>(out + g * 128 + 4 * c4) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
+}
+
+template <int G, int kWarps, int kRoom>
+__device__ __noinline__ void join_apart(const float* parts, int n_split, unsigned* ticket, uint8_t* smem, uint16_t* out,
+                                        float* lse) {
+  join_through_memory<G, kWarps, kRoom>(parts, n_split, ticket, smem, out, lse);
+}
+
 // Joins what the warps of a CTA hold of the G heads of pair (b, h), then the splits of the
 // pair, and writes the rows.  In shared memory, written and fenced by a barrier:
 //   wo  [warp][head] sums of 128 channels, heads kHeadStride floats apart, channel c at at(c)
 //   wm, wl  behind them, [warp][head] M and l (l = 0: saw no token)
 // Parts are joined in the order of their warps and splits: the result does not depend on
 // timing.  Splits of a cluster (n_split at most kMaxCluster) read one another's parts from
-// shared memory; else the last CTA of the pair to arrive joins them through c.ws.
-template <int G, int kWarps, int kHeadStride, class Chan>
+// shared memory; else the last CTA of the pair to arrive joins them through c.ws.  kRoom:
+// bytes of smem that may be used.  kApart: that join is a function of its own, and the
+// registers of the kernel's loops are allotted without it (the 4-bit kernel: 64 x 20,480
+// tokens 250 -> 245 us; the 8-bit one gains nothing and pays 0.4 us for the call).
+template <int G, int kWarps, int kHeadStride, int kRoom, bool kApart, class Chan>
 __device__ __forceinline__ void join_parts(const AttnCall& c, int Hq, int n_split, int cluster, unsigned* tickets,
                                            uint8_t* smem, int split, int pair, int b, int h, Chan at) {
   constexpr int kThreads = kWarps * 32;
@@ -154,97 +272,10 @@ __device__ __forceinline__ void join_parts(const AttnCall& c, int Hq, int n_spli
     return;
   }
 
-  // ---- the last CTA of the pair joins the splits, in their order ----
-  __shared__ int last;
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const unsigned t = atomicAdd(tickets + pair, 1u);
-    last = t == (unsigned)n_split - 1u;
-    if (last) tickets[pair] = 0;
-  }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  float* sw = reinterpret_cast<float*>(smem);  // weights [split][G]
-  float* sl = sw + kMaxSplits * G;             // [G] M, l
-  // G * 32 columns of four channels; where threads are left, several share a
-  // column, each a run of splits.  The first kFly parts of a run are on their way
-  // before the weights are formed.
-  constexpr int kCols = G * 32, kShare = kThreads / kCols, kFly = 16;
-  const int col = threadIdx.x % kCols, sh = threadIdx.x / kCols;
-  const int g = col >> 5, c4 = col & 31;
-  const int run = (n_split + kShare - 1) / kShare, s0 = sh * run, s1 = min(s0 + run, n_split);
-  auto part_of = [&](int s) {
-    return __ldcg(reinterpret_cast<const float4*>(parts + ((size_t)s * G + g) * kPart + 4) + c4);
-  };
-  float4 fly[kFly];
-#pragma unroll
-  for (int u = 0; u < kFly; ++u) fly[u] = part_of(min(s0 + u, n_split - 1));
-  if (warp < G) {
-    const int g = warp;
-    float M = kNoRef, l = 0.f;
-    float m[kMaxSplits / 32], ll[kMaxSplits / 32];
-#pragma unroll
-    for (int u = 0; u < kMaxSplits / 32; ++u) {
-      const int s = lane + 32 * u;
-      m[u] = kNoRef;
-      ll[u] = 0.f;
-      if (s < n_split) {
-        const float2 t = __ldcg(reinterpret_cast<const float2*>(parts + ((size_t)s * G + g) * kPart));
-        m[u] = t.x;
-        ll[u] = t.y;
-      }
-      M = fmaxf(M, m[u]);
-    }
-    M = warp_max_xor(M, 1);
-#pragma unroll
-    for (int u = 0; u < kMaxSplits / 32; ++u) {
-      const float f = ll[u] == 0.f ? 0.f : exp2_neg(m[u] - M);
-      l = fmaf(f, ll[u], l);
-      sw[(lane + 32 * u) * G + g] = ll[u] == 0.f ? -1.f : f;   // below 0: a split that saw no token
-    }
-    l = warp_sum_xor(l, 1);
-    if (lane == 0) {
-      sl[g] = l;
-      if (lse) lse[g] = lse_of(M, l);
-    }
-  }
-  __syncthreads();
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](int s, const float4& p) {
-    const float f = sw[s * G + g];
-    if (!(f < 0.f)) {
-      acc.x = fmaf(f, p.x, acc.x);
-      acc.y = fmaf(f, p.y, acc.y);
-      acc.z = fmaf(f, p.z, acc.z);
-      acc.w = fmaf(f, p.w, acc.w);
-    }
-  };
-#pragma unroll
-  for (int u = 0; u < kFly; ++u)
-    if (s0 + u < s1) add(s0 + u, fly[u]);
-#pragma unroll 8
-  for (int s = s0 + kFly; s < s1; ++s) add(s, part_of(s));
-  float4* red = reinterpret_cast<float4*>(sl + ((G + 3) & ~3));
-  if (kShare > 1) {
-    red[threadIdx.x] = acc;
-    __syncthreads();
-  }
-  if (sh == 0) {
-#pragma unroll
-    for (int u = 1; u < kShare; ++u) {
-      const float4 t = red[u * kCols + col];
-      acc.x += t.x;
-      acc.y += t.y;
-      acc.z += t.z;
-      acc.w += t.w;
-    }
-    const float l = sl[g], f = l == 0.f ? 0.f : 1.f / l;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * f, acc.y * f), hi = __floats2bfloat162_rn(acc.z * f, acc.w * f);
-    *reinterpret_cast<uint2*>(out + g * 128 + 4 * c4) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-  }
+  if (kApart)
+    join_apart<G, kWarps, kRoom>(parts, n_split, tickets + pair, smem, out, lse);
+  else
+    join_through_memory<G, kWarps, kRoom>(parts, n_split, tickets + pair, smem, out, lse);
 }
 
 
