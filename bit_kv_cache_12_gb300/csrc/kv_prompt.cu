@@ -56,7 +56,7 @@ constexpr int kKeys = 128;                     // keys of a tile
 constexpr int kThreads = 16 * 32;              // four warpgroups
 // registers per thread of the softmax warpgroups and of the two others: they share the
 // launch's 128 each
-constexpr int kSoftRegs = 184, kOtherRegs = 72;
+constexpr int kSoftRegs = 176, kOtherRegs = 80;
 static_assert(2 * kSoftRegs + 2 * kOtherRegs <= 4 * 128, "setmaxnreg.inc draws on the launch's registers");
 constexpr int kPolls = 1 << 18;                // bound of a wait: a poll suspends for up to 3.7 us, so about a second
 constexpr int kMaxSplits = 32;
@@ -101,7 +101,7 @@ struct Shared {
   uint64_t bars[kBars];
   uint32_t list[kLists][4];                    // of a pass that is seen in part: tokens with values that are not finite,
   uint32_t any[kLists];                        // and whether there are some
-  float2 ml[2][2][kRows];                      // of an item with keys (odd, even) and tile: each row's M and l,
+  float l[2][2][kRows];                        // of an item with keys (odd, even) and tile: each row's l,
   uint32_t poison[2][2][4];                    // and whether it sees a token listed before the last pass;
   int2 end[2];                                 // the last pass, and of those seen in part
   uint32_t tmem;
@@ -642,6 +642,14 @@ __device__ __forceinline__ float* part_of(const PromptArgs& a, const Work& w, co
   return static_cast<float*>(a.c.ws) + ((((size_t)w.s * a.c.max_q + r.token) * a.Hq + r.hq) * a.n_split + w.split) * kPart;
 }
 
+__device__ __forceinline__ void put_lse(const PromptArgs& a, const Work& w, const Row& r, float lse) {
+  if (!r.live) return;
+  if (a.n_split > 1)
+    *part_of(a, w, r) = lse;
+  else if (a.c.lse)
+    a.c.lse[r.qrow] = lse;
+}
+
 // Channels 32 q .. of a row that sees listed tokens: a bit for each that some visible value
 // makes not finite, from the tiles that are seen in part (in the others they went into the
 // products as they are).
@@ -674,46 +682,48 @@ __device__ __forceinline__ uint32_t spoiled(const PromptArgs& a, const Work& w, 
 
 // Rows of a tile, a thread to a row: its products times f to the output, or as a part of a
 // split.  `stage`: 4 KB of shared memory for 64 channels of the warp's 32 rows, from which
-// they are written 128 bytes at a time.  have: there are products (else f stands for all);
-// read: their barrier, arrived on once they are out of tensor memory.  Short loops: the code
-// is cold whenever it runs (unrolled, a tile took 11,000 clocks).
-__device__ __forceinline__ void write_rows(const PromptArgs& a, const Work& w, uint32_t to, uint8_t* stage, int row0, bool have,
-                                           float f, uint64_t* read) {
+// they are written 128 bytes at a time.  f 0: zeros, whatever the products are.  read: their
+// barrier, arrived on once they are out of tensor memory.  Short loops: the code is cold
+// whenever it runs (unrolled, a tile took 11,000 clocks; as it is 2,700).
+__device__ __forceinline__ void write_rows(const PromptArgs& a, const Work& w, uint32_t to, uint8_t* stage, int row0, float f,
+                                           uint64_t* read) {
   const int lane = threadIdx.x & 31, shift = __ffs(a.G) - 1;
   // to shared memory: this lane's row, 16-byte chunk c of row r at c ^ r % 8 (no bank
   // conflicts either way); from there: lane 8 u + c takes chunk c of rows 8 u + i
   uint8_t* put = stage + lane * 128;
+  const uint32_t keep = f != 0.f ? 0xFFFFFFFFu : 0u;
   const uint8_t* get = stage + (lane >> 3) * 1024;
   const int token = (w.row0 + row0 + 8 * (lane >> 3)) >> shift, m = w.m;
   uint4* out = static_cast<uint4*>(a.c.out) + (((size_t)w.c0 + token) * a.Hq + w.h * a.G) * 16 + (lane & 7);
 #pragma unroll 1
   for (int half = 0; half < 2; ++half) {
 #pragma unroll 1
-    for (int q = 0; q < 4; ++q) {
-      float o[16];
-      if (have) {
-        ld16(to + 64 * half + 16 * q, o);
-        settle16(o);
-      }
+    for (int q = 0; q < 2; ++q) {
+      float o[32];
+      ld32(to + 64 * half + 32 * q, o);
+      settle(o);
+      const uint64_t ff = f2(f, f);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[i] = have && f != 0.f ? o[i] * f : f;
+      for (int i = 0; i < 16; ++i) f2_split(f2_fma(f2(o[2 * i], o[2 * i + 1]), ff, f2(-0.f, -0.f)), o[2 * i], o[2 * i + 1]);
       if (a.n_split > 1) {
         const Row row(a, w, row0 + lane);
         if (row.live) {
-          float* part = part_of(a, w, row) + 4 + 64 * half + 16 * q;
+          float* part = part_of(a, w, row) + 4 + 64 * half + 32 * q;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(__float_as_uint(o[i]) & keep);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
             *reinterpret_cast<float4*>(part + 4 * i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       } else {
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          *reinterpret_cast<uint4*>(put + (((2 * q + c) ^ (lane & 7)) << 4)) =
-              make_uint4(pack_bf16(o[8 * c], o[8 * c + 1]), pack_bf16(o[8 * c + 2], o[8 * c + 3]),
-                         pack_bf16(o[8 * c + 4], o[8 * c + 5]), pack_bf16(o[8 * c + 6], o[8 * c + 7]));
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4*>(put + (((4 * q + c) ^ (lane & 7)) << 4)) =
+              make_uint4(pack_bf16(o[8 * c], o[8 * c + 1]) & keep, pack_bf16(o[8 * c + 2], o[8 * c + 3]) & keep,
+                         pack_bf16(o[8 * c + 4], o[8 * c + 5]) & keep, pack_bf16(o[8 * c + 6], o[8 * c + 7]) & keep);
       }
     }
-    if (have && half) {
+    if (half) {
       fence_before();
       __syncwarp();
       if (lane == 0) arrive(read);
@@ -757,37 +767,42 @@ __device__ __forceinline__ int write_items(const PromptArgs& a, uint32_t tmem, u
     const Work& w = sh->work[slot];
     if (w.state == kStop) break;
     const bool any = w.state == kKeyed;
+    float f0 = 0.f, f1 = 0.f;                  // of this thread's rows of the two tiles
+    uint32_t poison = 0;                       // whether they see a listed token
+    if (any) {
+      const int t0 = w.tile(w.i1 - 1) * kKeys;
+      const bool part = in_part(a, w, t0);
 #pragma unroll 1
-    for (int tile = 0; tile < 2; ++tile) {
-      const int i = tile * kRows + m;          // this thread's row of the block
-      float f = 0.f;
-      {                                        // before the last products are complete
-        float2 ml = make_float2(kNoRef, 0.f);
-        if (any) {
-          if (!__all_sync(0xffffffffu, wait(sh->bars + kLast + 2 * (keyed & 1) + tile, (keyed >> 1) & 1))) return item;
-          ml = sh->ml[keyed & 1][tile][m];
-        }
-        if (ml.y != 0.f) f = 1.f / ml.y;
-        const Row row(a, w, i);
-        if (row.live) {
-          const float lse = lse_of(ml.x, ml.y);
-          if (a.n_split > 1)
-            *part_of(a, w, row) = lse;
-          else if (a.c.lse)
-            a.c.lse[row.qrow] = lse;
-        }
-      }
-      if (any && !__all_sync(0xffffffffu, wait(sh->bars + kOFull + tile, keyed & 1))) return item;
-      fence_after();
-      write_rows(a, w, tmem + ((uint32_t)(32 * warp) << 16) + 256 + 128 * tile, sm + kOffOut + warp * 4096,
-                 tile * kRows + 32 * warp, any, f, sh->bars + kORead + tile);
-      if (any) {
-        bool poison = (sh->poison[keyed & 1][tile][warp] >> lane) & 1;
-        const int t0 = w.tile(w.i1 - 1) * kKeys;
-        if (in_part(a, w, t0)) poison |= poisoned(a, w, sh, i, t0, sh->end[keyed & 1].x, sh->end[keyed & 1].y);
-        if (poison) spoil_row(a, w, i);
+      for (int tile = 0; tile < 2; ++tile) {
+        if (!__all_sync(0xffffffffu, wait(sh->bars + kLast + 2 * (keyed & 1) + tile, (keyed >> 1) & 1))) return item;
+        const float l = sh->l[keyed & 1][tile][m];
+        f0 = f1;
+        f1 = l != 0.f ? 1.f / l : 0.f;
+        uint32_t hit = (sh->poison[keyed & 1][tile][warp] >> lane) & 1;
+        // asked before the products are given back: so the looking warp is at most two passes
+        // on, and the barrier of the last pass still in its phase
+        if (part) hit |= poisoned(a, w, sh, tile * kRows + m, t0, sh->end[keyed & 1].x, sh->end[keyed & 1].y);
+        poison |= hit << tile;
       }
     }
+#pragma unroll 1
+    for (int tile = 0; tile < 2; ++tile) {
+      if (!any) {
+        const Row row(a, w, tile * kRows + m);
+        put_lse(a, w, row, -INFINITY);
+        uint4* out = static_cast<uint4*>(a.c.out) + row.qrow * 16;
+#pragma unroll 1
+        for (int c = 0; c < 16 && row.live && a.n_split == 1; ++c) out[c] = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      if (!__all_sync(0xffffffffu, wait(sh->bars + kOFull + tile, keyed & 1))) return item;
+      fence_after();
+      write_rows(a, w, tmem + ((uint32_t)(32 * warp) << 16) + 256 + 128 * tile, sm + kOffOut + warp * 4096,
+                 tile * kRows + 32 * warp, tile ? f1 : f0, sh->bars + kORead + tile);
+    }
+#pragma unroll 1
+    for (int tile = 0; tile < 2; ++tile)
+      if ((poison >> tile) & 1) spoil_row(a, w, tile * kRows + m);
     if (any) ++keyed;
     __syncwarp();
     if (lane == 0) arrive(sh->bars + kFree + slot);
@@ -887,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w.state == kKeyed) {
         RowOut ro;
         if (!softmax_rows(a, w, trow, tile, sh, wait, g, parts, ro)) break;
-        sh->ml[keyed & 1][tile][threadIdx.x & 127] = make_float2(ro.M, ro.l);
+        sh->l[keyed & 1][tile][threadIdx.x & 127] = ro.l;
         const uint32_t poison = __ballot_sync(0xffffffffu, ro.poison);
         if (lane == 0) {
           sh->poison[keyed & 1][tile][warp & 3] = poison;
@@ -895,6 +910,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) arrive(sh->bars + kLast + 2 * (keyed & 1) + tile);
+        put_lse(a, w, Row(a, w, tile * kRows + (threadIdx.x & 127)), lse_of(ro.M, ro.l));   // while the last products run
         ++g;
         ++keyed;
       }
