@@ -115,7 +115,7 @@ constexpr uint32_t kSmem = kOffInfo + sizeof(Shared) + 1024;
 
 struct PromptArgs {
   PromptCall c;
-  int Hq, Hkv, G, n_split, q_blocks;
+  int Hq, Hkv, G, shift, n_split, q_blocks;    // G = 2^shift: 1, 2, 4 or 8
   int* err;
   int polls;
   int stall;                                   // test hook: CTA 0 withholds its first item's last values
@@ -159,12 +159,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // Item x of the grid; false where it has no rows (the whole warp calls this).
 __device__ __forceinline__ bool find_work(const PromptArgs& a, int x, Work& w) {
   // blocks of a sequence from its last (most keys) to its first
-  w.split = x % a.n_split;
-  x /= a.n_split;
-  w.h = x % a.Hkv;
-  x /= a.Hkv;
-  w.s = x % a.c.n_seqs;
-  const int blk = a.q_blocks - 1 - x / a.c.n_seqs;
+  unsigned y = x;
+  w.split = 0;
+  if (a.n_split > 1) {
+    w.split = y % a.n_split;
+    y /= a.n_split;
+  }
+  w.h = y % a.Hkv;
+  y /= a.Hkv;
+  w.s = y % a.c.n_seqs;
+  const int blk = a.q_blocks - 1 - (int)(y / a.c.n_seqs);
   w.c0 = a.c.cu_q[w.s];
   w.m = a.c.cu_q[w.s + 1] - w.c0;
   w.k0 = a.c.cu_k[w.s];
@@ -177,7 +181,7 @@ __device__ __forceinline__ bool find_work(const PromptArgs& a, int x, Work& w) {
   w.row0 = blk * 2 * kRows;
   if ((long long)w.row0 >= (long long)w.m * a.G) return false;
   w.pos0 = w.n - w.m;
-  const int p_lo = w.pos0 + w.row0 / a.G, p_hi = w.pos0 + min((w.row0 + 2 * kRows) / a.G, w.m) - 1;
+  const int p_lo = w.pos0 + (w.row0 >> a.shift), p_hi = w.pos0 + min((w.row0 + 2 * kRows) >> a.shift, w.m) - 1;
   w.low = a.c.window ? max(p_lo - a.c.window + 1, 0) : 0;
   const int end = max(p_hi + 1, 0);
   w.first = p_lo;
@@ -186,7 +190,7 @@ __device__ __forceinline__ bool find_work(const PromptArgs& a, int x, Work& w) {
   w.w0 = min(w.low, end) / kKeys;
   w.ns = min((min(w.sinks, end) + kKeys - 1) / kKeys, w.w0);
   const int total = w.ns + (end + kKeys - 1) / kKeys - w.w0;
-  const int per = (total + a.n_split - 1) / a.n_split;
+  const int per = a.n_split > 1 ? (unsigned)(total + a.n_split - 1) / a.n_split : total;
   w.i0 = min(w.split * per, total);
   w.i1 = min(w.i0 + per, total);
   w.state = w.i0 < w.i1 ? kKeyed : kNoKeys;
@@ -209,7 +213,7 @@ struct Maps {
 // complete, and the products of pass g - 2 with them.  q, g: items and passes loaded so far.
 __device__ __forceinline__ bool load_item(const PromptArgs& a, const Maps& maps, const Work& w, bool withhold, uint8_t* sm,
                                           Shared* sh, const Waiter& wait, int& q, int& g) {
-  const int lane = threadIdx.x & 31, tokens = kRows / a.G, h = w.h, k0 = w.k0, q0 = w.c0 + w.row0 / a.G;
+  const int lane = threadIdx.x & 31, tokens = kRows >> a.shift, h = w.h, k0 = w.k0, q0 = w.c0 + (w.row0 >> a.shift);
   const uint32_t base = smem_u32(sm);
   auto load = [&](uint32_t to, const CUtensorMap* map, int head, int row, int bar) {
     load_box(base + to, map, 0, head, row, sh->bars + bar);
@@ -341,8 +345,8 @@ __device__ __forceinline__ void walk(const PromptArgs& a, const CUtensorMap* q, 
   auto ready = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(sh->bars + bar, parity)) != 0; };
   auto publish = [&](const Work& w, int item) -> bool {
     const int slot = item & (kItems - 1);
-    if (w.state == kKeyed && lane < 4)         // its q comes to the L2 cache while the items before are worked on
-      prefetch_box(q, 64 * (lane & 1), w.h * a.G, w.c0 + w.row0 / a.G + (lane >> 1) * (kRows / a.G));
+    if (item && w.state == kKeyed && lane < 4) // its q comes to the L2 cache while the items before are worked on
+      prefetch_box(q, 64 * (lane & 1), w.h * a.G, w.c0 + (w.row0 >> a.shift) + (lane >> 1) * (kRows >> a.shift));
     if (item >= kItems && !ready(kFree + slot, (item / kItems - 1) & 1)) return false;
     if (lane == 0) {
       sh->work[slot] = w;
@@ -353,9 +357,7 @@ __device__ __forceinline__ void walk(const PromptArgs& a, const CUtensorMap* q, 
     __syncwarp();
     return true;
   };
-  int x = blockIdx.x, items = 0;
-  bool ok = true;
-  for (int asked = 0;; ++asked) {
+  auto ask = [&](int steps) {
     if (lane == 0) {
       fence_async();
       mbar_expect_tx(sh->bars + kCancel, 16);
@@ -364,11 +366,17 @@ __device__ __forceinline__ void walk(const PromptArgs& a, const CUtensorMap* q, 
               smem_u32(&sh->cancel)),
           "r"(smem_u32(sh->bars + kCancel))
           : "memory");
+      *reinterpret_cast<volatile int*>(&sh->steps) = steps;
     }
-    if (lane == 0) *reinterpret_cast<volatile int*>(&sh->steps) = asked + 1;
     __syncwarp();
+  };
+  int x = blockIdx.x, items = 0;
+  bool ok = true;
+  for (int asked = 0;; ++asked) {
+    if (asked) ask(asked + 1);
     Work w;
     if (find_work(a, x, w)) ok = publish(w, items++);
+    if (!asked) ask(1);                        // (after the first item, which everyone waits for)
     // the answer is waited for even when something failed: it is written to shared memory
     if (!__all_sync(0xffffffffu, mbar_wait(sh->bars + kCancel, asked & 1, kPolls))) {
       *reinterpret_cast<volatile int*>(wait.abort) = 1;
@@ -485,7 +493,7 @@ struct Row {
   size_t qrow;
   __device__ __forceinline__ Row(const PromptArgs& a, const Work& w, int i) {
     const int row = w.row0 + i;                // of the sequence's rows
-    token = row >> (__ffs(a.G) - 1);           // G: 1, 2, 4 or 8
+    token = row >> a.shift;
     hq = w.h * a.G + (row & (a.G - 1));
     live = token < w.m;
     qrow = ((size_t)w.c0 + token) * a.Hq + hq;
@@ -687,7 +695,7 @@ __device__ __forceinline__ uint32_t spoiled(const PromptArgs& a, const Work& w, 
 // whenever it runs (unrolled, a tile took 11,000 clocks; as it is 2,700).
 __device__ __forceinline__ void write_rows(const PromptArgs& a, const Work& w, uint32_t to, uint8_t* stage, int row0, float f,
                                            uint64_t* read) {
-  const int lane = threadIdx.x & 31, shift = __ffs(a.G) - 1;
+  const int lane = threadIdx.x & 31, shift = a.shift;
   // to shared memory: this lane's row, 16-byte chunk c of row r at c ^ r % 8 (no bank
   // conflicts either way); from there: lane 8 u + c takes chunk c of rows 8 u + i
   uint8_t* put = stage + lane * 128;
@@ -1029,7 +1037,7 @@ size_t prompt_workspace_up_to(const Pool& p, int n_seqs, int max_q, int max_k) {
 
 cudaError_t launch_prompt(const Pool& p, const PromptCall& c, cudaStream_t s) {
   if (c.max_q == 0) return cudaSuccess;
-  PromptArgs a{c, p.cfg.num_q_heads, p.cfg.num_kv_heads, p.G, splits(p, c.n_seqs, c.max_q, c.max_k, c.window, c.n_sink),
+  PromptArgs a{c, p.cfg.num_q_heads, p.cfg.num_kv_heads, p.G, __builtin_ctz(p.G), splits(p, c.n_seqs, c.max_q, c.max_k, c.window, c.n_sink),
                (int)q_blocks(p, c.max_q), p.err, p.test_wait_polls > 0 ? p.test_wait_polls : kPolls, p.test_stall_first_copy};
   const long long ctas = (long long)a.q_blocks * c.n_seqs * a.Hkv * a.n_split;
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
