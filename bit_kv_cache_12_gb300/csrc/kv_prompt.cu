@@ -30,15 +30,15 @@
 // joins by their log-sum-exp.
 //
 // Bound: the tensor cores.  A pass of both tiles over 128 keys is 2,048 clocks of products
-// and takes some 2,700 (1.44 us), an item 7 us beyond its passes, a call 9.6 us before its
-// first pass.  8192 tokens of 32 + 8 heads 370 us (1.49 PFLOP/s, 0.76 of a large library
-// product's rate), 4 chunks of 518 to 2000 tokens under a window of 4096 501 us (1.28), 512
-// tokens 15.4.  What lies between: the issuer's way from one group of products to the next
+// and takes some 2,700 (1.43 us), an item 7 us beyond its passes, a call 8.5 us before its
+// first pass.  8192 tokens of 32 + 8 heads 361 us (1.52 PFLOP/s, 0.78 of a large library
+// product's rate), 4 chunks of 518 to 2000 tokens under a window of 4096 490 us (1.31), 512
+// tokens 13.9.  What lies between: the issuer's way from one group of products to the next
 // (four products in the queue cover 256 of its 290 to 420 clocks), and an item's rows, read
-// from tensor memory by cold code, before its successor's first products.  A softmax of half
-// the work took 1.36 us a pass, the products with V alone left out 1.07; an issuer for each
-// tile made 8192 tokens take 463 us (both tiles' products interleave, and then both softmaxes
-// wait), weights handed on in halves 5% more than 376, items overlapped in full 385.
+// from tensor memory (2,700 clocks a tile), before its successor's first products.  A softmax
+// of half the work took 1.36 us a pass, the products with V alone left out 1.07; an issuer for
+// each tile made 8192 tokens take 463 us (both tiles' products interleave, and then both
+// softmaxes wait), weights handed on in halves 5% more than 376, items overlapped in full 385.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
