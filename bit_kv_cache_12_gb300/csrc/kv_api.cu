@@ -156,6 +156,9 @@ kv_status_t kv_pool_create(const kv_pool_config_t* cfg, void* stream, kv_pool_t*
     if (c.sink_tokens < 0 || c.recent_tokens <= 0 || c.sink_tokens > 4096 || c.recent_tokens > 4096)
       return KV_ERR_INVALID_ARG;
   }
+  // more than any device holds; up to here no size below passes 64 bits
+  const double heads = (double)c.num_layers * c.num_kv_heads;
+  if (heads * c.num_pages * c.page_size > 0x1p45 || heads * c.max_seqs > 0x1p40) return KV_ERR_OOM;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return KV_ERR_CUDA;
   kv_pool_t* pool = new (std::nothrow) kv_pool_t();
