@@ -27,8 +27,9 @@
 // CTAs (39; the append spills 12 to 24 bytes for it), starting before the kernel in front has ended
 // (37.3), rows on their way while the table is formed or the unit before is worked
 // on (35.0 us, 5.3 TB/s: 0.79 of a plain copy; issue slots half in use).  Rotary
-// rows alone, 8192 tokens of 64 + 8 heads: 52 us, 5.8 TB/s, 0.86 of a plain copy
-// (54 to 57 with such prefetches).
+// rows alone, 8192 tokens of 64 + 8 heads: 50.7 us, 6.0 TB/s, 0.89 of a plain copy
+// (54 to 57 with such prefetches; with a warp's first rows in registers before the
+// table is formed 50.7 instead of 52).
 #include <cuda_fp8.h>
 
 #include <cmath>
@@ -245,15 +246,19 @@ __device__ __forceinline__ int code_offset(bool v, int t, int c) {
 // One head of 16 tokens, rotated and stored as bf16: lanes 8k .. 8k + 7 hold one
 // row, four rows per pass.  pos[t] < 0: the row is not touched.
 template <bool kPairs>
-__device__ __forceinline__ void rows_unit(const RopeParams& rp, const float* tab, const int* pos, const uint16_t* in,
-                                          int64_t in_stride, uint16_t* out, int64_t out_stride, int lane) {
+__device__ __forceinline__ void rows_load(Run (&r)[4], const RopeParams& rp, const int* pos, const uint16_t* in,
+                                          int64_t in_stride, int lane) {
   const Chunks ch = chunks_of<kPairs>(rp, lane);
-  Run r[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int t = 4 * u + (lane >> 3);
     load_run(r[u], in + t * in_stride, ch.a, ch.b, pos[t] >= 0);
   }
+}
+template <bool kPairs>
+__device__ __forceinline__ void rows_rotate(const Run (&r)[4], const RopeParams& rp, const float* tab, const int* pos,
+                                            uint16_t* out, int64_t out_stride, int lane) {
+  const Chunks ch = chunks_of<kPairs>(rp, lane);
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int t = 4 * u + (lane >> 3);
@@ -273,6 +278,14 @@ __device__ __forceinline__ void rows_unit(const RopeParams& rp, const float* tab
   }
 }
 
+template <bool kPairs>
+__device__ __forceinline__ void rows_unit(const RopeParams& rp, const float* tab, const int* pos, const uint16_t* in,
+                                          int64_t in_stride, uint16_t* out, int64_t out_stride, int lane) {
+  Run r[4];
+  rows_load<kPairs>(r, rp, pos, in, in_stride, lane);
+  rows_rotate<kPairs>(r, rp, tab, pos, out, out_stride, lane);
+}
+
 struct RopeArgs {
   const uint16_t* in[2];       // q, k
   uint16_t* out[2];
@@ -282,7 +295,33 @@ struct RopeArgs {
   int n_tokens;
 };
 
-// kPairs: rotated pairs are neighbouring channels (interleaved style)
+// The rows of a tile's tokens, unit by unit.  fill() forms the table; a warp's first rows are
+// on their way meanwhile (8192 tokens of 64 + 8 heads 55.0 -> 51.1 us).  kPairs: rotated pairs
+// are neighbouring channels (interleaved style).
+template <bool kPairs, class Fill>
+__device__ __forceinline__ void rotate_tile(const RopeArgs& a, const RopeParams& rp, const float* tab, const int* pos, int t0,
+                                            Fill fill) {
+  const int lane = threadIdx.x & 31, units = a.heads[0] + a.heads[1];
+  int u = blockIdx.y * kWarps + (threadIdx.x >> 5);
+  bool k = u >= a.heads[0];
+  Run r[4];
+  auto load = [&]() {
+    const int64_t is = k ? a.in_stride[1] : a.in_stride[0];
+    rows_load<kPairs>(r, rp, pos, (k ? a.in[1] : a.in[0]) + t0 * is + (u - (k ? a.heads[0] : 0)) * 128, is, lane);
+  };
+  if (u < units) load();
+  fill();
+  __syncthreads();
+  while (u < units) {
+    const int64_t os = k ? a.out_stride[1] : a.out_stride[0];
+    rows_rotate<kPairs>(r, rp, tab, pos, (k ? a.out[1] : a.out[0]) + t0 * os + (u - (k ? a.heads[0] : 0)) * 128, os, lane);
+    u += gridDim.y * kWarps;
+    if (u >= units) break;
+    k = u >= a.heads[0];
+    load();
+  }
+}
+
 template <bool kPairs>
 __global__ void __launch_bounds__(kThreads, 4) rope_kernel(RopeArgs a, const __grid_constant__ RopeParams rp) {
   __shared__ __align__(16) float tab[kTile * kTokStride];
@@ -292,21 +331,12 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(RopeArgs a, const __g
   const int t0 = blockIdx.x * kTile;
   if (threadIdx.x < kTile) pos[threadIdx.x] = t0 + (int)threadIdx.x < a.n_tokens ? a.positions[t0 + threadIdx.x] : -1;
   __syncthreads();
-  fill_table(tab, rp, pos);
-  __syncthreads();
-  const int lane = threadIdx.x & 31, units = a.heads[0] + a.heads[1];
-  for (int u = blockIdx.y * kWarps + (threadIdx.x >> 5); u < units; u += gridDim.y * kWarps) {
-    const bool k = u >= a.heads[0];
-    const int h = u - (k ? a.heads[0] : 0);
-    const int64_t is = k ? a.in_stride[1] : a.in_stride[0], os = k ? a.out_stride[1] : a.out_stride[0];
-    rows_unit<kPairs>(rp, tab, pos, (k ? a.in[1] : a.in[0]) + t0 * is + h * 128, is,
-                      (k ? a.out[1] : a.out[0]) + t0 * os + h * 128, os, lane);
-  }
+  rotate_tile<kPairs>(a, rp, tab, pos, t0, [&] { fill_table(tab, rp, pos); });
 }
 
 // The same with a position for each axis: a pair turns by that of its own.  Only the
-// table differs: 8192 tokens of 64 + 8 heads on three axes 57 us, 5.3 TB/s, 0.79 of a plain
-// copy (one position: 52).  64 tokens 4.7 us, 11 with the host's part.
+// table differs: 8192 tokens of 64 + 8 heads on three axes 51.1 us by graph replay, 5.9 TB/s,
+// 0.88 of a plain copy (one position: 50.5).  64 tokens 4.4 us, 11 with the host's part.
 template <bool kPairs>
 __global__ void __launch_bounds__(kThreads, 4)
     rope_axes_kernel(RopeArgs a, int64_t pos_stride, const __grid_constant__ RopeAxes axes,
@@ -321,33 +351,30 @@ __global__ void __launch_bounds__(kThreads, 4)
     reinterpret_cast<uint32_t*>(axis)[threadIdx.x - kTile] = reinterpret_cast<const uint32_t*>(axes.axis)[threadIdx.x - kTile];
   if (threadIdx.x < kTile) {
     const int t = threadIdx.x;
-    int low = t0 + t < a.n_tokens ? 0 : -1;    // below 0: a token without work
-    for (int x = 0; x < axes.n; ++x) {
-      at[x][t] = low < 0 ? -1 : a.positions[x * pos_stride + t0 + t];
-      low = min(low, at[x][t]);
+    const bool live = t0 + t < a.n_tokens;
+    int p[4], low = live ? 0 : -1;             // below 0: a token without work
+#pragma unroll
+    for (int x = 0; x < 4; ++x) p[x] = live && x < axes.n ? a.positions[x * pos_stride + t0 + t] : low;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {              // (no load above waits for another)
+      at[x][t] = p[x];
+      low = min(low, p[x]);
     }
     pos[t] = low;
   }
   __syncthreads();
-  const int n = rp.rd >> 1;
-  for (int i = threadIdx.x; i < kTile * 64; i += kThreads) {
-    const int t = i >> 6, f = i & 63;
-    if (f < n && pos[t] >= 0) {
-      const float2 cs = turn_cos_sin((unsigned long long)at[axis[f]][t] * rp.turn[f], rp.att);
-      float* d = tab + t * kTokStride + 4 * (f >> 3) + (f & 3) + 32 * ((f >> 2) & 1);
-      d[0] = cs.x;
-      d[64] = cs.y;
+  rotate_tile<kPairs>(a, rp, tab, pos, t0, [&] {
+    const int n = rp.rd >> 1;
+    for (int i = threadIdx.x; i < kTile * 64; i += kThreads) {
+      const int t = i >> 6, f = i & 63;
+      if (f < n && pos[t] >= 0) {
+        const float2 cs = turn_cos_sin((unsigned long long)at[axis[f]][t] * rp.turn[f], rp.att);
+        float* d = tab + t * kTokStride + 4 * (f >> 3) + (f & 3) + 32 * ((f >> 2) & 1);
+        d[0] = cs.x;
+        d[64] = cs.y;
+      }
     }
-  }
-  __syncthreads();
-  const int lane = threadIdx.x & 31, units = a.heads[0] + a.heads[1];
-  for (int u = blockIdx.y * kWarps + (threadIdx.x >> 5); u < units; u += gridDim.y * kWarps) {
-    const bool k = u >= a.heads[0];
-    const int h = u - (k ? a.heads[0] : 0);
-    const int64_t is = k ? a.in_stride[1] : a.in_stride[0], os = k ? a.out_stride[1] : a.out_stride[0];
-    rows_unit<kPairs>(rp, tab, pos, (k ? a.in[1] : a.in[0]) + t0 * is + h * 128, is,
-                      (k ? a.out[1] : a.out[0]) + t0 * os + h * 128, os, lane);
-  }
+  });
 }
 
 struct AppendFp8Args {
@@ -503,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_fp8_kernel(AppendFp8Args a
 // Slices of the heads per tile: about `per_sm` CTAs per SM, at most one unit per
 // warp.  A slice forms the tile's table again, so the append, whose units are
 // longer, takes fewer (8: ragged chunks 55 us, with 4: 61; a prompt of 8192 35,
-// with 16: 38) than the rotary rows (16: 52 us, with 8 or 32: 55).
+// with 16: 38) than the rotary rows (16: 51.1 us on three axes, with 8 or 24: 52).
 constexpr int kRopePerSm = 16, kAppendPerSm = 8;
 unsigned slices(const Pool& p, long long tiles, int units, int per_sm) {
   const long long want = ((long long)per_sm * p.sm_count + tiles - 1) / tiles;
