@@ -17,12 +17,13 @@
 // append of 8192 tokens took 15.0 us, reading 8 x 6500 back 57.8); two lanes share a block
 // and exchange its maximum.
 //
-// Measured (8 KV heads): append of 8192 tokens 10.1 us, and the same to read back, of which
-// 2.5 are the launch and rows and tiles fit in the L2 cache; ragged appends and reads of 8 x
-// 6500 tokens on average 50.3 and 44.8 us (273 MB: 5.4 and 6.1 TB/s, 0.81 and 0.91 of a plain
-// copy), with 60% of the issue slots in use; a token of each of 64 sequences 3.7 us, of one
+// Measured (8 KV heads): append of 8192 tokens 10.2 us, 8.3 to read them back, of which 2.5
+// are the launch and rows and tiles fit in the L2 cache; ragged appends and reads of 8 x 6500
+// tokens on average 51.9 and 44.7 us (273 MB: 5.3 and 6.1 TB/s, 0.79 and 0.91 of a plain
+// copy), with 60% of the issue slots in use; a token of each of 64 sequences 3.6 us, a
 // 1000-token prefix back 3.2 (launch and latency).  CTAs of 128 threads, a tile and up to two
-// heads each: with 256 the ragged append took 57.6 us.
+// heads each: with 256 the ragged append took 57.6 us.  Seven of them per SM for the append
+// (72 registers; with eight 10.6 us and 3.9), eight for the read.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -268,7 +269,7 @@ __device__ __forceinline__ void store_v(const uint4 (&x)[8], int t0, int t1, int
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 8) append_fp4_kernel(Fp4CacheArgs a) {
+__global__ void __launch_bounds__(kThreads, 7) append_fp4_kernel(Fp4CacheArgs a) {
   release_successor();
   after_predecessor();
   Place p;
@@ -312,6 +313,13 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b, float s) {
   return *reinterpret_cast<const uint32_t*>(&y);
 }
 
+// First to leave the L2 cache, so that the tiles stay: 8192 tokens of three layers in turn 10.1
+// -> 8.3 us; prompt attention over the rows behind it takes the same (78.1 and 78.1 us for 512
+// queries, 41.7 and 42.2 for 64).
+__device__ __forceinline__ void put_row(uint16_t* to, const uint32_t (&y)[4]) {
+  __stcs(reinterpret_cast<uint4*>(to), make_uint4(y[0], y[1], y[2], y[3]));
+}
+
 __device__ __forceinline__ void load_k(uint16_t* out, int64_t stride, int t0, int t1, int e, const uint8_t* tile, int lane) {
   const int c = lane & 15;
   uint32_t w[8], sc[8];
@@ -334,7 +342,7 @@ __device__ __forceinline__ void load_k(uint16_t* out, int64_t stride, int t0, in
       const float2 x = __half22float2(u32_as_h2(f[k]));
       y[k] = bf16_pair(x.x, x.y, s);
     }
-    *reinterpret_cast<uint4*>(out + t * stride + 8 * c) = make_uint4(y[0], y[1], y[2], y[3]);
+    put_row(out + t * stride + 8 * c, y);
   }
 }
 
@@ -365,7 +373,7 @@ __device__ __forceinline__ void load_v(uint16_t* out, int64_t stride, int t0, in
         const float2 a = __half22float2(u32_as_h2(f[i][2 * (u >> 1)])), b = __half22float2(u32_as_h2(f[i][2 * (u >> 1) + 1]));
         y[i] = u & 1 ? bf16_pair(a.y, b.y, s) : bf16_pair(a.x, b.x, s);
       }
-      *reinterpret_cast<uint4*>(out + t * stride + 8 * c) = make_uint4(y[0], y[1], y[2], y[3]);
+      put_row(out + t * stride + 8 * c, y);
     }
   }
 }
