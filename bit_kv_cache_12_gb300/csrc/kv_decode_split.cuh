@@ -195,8 +195,8 @@ __device__ __noinline__ void join_apart(const float* parts, int n_split, unsigne
 // timing.  Splits of a cluster (n_split at most kMaxCluster) read one another's parts from
 // shared memory; else the last CTA of the pair to arrive joins them through c.ws.  kRoom:
 // bytes of smem that may be used.  kApart: that join is a function of its own, and the
-// registers of the kernel's loops are allotted without it (the 4-bit kernel: 64 x 20,480
-// tokens 250 -> 245 us; the 8-bit one gains nothing and pays 0.4 us for the call).
+// registers of the kernel's loops are allotted without it (the 4-bit kernel with G = 2, 4: 64 x
+// 20,480 tokens 250 -> 245 us; the 8-bit one gains nothing and pays 0.4 us for the call).
 template <int G, int kWarps, int kHeadStride, int kRoom, bool kApart, class Chan>
 __device__ __forceinline__ void join_parts(const AttnCall& c, int Hq, int n_split, int cluster, unsigned* tickets,
                                            uint8_t* smem, int split, int pair, int b, int h, Chan at) {
