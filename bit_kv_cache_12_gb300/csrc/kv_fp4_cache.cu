@@ -4,7 +4,7 @@
 //   s = e4m3(max |x| / 6),  code = e2m1(x / s),  value = code * s * 2^e.
 // The codes are those of exact quotients.  max |x| has 8 bits and its product with
 // fl(1 / 6) comes out exactly where the quotient lies halfway between two e4m3 numbers (the
-// constant is off by 2^-25.4, less than half a last place of any such number), and on the
+// constant is off by 2^-25 of itself, less than half a last place of any such number), and on the
 // right side of it elsewhere.  x / s is the product with a reciprocal that is off by a last
 // place or two of fp32, rounded to fp16 on the way to e2m1: a quotient halfway between two
 // codes (3 bits) comes out exactly, and as x of 8 bits over s of 4 is otherwise at least 2^-9
