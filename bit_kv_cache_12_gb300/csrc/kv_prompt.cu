@@ -776,6 +776,7 @@ __device__ __forceinline__ int write_items(const PromptArgs& a, uint32_t tmem, u
     if (w.state == kStop) break;
     const bool any = w.state == kKeyed;
     float f0 = 0.f, f1 = 0.f;                  // of this thread's rows of the two tiles
+    const int rows = (w.m << a.shift) - w.row0 - 32 * warp;   // from this warp's first on
     uint32_t poison = 0;                       // whether they see a listed token
     if (any) {
       const int t0 = w.tile(w.i1 - 1) * kKeys;
@@ -805,6 +806,10 @@ __device__ __forceinline__ int write_items(const PromptArgs& a, uint32_t tmem, u
       }
       if (!__all_sync(0xffffffffu, wait(sh->bars + kOFull + tile, keyed & 1))) return item;
       fence_after();
+      if (tile * kRows >= rows) {              // none of this warp's exist (one token 8.5 -> 7.7 us; 512 13.9 -> 14.0)
+        if (lane == 0) arrive(sh->bars + kORead + tile);
+        continue;
+      }
       write_rows(a, w, tmem + ((uint32_t)(32 * warp) << 16) + 256 + 128 * tile, sm + kOffOut + warp * 4096,
                  tile * kRows + 32 * warp, tile ? f1 : f0, sh->bars + kORead + tile);
     }
