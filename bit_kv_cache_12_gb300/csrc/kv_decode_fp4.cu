@@ -21,8 +21,8 @@
 // use, tensor pipe 31%).  A warp takes two tiles at a step, copied whole (TMA, 4608 bytes)
 // two steps ahead, so that one tile's conversions run beside the other's products: with one
 // tile 64 sequences of 20,480 tokens took 317 us, with two 255.  Measured: 1024 tokens of 2
-// KV heads 5.0 us (6.3 with the host's part), 100,000 tokens of 8 27.0 us (115 MB, 4.3 TB/s),
-// 64 ragged sequences of 8k to 32k 296 us (1745 MB, 5.9 TB/s, 0.88 of a plain copy).
+// KV heads 4.8 us (5.7 with the host's part), 16,384 tokens of 8 9.7, 100,000 26.3 (115 MB,
+// 4.4 TB/s), 64 ragged sequences of 8k to 32k 296 us (1745 MB, 5.9 TB/s, 0.88 of a plain copy).
 #include <algorithm>
 
 #include "kv_decode_split.cuh"
@@ -364,22 +364,29 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp4_kernel(DecodeFp4Args a
                                                         h, [](int c) { return c; });
 }
 
+// Shared memory of which an SM has room for one CTA: where there are no more CTAs than SMs,
+// each gets one to itself (the scheduler puts two on some and leaves others idle: 144 CTAs
+// of 8 pairs of 16,384 tokens took 12.8 us, 152 9.8).
+constexpr uint32_t kSmemAlone = 120 << 10;
+static_assert(kSmem <= kSmemAlone, "room for one");
+uint32_t smem_of(const Pool& p, long long ctas) { return ctas <= p.sm_count ? kSmemAlone : kSmem; }
+
 // Microseconds that a call takes with each (sequence, KV head) pair in n splits of `units`
-// units, as far as they depend on n.  A warp takes 0.62 us for a unit where an SM has one
-// CTA and 0.88 where it has two (measured by graph replay: 8 pairs of 100,000 tokens in 19
-// splits, one CTA per SM, 28.2 us; in 38, two, 27.6).  Up to two CTAs per SM all run at
-// once; more come in waves, with 2.1 us for the start and end of each and an uneven last
-// one (512 pairs of 20,480 tokens: 263 us in one split, 247 in two, 255 in three; of 8,192:
-// 110, 115 and 120).  A join inside a cluster (up to 8 splits) costs 1 us, through memory
-// 0.1 and 0.13 for each split (1024 tokens of 2 pairs: 5.0 us in 8 splits, 6.9 in 9, 7.1 in
-// one).  What the largest length of a batch costs, so that shorter ones are even with it.
+// units, by graph replay.  A step of eight warps takes 1.0 us where an SM has one CTA and
+// 1.75 where it has two, which also start 1 us later (8 pairs of 100,000 tokens in 19 splits
+// 27.9 us, in 38 25.9; of 32,768 13.2 and 14.1).  Up to two CTAs per SM all run at once;
+// more come in waves, with 5.5 us for the start and end of each and an uneven last one (512
+// pairs of 20,480 tokens: 263 us in one split, 247 in two, 255 in three; of 8,192: 110, 115
+// and 120).  A join inside a cluster (up to 8 splits) costs 1.8 us, through memory 2.6 and
+// 0.045 for each split (1024 tokens of 2 pairs: 4.8 us in 8 splits, 6.2 in 9, 6.8 in one).
+// What the largest length of a batch costs, so that shorter ones are even with it.
 double cost_of(const Pool& p, long long pairs, long long units, int n) {
   const long long ctas = pairs * n, sms = p.sm_count;
-  const double steps = (double)(((units + n - 1) / n + kWarps - 1) / kWarps);
-  const double join = n == 1 ? 0. : (n <= kMaxCluster ? 1. : 0.1 + 0.13 * n);
-  if (ctas <= sms) return join + 0.62 * steps;
-  if (ctas <= 2 * sms) return join + 0.88 * steps;
-  return join + (double)ctas / (2 * sms) * (0.88 * steps + 2.1) + 0.21 * steps;
+  const double steps = (double)units / n / kWarps;
+  const double join = n == 1 ? 0. : (n <= kMaxCluster ? 1.8 : 2.6 + 0.045 * n);
+  if (ctas <= sms) return join + 1.0 * steps;
+  if (ctas <= 2 * sms) return join + 1.75 * steps + 1.;
+  return join + (double)ctas / (2 * sms) * (1.75 * steps + 5.5) + 0.42 * steps;
 }
 
 // More than one split only up to so many CTAs: what the workspace is sized by.
@@ -389,15 +396,19 @@ int most_splits(const Pool& p, long long pairs, long long units) {
 }
 
 template <int G>
-cudaError_t launch_t(const DecodeFp4Args& a, int device, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(decode_fp4_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+cudaError_t launch_t(const DecodeFp4Args& a, const Pool& p, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(decode_fp4_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemAlone);
   if (e != cudaSuccess) return e;
   const long long pairs = (long long)a.B * a.L.Hkv;
   if (pairs * a.n_split > INT32_MAX) return cudaErrorInvalidValue;
-  DecodeFp4Args b = a;
-  b.cluster = a.n_split > 1 && a.n_split <= kMaxCluster &&
-              pairs <= resident_clusters<decode_fp4_kernel<G>>(device, a.n_split, kThreads, kSmem);
-  return launch_dependent(decode_fp4_kernel<G>, dim3((unsigned)(pairs * a.n_split)), kThreads, kSmem, s,
+  DecodeFp4Args b = a;                         // (b.cluster is 0)
+  uint32_t smem = smem_of(p, pairs * a.n_split);
+  if (a.n_split > 1 && a.n_split <= kMaxCluster) {
+    // fewer clusters of CTAs that have an SM to themselves fit than of others
+    if (smem == kSmemAlone && pairs > resident_clusters<decode_fp4_kernel<G>, kSmemAlone>(p.device, a.n_split, kThreads)) smem = kSmem;
+    b.cluster = smem == kSmemAlone || pairs <= resident_clusters<decode_fp4_kernel<G>, kSmem>(p.device, a.n_split, kThreads);
+  }
+  return launch_dependent(decode_fp4_kernel<G>, dim3((unsigned)(pairs * a.n_split)), kThreads, smem, s,
                           b.cluster ? a.n_split : 1, b);
 }
 
@@ -437,10 +448,10 @@ cudaError_t launch_decode_fp4(const Pool& p, const Fp4Layer& L, int layer, int B
                   p.tickets + (size_t)layer * p.cfg.max_seqs * p.cfg.num_kv_heads, p.err,
                   p.test_wait_polls > 0 ? p.test_wait_polls : kPolls, p.test_stall_first_copy};
   switch (p.G) {
-    case 1: return launch_t<1>(a, p.device, s);
-    case 2: return launch_t<2>(a, p.device, s);
-    case 4: return launch_t<4>(a, p.device, s);
-    default: return launch_t<8>(a, p.device, s);
+    case 1: return launch_t<1>(a, p, s);
+    case 2: return launch_t<2>(a, p, s);
+    case 4: return launch_t<4>(a, p, s);
+    default: return launch_t<8>(a, p, s);
   }
 }
 

@@ -349,7 +349,7 @@ cudaError_t launch_t(const DecodeFp8Args& a, int device, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const long long pairs = (long long)a.B * a.L.Hkv;
   DecodeFp8Args b = a;
-  b.cluster = a.n_split > 1 && a.n_split <= kMaxCluster && pairs <= resident_clusters<decode_fp8_kernel<G>>(device, a.n_split, kThreads, kSmem);
+  b.cluster = a.n_split > 1 && a.n_split <= kMaxCluster && pairs <= resident_clusters<decode_fp8_kernel<G>, kSmem>(device, a.n_split, kThreads);
   return launch_dependent(decode_fp8_kernel<G>, dim3((unsigned)(pairs * a.n_split)), kThreads, kSmem, s,
                           b.cluster ? a.n_split : 1, b);
 }

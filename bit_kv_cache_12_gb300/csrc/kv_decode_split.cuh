@@ -281,15 +281,15 @@ __device__ __forceinline__ void join_parts(const AttnCall& c, int Hq, int n_spli
 
 // Clusters of n CTAs that the pool's device (the current one) holds at once.
 constexpr int kDevices = 16;                                 // remembered: the first 16 devices
-template <auto kernel>
-int resident_clusters(int device, int n, int threads, size_t smem) {
+template <auto kernel, size_t kSmemBytes>
+int resident_clusters(int device, int n, int threads) {
   static std::atomic<int> known[kDevices][kMaxCluster + 1];  // + 1; 0: not asked yet
   int have = device < kDevices ? known[device][n].load(std::memory_order_relaxed) : 0;
   if (have == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(n);
     cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = kSmemBytes;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim = {(unsigned)n, 1, 1};
