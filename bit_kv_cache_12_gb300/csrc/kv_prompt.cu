@@ -108,7 +108,8 @@ struct Shared {
   int abort;
   int steps;                                   // items looked at so far
   int given;                                   // items published so far
-  int taken;                                   // an item taken on but not published yet, else -1
+  int taken[2];                                // blocks taken on but not published: the one at hand, and (when that one
+                                               // never will be) the one that the scheduler had been asked for; else -1
   int next[4];                                 // writing warps, at their end: the item whose rows would have come next
 };
 constexpr uint32_t kSmem = kOffInfo + sizeof(Shared) + 1024;
@@ -351,7 +352,7 @@ __device__ __forceinline__ void walk(const PromptArgs& a, const CUtensorMap* q, 
     if (lane == 0) {
       sh->work[slot] = w;
       sh->given = item + 1;
-      sh->taken = -1;
+      sh->taken[0] = -1;
       arrive(sh->bars + kItem + slot);
     }
     __syncwarp();
@@ -390,7 +391,7 @@ __device__ __forceinline__ void walk(const PromptArgs& a, const CUtensorMap* q, 
         : "=r"(got), "+r"(x)
         : "r"(smem_u32(&sh->cancel))
         : "memory");
-    if (lane == 0) sh->taken = got ? x : -1;
+    if (lane == 0) sh->taken[!ok] = got ? x : -1;
     if (!ok) return;
     if (!__all_sync(0xffffffffu, got)) break;
   }
@@ -830,12 +831,12 @@ __device__ __forceinline__ void abandon(const PromptArgs& a, const Shared* sh, i
   const int given = sh->given;
   const float nan = __uint_as_float(0x7FC00000u);
 #pragma unroll 1
-  for (int item = first; item <= given; ++item) {
+  for (int item = first; item < given + 2; ++item) {
     Work w;
     if (item < given)
       w = sh->work[item & (kItems - 1)];
-    else if (sh->taken < 0 || !find_work(a, sh->taken, w))
-      return;
+    else if (sh->taken[item - given] < 0 || !find_work(a, sh->taken[item - given], w))
+      continue;
     if (w.state == kStop) return;
 #pragma unroll 1
     for (int tile = 0; tile < 2; ++tile) {     // this thread's rows
@@ -888,7 +889,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     sh->abort = 0;
     sh->steps = 0;
     sh->given = 0;
-    sh->taken = blockIdx.x;
+    sh->taken[0] = blockIdx.x;
+    sh->taken[1] = -1;
   }
   if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh->tmem)),
