@@ -430,7 +430,7 @@ kv_status_t kv_debug_stall_first_copy(kv_pool_t* pool, int32_t enable, int32_t m
   // those decodes wait for their copies in flight with the same limit: it has to outlast them
   const int kind = pool->p.cfg.kind;
   if (kind != KV_POOL_FP8 && kind != KV_POOL_FP4 && max_polls > 0 && max_polls < 1024) return KV_ERR_INVALID_ARG;
-  pool->p.test_stall_first_copy = enable ? 1 : 0;
+  pool->p.test_stall_first_copy = enable == 2 ? 2 : enable != 0;
   pool->p.test_wait_polls = max_polls;
   return KV_OK;
 }

@@ -108,7 +108,8 @@ struct Shared {
   int converted;                               // passes whose K is in shared memory
   int steps;                                   // items looked at so far
   int given;                                   // items published so far
-  int taken;                                   // an item taken on but not published yet, else -1
+  int taken[2];                                // blocks taken on but not published: the one at hand, and (when that one
+                                               // never will be) the one that the scheduler had been asked for; else -1
   int next[8];                                 // softmax warps, at their end: the item whose rows would have come next
 };
 constexpr uint32_t kSmem = kOffInfo + sizeof(Shared) + 1024;
@@ -120,7 +121,8 @@ struct PrefillFp8Args {
   int n_seqs, max_q, Hq, G, n_split, q_blocks;
   int* err;
   int polls;
-  int stall;                                   // test hook: CTA 0's walker withholds its first item's last pass
+  int stall;                                   // test hook: CTA 0's walker (1) or its converters (2) withhold its first
+                                               // item's last pass
 };
 
 // ---- tcgen05 ----------------------------------------------------------------
@@ -251,6 +253,7 @@ __device__ __forceinline__ void convert_tiles(const PrefillFp8Args& a, uint8_t* 
     const uint32_t present = p.blocks;
     const int t0 = p.t0, keys = p.keys;
     const uint4 zero = make_uint4(0, 0, 0, 0);
+    if (a.stall == 2 && last && blockIdx.x == 0) return;
     if (it >= 2 && !__all_sync(0xffffffffu, wait(sh->bars + kKEmpty + stage, ph))) return;
     uint8_t* sk = sm + kOffK + stage * kOperand;
 #pragma unroll
@@ -373,7 +376,7 @@ __device__ __forceinline__ bool walk_item(const PrefillFp8Args& a, const Work& w
                     (a.c.window && t0 < w.keys - a.c.window && t0 + kKeys > w.sinks);
       }
       __syncwarp();
-      if (a.stall && last && blockIdx.x == 0) return false;
+      if (a.stall == 1 && last && blockIdx.x == 0) return false;
       if (lane == 0) arrive(sh->bars + kPass + (n & (kRing - 1)));
       ++n;
     } while (left);
@@ -394,7 +397,7 @@ __device__ __forceinline__ void walk(const PrefillFp8Args& a, Shared* sh, const 
     if (lane == 0) {
       sh->work[slot] = w;
       sh->given = item + 1;
-      sh->taken = -1;
+      sh->taken[0] = -1;
       arrive(sh->bars + kItem + slot);
     }
     __syncwarp();
@@ -429,7 +432,7 @@ __device__ __forceinline__ void walk(const PrefillFp8Args& a, Shared* sh, const 
         : "=r"(got), "+r"(x)
         : "r"(smem_u32(&sh->cancel))
         : "memory");
-    if (lane == 0) sh->taken = got ? x : -1;
+    if (lane == 0) sh->taken[!ok] = got ? x : -1;
     if (!ok) return;
     if (!__all_sync(0xffffffffu, got)) break;
   }
@@ -787,12 +790,12 @@ __device__ __forceinline__ void abandon(const PrefillFp8Args& a, const Shared* s
   const int i = threadIdx.x, given = sh->given;   // this thread's row of a block
   const float nan = __uint_as_float(0x7FC00000u);
 #pragma unroll 1
-  for (int item = first; item <= given; ++item) {
+  for (int item = first; item < given + 2; ++item) {
     Work w;
     if (item < given)
       w = sh->work[item & (kItems - 1)];
-    else if (sh->taken < 0 || !find_work(a, sh->taken, w))
-      return;
+    else if (sh->taken[item - given] < 0 || !find_work(a, sh->taken[item - given], w))
+      continue;
     if (w.state == kStop) return;
     const Row row(a, w, i);
     if (!row.live) continue;
@@ -836,7 +839,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
     sh->converted = 0;
     sh->steps = 0;
     sh->given = 0;
-    sh->taken = blockIdx.x;
+    sh->taken[0] = blockIdx.x;
+    sh->taken[1] = -1;
   }
   if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh->tmem)),

@@ -377,7 +377,8 @@ kv_status_t kv_decode_attention_noalloc(kv_pool_t* pool, int32_t layer, int32_t 
  * kv_decode_attention_fp8's first CTA waits for a copy that is never started,
  * and kv_prefill_attention_fp8's first CTA for keys that are never handed over;
  * both end the same way (the decode skips that warp's share of the tokens, the
- * prompt rows that CTA had taken on and not finished become NaN).  On an FP4 pool
+ * prompt rows that CTA had taken on and not finished become NaN; with enable = 2 the
+ * prompt's keys are handed over and not taken up, so that its blocks of rows queue).  On an FP4 pool
  * the first warp of kv_decode_attention_fp4's first CTA waits like that, and on a
  * pool of any kind kv_prompt_attention's first CTA.  max_polls > 0
  * replaces the default poll limit of those waits (one to four seconds; a poll

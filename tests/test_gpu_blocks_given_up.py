@@ -3,8 +3,10 @@ that it could not publish, and has asked the scheduler for another.  All of thei
 
 import numpy as np
 import pytest
+import torch
 
 from bit_kv_cache_12_gb300 import native
+from tests.fp8_util import Setup, bf16, f64, i32
 from tests.test_gpu_prompt import Prompt
 
 pytestmark = pytest.mark.gpu
@@ -39,3 +41,30 @@ def test_prompt_blocks_behind_a_full_queue(cuda_lib):
     np.testing.assert_array_equal(again, want)
     np.testing.assert_array_equal(again_lse, want_lse)
     p.close()
+
+
+def test_prefill_blocks_behind_a_full_queue(cuda_lib):
+    """1,200 blocks with one pass each: the queue fills before the ring of passes does."""
+    s = Setup(64, 8, 16, 150, 40, seed=22)
+    s.fill(spread=0)
+    count = [32] * 150
+    n = s.rng.integers(32, 41, 150).tolist()
+    q = bf16(s.rng.standard_normal((32 * 150, 64, 128)))
+    cu, length, table = i32(np.arange(151) * 32), i32(n), i32(s.table)
+    need = native.kv_prefill_workspace_bytes(s.pool.handle, 150, 32, 40)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def run(stalled):
+        out = torch.full((q.shape[0], 64, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((q.shape[0], 64), 7.0, device="cuda")
+        native.kv_debug_stall_first_copy(s.pool.handle, 2 if stalled else 0, 2000 if stalled else 0)
+        native.kv_prefill_attention_fp8(s.pool.handle, 0, 150, q, cu, length, table, s.width, 32, 40, 0.1, 0, 0, out, lse, ws, need)
+        torch.cuda.synchronize()
+        assert s.pool.error() == (KV_DEVERR_TIMEOUT if stalled else 0)
+        return f64(out), f64(lse)
+
+    want, got, again = run(0), run(1), run(0)
+    check(*got, *want, 8, 32)
+    np.testing.assert_array_equal(again[0], want[0])
+    np.testing.assert_array_equal(again[1], want[1])
+    s.pool.close()
