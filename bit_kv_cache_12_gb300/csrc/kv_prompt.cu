@@ -78,8 +78,10 @@ constexpr int kRing = 4;                       // of barriers that may run ahead
 
 // Barriers.  kData: V of a pass and K of the next (an item's first K comes with q).  kGo:
 // all that the products of a pass wait for, a ring for each tile: P, and for tile 0 that the
-// data are there.  kSFull: a tile's scores of a pass; those of tile 1 also say that what came
-// before them is done with, the products of the pass before and its values among it.
+// data are there; for tile 1 that the loader has seen its scores.  kSFull: a tile's scores of a
+// pass; those of tile 1 also say that what came before them is done with, the products of the
+// pass before and its values among it.  A wait looks at one bit of its barrier's phase, so no
+// barrier may complete twice before everyone who waits for it has looked.
 enum { kData = 0, kGo = kData + kStages, kLooked = kGo + 2 * kRing, kQFull = kLooked + kRing, kSFull = kQFull + 2,
        kOFull = kSFull + 2, kORead = kOFull + 2, kLast = kORead + 2, kDrain = kLast + 4, kCancel, kItem, kFree = kItem + kItems,
        kBars = kFree + kItems };
@@ -211,7 +213,10 @@ struct Maps {
 
 // The loads of an item: false where a wait ran out.  Pass g brings V of its own and K of the
 // next pass, into stages g and g + 1 modulo two: free when the scores of pass g - 1 are
-// complete, and the products of pass g - 2 with them.  q, g: items and passes loaded so far.
+// complete, and the products of pass g - 2 with them.  K of pass g is there before that: only
+// the loader's word that it has seen those scores holds back the next ones, of the same barrier
+// (with a ring of barriers instead the softmax spilled more, 8192 tokens 2.5% slower).  q, g:
+// items and passes loaded so far.
 __device__ __forceinline__ bool load_item(const PromptArgs& a, const Maps& maps, const Work& w, bool withhold, uint8_t* sm,
                                           Shared* sh, const Waiter& wait, int& q, int& g) {
   const int lane = threadIdx.x & 31, tokens = kRows >> a.shift, h = w.h, k0 = w.k0, q0 = w.c0 + (w.row0 >> a.shift);
@@ -222,7 +227,6 @@ __device__ __forceinline__ bool load_item(const PromptArgs& a, const Maps& maps,
   };
   for (int i = w.i0; i < w.i1; ++i, ++g) {
     const int stage = g % kStages, last = i + 1 == w.i1;
-    if (g && !__all_sync(0xffffffffu, wait(sh->bars + kSFull + 1, (g - 1) & 1))) return false;
     if (i == w.i0) {                           // q, in the place of the item's before, whose last scores these are
       if (lane == 0) {
         for (int tile = 0; tile < 2; ++tile) {
@@ -239,6 +243,11 @@ __device__ __forceinline__ bool load_item(const PromptArgs& a, const Maps& maps,
       if (!last) load(kOffK + (g + 1) % kStages * kOperand, maps.k, h, k0 + w.tile(i + 1) * kKeys, kData + stage);
       load(kOffV + stage * kOperand, maps.v, h, k0 + w.tile(i) * kKeys, kData + stage);
     }
+    if (!__all_sync(0xffffffffu, wait(sh->bars + kSFull + 1, g & 1))) {
+      ++g;                                     // (its loads are on their way)
+      return false;
+    }
+    if (lane == 0) arrive(sh->bars + kGo + kRing + g % kRing);
   }
   __syncwarp();
   return true;
@@ -868,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(sh->bars + kGo + i, 4 + 1);    // softmax warps, looking warp
-      mbar_init(sh->bars + kGo + kRing + i, 4);
+      mbar_init(sh->bars + kGo + kRing + i, 4 + 1);   // softmax warps, loader
       mbar_init(sh->bars + kLooked + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
