@@ -85,7 +85,7 @@ bool valid_rows(const void* p, int64_t stride, int heads) {
 // sequences and queries of a prompt call; its grid: a CTA per 256 rows and KV head
 bool valid_prefill(const Pool& p, int32_t n_seqs, int32_t max_q) {
   if (n_seqs <= 0 || n_seqs > p.cfg.max_seqs || max_q < 0 || max_q > kvint2::kMaxDecodeLen) return false;
-  return ((int64_t)max_q * p.G + 255) / 256 * n_seqs * p.cfg.num_kv_heads <= INT32_MAX;
+  return std::max<int64_t>(((int64_t)max_q * p.G + 255) / 256, 1) * n_seqs * p.cfg.num_kv_heads <= INT32_MAX;
 }
 
 // the arguments the two rotary calls share

@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 8) read_fp4_kernel(Fp4CacheArgs a) {
 
 template <class K>
 cudaError_t launch_cache(K kernel, const Pool& p, const Fp4Layer& L, const Fp4Tokens& t, const Fp4Rows& rows, cudaStream_t s) {
-  if (t.n_seqs == 0 || t.max_tokens == 0) return cudaSuccess;
+  if (t.n_seqs == 0) return cudaSuccess;       // (with a bound of 0 a CTA for each sequence still looks at its count)
   Fp4CacheArgs a{L, t, rows, (int)(((long long)t.max_tokens + 30) / kTile), p.err};   // n tokens touch at most that many tiles
   const dim3 grid((unsigned)((long long)t.n_seqs * a.tiles), (2 * L.Hkv + kWarps - 1) / kWarps);
   return launch_dependent(kernel, grid, kThreads, 0, s, 1, a);

@@ -969,7 +969,8 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(PrefillFp8Args a) {
     a.c.lse[row] = nan ? __uint_as_float(0x7FC00000u) : (sum == 0.f ? -INFINITY : top + logf(sum));
 }
 
-long long q_blocks(const Pool& p, int max_q) { return ((long long)max_q * p.G + 2 * kRows - 1) / (2 * kRows); }
+// of a sequence, at most; one where the bound is 0, which looks at the sequence's count
+long long q_blocks(const Pool& p, int max_q) { return std::max(((long long)max_q * p.G + 2 * kRows - 1) / (2 * kRows), 1ll); }
 
 // Splits of the keys: where the blocks of rows fill less than half of the SMs,
 // as many as fit in one wave, of at least four tiles each.
@@ -977,7 +978,7 @@ int splits(const Pool& p, int n_seqs, int max_q, long long max_len, int window, 
   long long keys = max_len;
   if (window) keys = std::min(keys, (long long)window + n_sink + std::min<long long>(max_q, 2 * kRows / p.G) + 2 * kKeys);
   const long long tiles = (keys + kKeys - 1) / kKeys, blocks = q_blocks(p, max_q) * n_seqs * p.cfg.num_kv_heads;
-  if (blocks == 0) return 1;
+  if (max_q == 0) return 1;
   return (int)std::max(1ll, std::min<long long>({p.sm_count / blocks, tiles / 4, kMaxSplits}));
 }
 
@@ -1002,7 +1003,6 @@ size_t prefill_fp8_workspace_up_to(const Pool& p, int n_seqs, int max_q, int max
 
 cudaError_t launch_prefill_fp8(const Pool& p, const Fp8Store& f, int layer, int n_seqs, const int32_t* cu_q,
                                int max_q, const AttnCall& c, cudaStream_t s) {
-  if (max_q == 0) return cudaSuccess;
   PrefillFp8Args a{fp8_layer(p, f, layer), c, cu_q, n_seqs, max_q, p.cfg.num_q_heads, p.G,
                    splits(p, n_seqs, max_q, c.max_len, c.window, c.n_sink), (int)q_blocks(p, max_q), p.err,
                    p.test_wait_polls > 0 ? p.test_wait_polls : kPolls, p.test_stall_first_copy};

@@ -1008,7 +1008,8 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(PromptArgs a) {
     a.c.lse[row] = nan ? __uint_as_float(0x7FC00000u) : (sum == 0.f ? -INFINITY : top + logf(sum));
 }
 
-long long q_blocks(const Pool& p, int max_q) { return ((long long)max_q * p.G + 2 * kRows - 1) / (2 * kRows); }
+// of a sequence, at most; one where the bound is 0, which looks at the sequence's count
+long long q_blocks(const Pool& p, int max_q) { return std::max(((long long)max_q * p.G + 2 * kRows - 1) / (2 * kRows), 1ll); }
 
 // Splits of the keys: where the blocks of rows fill less than half of the SMs, as many as
 // fit in one wave, of at least four tiles each.
@@ -1016,7 +1017,7 @@ int splits(const Pool& p, int n_seqs, int max_q, long long max_k, int window, in
   long long keys = max_k;
   if (window) keys = std::min(keys, (long long)window + n_sink + std::min<long long>(max_q, 2 * kRows / p.G) + 2 * kKeys);
   const long long tiles = (keys + kKeys - 1) / kKeys, blocks = q_blocks(p, max_q) * n_seqs * p.cfg.num_kv_heads;
-  if (blocks == 0) return 1;
+  if (max_q == 0) return 1;
   return (int)std::max(1ll, std::min<long long>({p.sm_count / blocks, tiles / 4, kMaxSplits}));
 }
 
@@ -1052,7 +1053,6 @@ size_t prompt_workspace_up_to(const Pool& p, int n_seqs, int max_q, int max_k) {
 }
 
 cudaError_t launch_prompt(const Pool& p, const PromptCall& c, cudaStream_t s) {
-  if (c.max_q == 0) return cudaSuccess;
   PromptArgs a{c, p.cfg.num_q_heads, p.cfg.num_kv_heads, p.G, __builtin_ctz(p.G), splits(p, c.n_seqs, c.max_q, c.max_k, c.window, c.n_sink),
                (int)q_blocks(p, c.max_q), p.err, p.test_wait_polls > 0 ? p.test_wait_polls : kPolls, p.test_stall_first_copy};
   const long long ctas = (long long)a.q_blocks * c.n_seqs * a.Hkv * a.n_split;

@@ -207,7 +207,8 @@ kv_status_t kv_quantize_pack_f32(kv_pool_t* pool, int32_t layer, int32_t tensor,
  *   page_table  device int32 [n_seqs][max_pages_per_seq]: history position p
  *               of sequence i lives in page page_table[i][p / page_size]
  *   max_tokens_per_seq  host bound on tokens of any one sequence (sizes the
- *               grid; sequences above it are flagged and truncated)
+ *               grid; sequences above it are flagged and truncated; with 0
+ *               nothing is done and no count is looked at)
  * Tiles partly covered keep the other tokens' bits (appends may continue a
  * partly filled page).  Rotation runs on the tcgen05 tensor cores with R split
  * into two bf16 terms (about 16 significant bits), fp32 accumulation; the
