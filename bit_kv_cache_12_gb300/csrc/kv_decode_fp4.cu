@@ -7,22 +7,24 @@
 //
 // Both products are m16n8k16 tensor-core steps with the cached tile as the A operand and
 // the (up to 8) query heads of the KV head as the 8 columns.  A code pair becomes an fp16
-// register by one conversion.  K's scales multiply the operand (code * scale has 6 bits:
-// exact); which channels a step takes is free as long as q's rows agree, and with 32
-// neighbouring ones to a lane it needs two scales per token.  V's scales ride on the
-// weights, the B operand: 16 rows of A are 16 channels of one block.  q enters as fp16
-// scaled per head by a power of two (largest element in [2^14, 2^15)): exact for bf16's 8
-// bits down to 2^-32 of it.  The weights are rounded to fp16, and again times sV; M lags
-// so that the largest is between 2^3 and 2^7 (2^7 * 448 is in fp16's range), and weights
-// below 2^-28 of the largest are dropped.
+// register by one conversion.  The scales multiply the operand (code * scale has 6 bits and
+// lies between 2^-10 and 2688: exact); which channels a step of K takes is free as long as
+// q's rows agree, and with 32 neighbouring ones to a lane it needs two scales per token.  Of
+// V the 16 rows of A are 16 channels of one block, a scale for each token.  (On the weights
+// instead, the other operand, V's scales take half the multiplications and 64 sequences of 8k
+// to 32k 295 us instead of 298; but a product below fp16's range is lost, 2^-19 of the largest
+// weight where the scales are smallest, and tails of thousands of tokens with it.)  q
+// enters as fp16 scaled per head by a power of two (largest element in [2^14, 2^15)): exact
+// for bf16's 8 bits down to 2^-32 of it.  The weights are rounded to fp16; M lags so that the
+// largest is between 2^7 and 2^15, and weights below 2^-32 of the largest are dropped.
 //
 // Bound: the cache's bytes (144 per token and KV head) for batches, latency for one short
 // sequence, between them the instructions that turn codes into operands (issue slots 62% in
 // use, tensor pipe 31%).  A warp takes two tiles at a step, copied whole (TMA, 4608 bytes)
 // two steps ahead, so that one tile's conversions run beside the other's products: with one
 // tile 64 sequences of 20,480 tokens took 317 us, with two 255.  Measured: 1024 tokens of 2
-// KV heads 4.8 us (5.7 with the host's part), 16,384 tokens of 8 9.7, 100,000 26.3 (115 MB,
-// 4.4 TB/s), 64 ragged sequences of 8k to 32k 296 us (1745 MB, 5.9 TB/s, 0.88 of a plain copy).
+// KV heads 4.8 us (5.5 with the host's part), 16,384 tokens of 8 9.7, 100,000 26.5 (115 MB,
+// 4.4 TB/s), 64 ragged sequences of 8k to 32k 298 us (1745 MB, 5.9 TB/s, 0.87 of a plain copy).
 #include <algorithm>
 
 #include "kv_decode_split.cuh"
@@ -38,7 +40,7 @@ constexpr int kUnit = 2 * kTile;               // tokens of a step: two tiles
 constexpr uint32_t kUnitBytes = 2 * kFp4TileBytes;
 constexpr int kStages = 3;                     // units in flight per warp
 constexpr int kPolls = 1 << 18;                // bound of a copy's wait: a poll suspends for up to 3.7 us, so about a second
-constexpr float kRaise = 7.f, kHead = 3.f;     // M moves when x > M + 7, to the largest x - 3
+constexpr float kRaise = 15.f, kHead = 7.f;    // M moves when x > M + 15, to the largest x - 7
 constexpr uint32_t kRing = kWarps * kStages * kUnitBytes;
 constexpr uint32_t kSmem = kRing + kWarps * kStages * 8;
 // Results of the warps in shared memory (over the ring): heads 136 floats apart, so that a
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp4_kernel(DecodeFp4Args a
         keep[t] = (lo & 1 ? 0xFFu : 0u) | (lo & 2 ? 0xFF00u : 0u) | (hi & 1 ? 0xFF0000u : 0u) | (hi & 2 ? 0xFF000000u : 0u);
       }
     }
-    // as differences: where M is large, M + 7 is rounded by as much as that
+    // as differences: where M is large, M + 15 is rounded by as much as that
     const float t0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
     const float t1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
     if (__any_sync(0xffffffffu, fmaxf(t0 - M0, t1 - M1) > kRaise)) {
@@ -301,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_fp4_kernel(DecodeFp4Args a
         for (int w = 0; w < 4; ++w) {
           uint32_t v0, v1, v2, v3;
           codes4((&v.x)[w], v0, v1, v2, v3);
-          const uint32_t s = (&g.x)[w] & keep[t];
-          mma_f16(o[4 * q + w], v0, v1, v2, v3, mul2(p[t][0], cvt_lo(s)), mul2(p[t][1], cvt_hi(s)));
+          const uint32_t s = (&g.x)[w] & keep[t], lo = cvt_lo(s), hi = cvt_hi(s);
+          mma_f16(o[4 * q + w], mul2(v0, lo), mul2(v1, lo), mul2(v2, hi), mul2(v3, hi), p[t][0], p[t][1]);
         }
       }
     }
