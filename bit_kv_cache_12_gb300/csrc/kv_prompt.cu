@@ -159,6 +159,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&y);
 }
 
+// Whether a sequence's rows [c0, c1) and [k0, k1) are ones, as many as it may have.  (Differences
+// are taken of what is known to be in order: others could pass 32 bits.)
+__device__ __forceinline__ bool rows_in_range(const PromptArgs& a, int c0, int c1, int k0, int k1) {
+  return c0 >= 0 && c1 >= c0 && c1 - c0 <= a.c.max_q && c1 <= a.c.q_rows && k0 >= 0 && k1 >= k0 && k1 - k0 <= a.c.max_k &&
+         k1 <= a.c.kv_rows;
+}
+
 // Item x of the grid; false where it has no rows (the whole warp calls this).
 __device__ __forceinline__ bool find_work(const PromptArgs& a, int x, Work& w) {
   // blocks of a sequence from its last (most keys) to its first
@@ -173,14 +180,14 @@ __device__ __forceinline__ bool find_work(const PromptArgs& a, int x, Work& w) {
   w.s = y % a.c.n_seqs;
   const int blk = a.q_blocks - 1 - (int)(y / a.c.n_seqs);
   w.c0 = a.c.cu_q[w.s];
-  w.m = a.c.cu_q[w.s + 1] - w.c0;
   w.k0 = a.c.cu_k[w.s];
-  w.n = a.c.cu_k[w.s + 1] - w.k0;
-  if (w.m < 0 || w.m > a.c.max_q || w.n < 0 || w.n > a.c.max_k || w.c0 < 0 || (long long)w.c0 + w.m > a.c.q_rows || w.k0 < 0 ||
-      (long long)w.k0 + w.n > a.c.kv_rows) {
+  const int c1 = a.c.cu_q[w.s + 1], k1 = a.c.cu_k[w.s + 1];
+  if (!rows_in_range(a, w.c0, c1, w.k0, k1)) {
     if ((threadIdx.x & 31) == 0 && blk == 0 && w.split == 0 && w.h == 0) flag_error(a.err, KV_DEVERR_SEQ_RANGE);
     return false;
   }
+  w.m = c1 - w.c0;
+  w.n = k1 - w.k0;
   w.row0 = blk * 2 * kRows;
   if ((long long)w.row0 >= (long long)w.m * a.G) return false;
   w.pos0 = w.n - w.m;
@@ -980,10 +987,8 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(PromptArgs a) {
   const long long t = item / a.Hq;
   const int s = (int)(t / a.c.max_q), i = (int)(t % a.c.max_q);
   if (s >= a.c.n_seqs) return;
-  const int c0 = a.c.cu_q[s], m = a.c.cu_q[s + 1] - c0, k0 = a.c.cu_k[s], n = a.c.cu_k[s + 1] - k0;
-  if (m > a.c.max_q || i >= m || n < 0 || n > a.c.max_k || c0 < 0 || (long long)c0 + m > a.c.q_rows || k0 < 0 ||
-      (long long)k0 + n > a.c.kv_rows)
-    return;
+  const int c0 = a.c.cu_q[s], c1 = a.c.cu_q[s + 1];
+  if (!rows_in_range(a, c0, c1, a.c.cu_k[s], a.c.cu_k[s + 1]) || i >= c1 - c0) return;
   const float* part = static_cast<const float*>(a.c.ws) + (size_t)item * a.n_split * kPart;
   const float mine = lane < a.n_split ? part[(size_t)lane * kPart] : -INFINITY;
   const bool nan = __any_sync(0xffffffffu, isnan(mine));
