@@ -156,6 +156,12 @@ __device__ __forceinline__ uint32_t cvt_hi(uint32_t w) {
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) { return h2_as_u32(__floats2half2_rn(a, b)); }
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
+// Whether a sequence's rows [c0, c1) are ones, as many as it may have.  (Their difference is taken
+// when they are known to be in order: others could pass 32 bits.)
+__device__ __forceinline__ bool rows_in_range(const PrefillFp8Args& a, int c0, int c1) {
+  return c0 >= 0 && c1 >= c0 && c1 - c0 <= a.max_q;
+}
+
 // Item x of the grid; false where it has no rows (the whole warp calls this).
 __device__ __forceinline__ bool find_work(const PrefillFp8Args& a, int x, Work& w) {
   // blocks of a sequence from its last (most keys) to its first
@@ -166,13 +172,14 @@ __device__ __forceinline__ bool find_work(const PrefillFp8Args& a, int x, Work& 
   w.s = x % a.n_seqs;
   const int blk = a.q_blocks - 1 - x / a.n_seqs;
   w.c0 = a.cu[w.s];
-  w.m = a.cu[w.s + 1] - w.c0;
+  const int c1 = a.cu[w.s + 1];
   w.n = a.c.seq_len[w.s];
   const bool first = (threadIdx.x & 31) == 0 && blk == 0 && w.split == 0 && w.h == 0;
-  if (w.m < 0 || w.m > a.max_q) {
+  if (!rows_in_range(a, w.c0, c1)) {
     if (first) flag_error(a.err, KV_DEVERR_SEQ_RANGE);
     return false;
   }
+  w.m = c1 - w.c0;
   if (w.n < 0 || w.n > a.c.max_len) {
     if (first) flag_error(a.err, KV_DEVERR_LENGTH);
     w.n = min(max(w.n, 0), a.c.max_len);
@@ -942,8 +949,8 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(PrefillFp8Args a) {
   const long long t = item / a.Hq;
   const int s = (int)(t / a.max_q), i = (int)(t % a.max_q);
   if (s >= a.n_seqs) return;
-  const int c0 = a.cu[s], m = a.cu[s + 1] - c0;
-  if (m > a.max_q || i >= m) return;
+  const int c0 = a.cu[s], c1 = a.cu[s + 1];
+  if (!rows_in_range(a, c0, c1) || i >= c1 - c0) return;
   const float* part = static_cast<const float*>(a.c.ws) + (size_t)item * a.n_split * 132;
   const float mine = lane < a.n_split ? part[(size_t)lane * 132] : -INFINITY;
   const bool nan = __any_sync(0xffffffffu, isnan(mine));

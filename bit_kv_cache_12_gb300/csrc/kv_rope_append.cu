@@ -465,14 +465,18 @@ __global__ void __launch_bounds__(kThreads, 4) append_fp8_kernel(AppendFp8Args a
   release_successor();
   after_predecessor();
   const int s = blockIdx.x / a.tiles, i = blockIdx.x - s * a.tiles;
-  const int c0 = a.cu[s];
-  int n = a.cu[s + 1] - c0;
+  const int c0 = a.cu[s], c1 = a.cu[s + 1];
   const int start = a.start[s];
-  if (n < 0 || n > a.max_tokens) {
+  if (c0 < 0 || c1 < c0) {                     // (no difference of these is taken: it could pass 32 bits)
     if (i == 0 && threadIdx.x == 0) flag_error(a.err, KV_DEVERR_SEQ_RANGE);
-    n = min(n, a.max_tokens);
+    return;
   }
-  if (n <= 0) return;
+  int n = c1 - c0;
+  if (n > a.max_tokens) {
+    if (i == 0 && threadIdx.x == 0) flag_error(a.err, KV_DEVERR_SEQ_RANGE);
+    n = a.max_tokens;
+  }
+  if (n == 0) return;
   if (start < 0 || (long long)start + n > min((long long)a.max_pages * a.P, (long long)INT32_MAX)) {
     if (i == 0 && threadIdx.x == 0) flag_error(a.err, KV_DEVERR_SEQ_RANGE);
     return;

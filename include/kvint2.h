@@ -491,7 +491,8 @@ kv_status_t kv_rope_apply(const kv_pool_t* pool, int32_t layer, int32_t n_tokens
  *   q_out      device bf16 [T][Hq][128] contiguous: the rotated q; NULL with q;
  *              may be q itself if q_stride is Hq * 128
  *   cu_tokens  device int32 [n_seqs+1] prefix sums; rows from
- *              cu_tokens[n_seqs] on are neither read nor written
+ *              cu_tokens[n_seqs] on are neither read nor written; a sequence whose
+ *              first row or count is negative is skipped (KV_DEVERR_SEQ_RANGE)
  *   start_pos  device int32 [n_seqs]: tokens the sequence already caches
  *   max_tokens_per_seq  host bound (sizes the grid; longer sequences are
  *              flagged KV_DEVERR_SEQ_RANGE and truncated)
@@ -551,8 +552,8 @@ kv_status_t kv_decode_attention_fp8(kv_pool_t* pool, int32_t layer, int32_t B, c
  *   max_q_per_seq, max_seq_len  host bounds, each at most KV_MAX_DECODE_LEN (and
  *            max_seq_len at most the page table's span; blocks of 256 rows of all
  *            sequences and KV heads at most 2^31 - 1); a sequence with more
- *            queries (or a negative count) sets KV_DEVERR_SEQ_RANGE and gets none
- *            of its rows written
+ *            queries (or a negative count or first row) sets KV_DEVERR_SEQ_RANGE
+ *            and gets none of its rows written
  *   out, lse [T][Hq][128] bf16 and [T][Hq] fp32 (or NULL)
  *   workspace  >= kv_prefill_workspace_bytes(pool, n_seqs, max_q_per_seq,
  *            max_seq_len); one for the largest bounds serves every call up to them
@@ -702,7 +703,7 @@ kv_status_t kv_decode_attention_fp4(kv_pool_t* pool, int32_t layer, int32_t B, c
  *   workspace  16-byte aligned, >= kv_prompt_workspace_bytes(pool, n_seqs,
  *              max_q_per_seq, max_k_per_seq); one for the largest bounds serves every
  *              call up to them
- * A sequence with more queries or keys than its bound, a negative count, or rows
+ * A sequence with more queries or keys than its bound, a negative count or first row, or rows
  * outside [0, q_rows) or [0, kv_rows) sets KV_DEVERR_SEQ_RANGE and gets none of its
  * rows written.  Logits are fp32.  What hidden keys and values hold never reaches the
  * output, NaN and infinities included; a visible value that is not finite makes that
