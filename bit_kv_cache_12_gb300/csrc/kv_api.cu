@@ -171,10 +171,7 @@ kv_status_t kv_pool_create(const kv_pool_config_t* cfg, void* stream, kv_pool_t*
   if (p.sm_count <= 0) p.sm_count = 1;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const size_t L = c.num_layers, H = c.num_kv_heads;
-  pool->rope = new (std::nothrow) kvint2::RopeParams[L]();
-  pool->axes = new (std::nothrow) kvint2::RopeAxes[L]();
-  pool->range = new (std::nothrow) kvint2::Fp4Range[L]();
-  bool ok = pool->rope && pool->axes && pool->range;
+  bool ok = true;
   if (c.kind == KV_POOL_INT2_3TIER) {
     p.tile_bytes = 1024 + kvint2::kTile * 8 * (128 / c.group_size);
     p.page_bytes = H * (c.page_size / kvint2::kTile) * p.tile_bytes;
@@ -208,6 +205,12 @@ kv_status_t kv_pool_create(const kv_pool_config_t* cfg, void* stream, kv_pool_t*
   ok = ok && dev_alloc(&p.arrive, L * c.max_seqs * H * kvint2::kMaskWords * sizeof(unsigned));
   ok = ok && dev_alloc(&p.step_tickets, L * ((c.max_seqs + 127) / 128) * sizeof(unsigned));
   ok = ok && dev_alloc(&p.err, sizeof(int));
+  if (ok) {                                    // (last: of more layers than the device holds the host may not hold these)
+    pool->rope = new (std::nothrow) kvint2::RopeParams[L]();
+    pool->axes = new (std::nothrow) kvint2::RopeAxes[L]();
+    pool->range = new (std::nothrow) kvint2::Fp4Range[L]();
+    ok = pool->rope && pool->axes && pool->range;
+  }
   if (!ok) {
     free_pool(pool);
     return KV_ERR_OOM;
