@@ -121,8 +121,8 @@ struct PrefillFp8Args {
   int n_seqs, max_q, Hq, G, n_split, q_blocks;
   int* err;
   int polls;
-  int stall;                                   // test hook: CTA 0's walker (1) or its converters (2) withhold its first
-                                               // item's last pass
+  int stall;                                   // test hook: CTA 0's walker withholds its first item's last pass (1), or
+                                               // its issuer does nothing (2; asked in the converters' loop it costs 2%)
 };
 
 // ---- tcgen05 ----------------------------------------------------------------
@@ -260,7 +260,6 @@ __device__ __forceinline__ void convert_tiles(const PrefillFp8Args& a, uint8_t* 
     const uint32_t present = p.blocks;
     const int t0 = p.t0, keys = p.keys;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    if (a.stall == 2 && last && blockIdx.x == 0) return;
     if (it >= 2 && !__all_sync(0xffffffffu, wait(sh->bars + kKEmpty + stage, ph))) return;
     uint8_t* sk = sm + kOffK + stage * kOperand;
 #pragma unroll
@@ -458,7 +457,8 @@ __device__ __forceinline__ void walk(const PrefillFp8Args& a, Shared* sh, const 
 // The whole warp runs this, in step, and one lane of it issues: addresses stay in
 // uniform registers.  The loops are not unrolled: the code of the other warps
 // passes through the same instruction cache, and a short loop stays in it.
-__device__ __forceinline__ void issue_products(uint32_t tmem, uint8_t* sm, Shared* sh, const Waiter& wait) {
+__device__ __forceinline__ void issue_products(bool none, uint32_t tmem, uint8_t* sm, Shared* sh, const Waiter& wait) {
+  if (none) return;
   const uint32_t base = smem_u32(sm);
   const uint64_t q0 = desc(base + kOffQ, 16), k0 = desc(base + kOffK, 16), v0 = desc(base + kOffV, kOperand / 2);
   auto ready = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(sh->bars + bar, parity)) != 0; };
@@ -919,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp8_kernel(PrefillFp8Args
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (warp == 13) walk(a, sh, wait);
-    if (warp == 12) issue_products(__shfl_sync(0xffffffffu, tmem, 0), sm, sh, wait);
+    if (warp == 12) issue_products(a.stall == 2 && blockIdx.x == 0, __shfl_sync(0xffffffffu, tmem, 0), sm, sh, wait);
   }
   __syncwarp();
   fence_before();
