@@ -576,9 +576,13 @@ kv_status_t kv_prefill_attention_fp8(kv_pool_t* pool, int32_t layer, int32_t n_s
  * kv_rope_apply_axes, kv_prompt_attention over its own rows, kv_append_fp4.  A
  * token: kv_rope_apply_axes, kv_append_fp4, kv_decode_attention_fp4.  A chunk
  * behind cached tokens: kv_read_fp4 of those in front of the chunk's own k and v
- * rows, kv_prompt_attention.  Every call below requires the pool's device to be the
- * current one (KV_ERR_INVALID_ARG otherwise) and reads the caller's buffers from
- * device memory only.
+ * rows, kv_prompt_attention.  The rows that one call reads back lie without gaps:
+ * for the chunks of several sequences either a call for each, or the chunks are
+ * appended first, all tokens of every sequence are read, and the chunks' own rows are
+ * copied over their stored ones.  Pools of other kinds are not read back as rows;
+ * there kv_prompt_attention serves prompts without a cached prefix.  Every call below
+ * requires the pool's device to be the current one (KV_ERR_INVALID_ARG otherwise) and
+ * reads the caller's buffers from device memory only.
  *
  * Format.  A token's 128 channels of one KV head and tensor (K or V) are 8 blocks of
  * 16; a block has one e4m3 scale s and 16 e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
@@ -674,7 +678,8 @@ kv_status_t kv_read_fp4(const kv_pool_t* pool, int32_t layer, int32_t n_seqs,
                         int64_t v_out_stride, void* stream);
 
 /* One decode step over an FP4 pool.  Arguments, visible tokens, errors and limits as
- * in kv_decode_attention_fp8. */
+ * in kv_decode_attention_fp8.  A weight is rounded to fp16 for its product with v, and
+ * weights below 2^-32 of the largest count in lse only. */
 kv_status_t kv_decode_attention_fp4(kv_pool_t* pool, int32_t layer, int32_t B, const void* q,
                                     const int32_t* seq_len, const int32_t* page_table,
                                     int32_t max_pages_per_seq, int32_t max_seq_len,
@@ -692,9 +697,9 @@ kv_status_t kv_decode_attention_fp4(kv_pool_t* pool, int32_t layer, int32_t B, c
  *              the same with their Hkv heads.  16-byte aligned, strides in elements,
  *              multiples of 8 and at least a token's channels, below 2^31
  *   q_rows, kv_rows  host: rows that q, and k and v, hold (no row behind is touched)
- *   cu_q, cu_k device int32 [n_seqs+1] prefix sums, from 0; rows from cu_q[n_seqs]
- *              on are neither read nor written, rows of k and v from cu_k[n_seqs] on
- *              never reach an output
+ *   cu_q, cu_k device int32 [n_seqs+1] prefix sums, from 0; rows of out and lse from
+ *              cu_q[n_seqs] on are not written, rows of q from there on and of k and
+ *              v from cu_k[n_seqs] on never reach an output
  *   max_q_per_seq, max_k_per_seq  host bounds, each at most KV_MAX_DECODE_LEN (blocks
  *              of 256 rows of all sequences and KV heads at most 2^31 - 1)
  *   out, lse   [q_rows][Hq][128] bf16, 16-byte aligned, and [q_rows][Hq] fp32 or NULL
@@ -707,8 +712,9 @@ kv_status_t kv_decode_attention_fp4(kv_pool_t* pool, int32_t layer, int32_t B, c
  * outside [0, q_rows) or [0, kv_rows) sets KV_DEVERR_SEQ_RANGE and gets none of its
  * rows written.  Logits are fp32.  What hidden keys and values hold never reaches the
  * output, NaN and infinities included; a visible value that is not finite makes that
- * output channel not finite.  n_seqs at most the pool's max_seqs.  Calls may overlap if their
- * workspaces and outputs differ. */
+ * output channel not finite.  A weight is rounded to bf16 (2^-8 of it at most) for its
+ * product with v, not in the sum of weights.  n_seqs at most the pool's max_seqs.  Calls
+ * may overlap if their workspaces and outputs differ. */
 size_t kv_prompt_workspace_bytes(const kv_pool_t* pool, int32_t n_seqs, int32_t max_q_per_seq,
                                  int32_t max_k_per_seq);
 kv_status_t kv_prompt_attention(kv_pool_t* pool, int32_t n_seqs, const void* q, int64_t q_stride,
