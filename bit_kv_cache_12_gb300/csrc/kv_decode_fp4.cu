@@ -19,12 +19,14 @@
 // largest is between 2^7 and 2^15, and weights below 2^-32 of the largest are dropped.
 //
 // Bound: the cache's bytes (144 per token and KV head) for batches, latency for one short
-// sequence, between them the instructions that turn codes into operands (issue slots 62% in
+// sequence, between them the instructions that turn codes into operands (issue slots 66% in
 // use, tensor pipe 31%).  A warp takes two tiles at a step, copied whole (TMA, 4608 bytes)
 // two steps ahead, so that one tile's conversions run beside the other's products: with one
 // tile 64 sequences of 20,480 tokens took 317 us, with two 255.  Measured: 1024 tokens of 2
 // KV heads 4.8 us (5.5 with the host's part), 16,384 tokens of 8 9.7, 100,000 26.5 (115 MB,
-// 4.4 TB/s), 64 ragged sequences of 8k to 32k 298 us (1745 MB, 5.9 TB/s, 0.87 of a plain copy).
+// 4.4 TB/s), 64 ragged sequences of 8k to 32k 298 us (1745 MB, 5.9 TB/s, 0.87 of a plain copy);
+// under a window of 4096 with 64 first tokens 1 x 131,072 tokens of 8 KV heads 7.1, 16 of them
+// 21.2 (77 MB, 3.6 TB/s).
 #include <algorithm>
 
 #include "kv_decode_split.cuh"

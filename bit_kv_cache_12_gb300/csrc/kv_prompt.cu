@@ -30,15 +30,19 @@
 // joins by their log-sum-exp.
 //
 // Bound: the tensor cores.  A pass of both tiles over 128 keys is 2,048 clocks of products
-// and takes some 2,700 (1.43 us), an item 7 us beyond its passes, a call 8.5 us before its
-// first pass.  8192 tokens of 32 + 8 heads 361 us (1.52 PFLOP/s, 0.78 of a large library
-// product's rate), 4 chunks of 518 to 2000 tokens under a window of 4096 490 us (1.31), 512
-// tokens 13.9.  What lies between: the issuer's way from one group of products to the next
-// (four products in the queue cover 256 of its 290 to 420 clocks), and an item's rows, read
-// from tensor memory (2,700 clocks a tile), before its successor's first products.  A softmax
-// of half the work took 1.36 us a pass, the products with V alone left out 1.07; an issuer for
-// each tile made 8192 tokens take 463 us (both tiles' products interleave, and then both
-// softmaxes wait), weights handed on in halves 5% more than 376, items overlapped in full 385.
+// and takes some 2,700 (1.43 us), an item 7 us beyond its passes.  A call of 512 tokens (four
+// passes) spends 4,600 clocks up to its first scores (1,900 of them to find its item, 1,700 to
+// have q and K), 2,000 to 3,000 in each softmax, and 10,700 behind the last one: 2,900 in the last
+// products, 6,300 in writing two tiles' rows.  One token takes 13,800 in all.  8192 tokens of 32
+// + 8 heads 363 us where the clock holds (two dozen calls; 1.51 PFLOP/s, 0.77 of a large library
+// product's rate), 394 in a long stream, 4 chunks of 518 to 2000 tokens under a window of 4096
+// 490 (1.31) and 520, 512 tokens 14.1.  What lies between: the issuer's way from one group of
+// products to the next (four products in the queue cover 256 of its 290 to 420 clocks), and an
+// item's rows, read from tensor memory (2,700 clocks a tile), before its successor's first
+// products.  A softmax of half the work took 1.36 us a pass, the products with V alone left
+// out 1.07; an issuer for each tile made 8192 tokens take 463 us (both tiles' products
+// interleave, and then both softmaxes wait), weights handed on in halves 5% more than 376,
+// items overlapped in full 385.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
